@@ -30,6 +30,9 @@
  *   - Device-side conditions (a key length outside [1, Lk], a pipeline wait
  *     that exceeded its time limit) set a per-device error word that
  *     mha_check() reads.  The affected rows are written as zeros.
+ *   - Paged key/value caches are described by an mha_kv_pages (below);
+ *     its pools follow the same alignment rule, its page table and lengths
+ *     are 4-byte aligned device int32 arrays.
  *   - Masks: mask_kind is a bit set of MHA_MASK_CAUSAL (key j blocked for
  *     query i when j > i; requires Lq == Lk) and MHA_MASK_KEY_PADDING (key j
  *     blocked for batch item b when j >= key_lengths[b]).  There are no
@@ -62,7 +65,8 @@ enum {
     MHA_MASK_NONE = 0,
     MHA_MASK_CAUSAL = 1,
     MHA_MASK_KEY_PADDING = 2,
-    /* sdpa_decode only: query i of Lq sees keys j <= len_b - Lq + i */
+    /* sdpa_decode and sdpa_paged only: query i of the newest Lq sees keys
+     * j <= len_b - Lq + i */
     MHA_MASK_CAUSAL_BOTTOM_RIGHT = 4
 };
 
@@ -273,6 +277,218 @@ mha_status embed_pe_forward(const int32_t *ids, const void *table, int vocab,
                             const float *pe, int pe_rows, void *x, int B,
                             int L, int d_model, int pos_offset, float scale,
                             mha_dtype dtype, mha_stream stream);
+
+/*
+ * A paged key/value cache: the rows of a sequence's keys and values lie in
+ * pages of page_size rows that need not be neighbours, so that no sequence
+ * reserves rows it does not hold and sequences can share pages (the
+ * PagedAttention remark of "How Transformers Work" (worksonmygpu.com), "What
+ * changed since 2017").  One page table serves `layers` pools.
+ *   K, V : pools.  Row s of page p, kv head g, layer y starts at element
+ *          y*layer_stride + p*page_stride + (g*page_size + s)*d.
+ *   page_stride  : 0 selects the dense kv_heads*page_size*d.
+ *   layer_stride : 0 selects num_pages*page_stride.  Both are multiples of
+ *          16 bytes and at least one page.
+ *   page_table : device int32 [B, table_cols]; token j of sequence b lies in
+ *          row j % page_size of page page_table[b][j / page_size].  Entries
+ *          behind a sequence's last held page are never read.
+ *   kv_lengths : device int32 [B], tokens held by each sequence.
+ * page_size is a power of two from 16 to 256; table_cols*page_size <= 2^30.
+ */
+typedef struct {
+    void *K, *V;
+    mha_dtype dtype;
+    int num_pages, page_size, kv_heads, d, layers;
+    int64_t page_stride, layer_stride;
+    int32_t *page_table;
+    int32_t *kv_lengths;
+    int B, table_cols;
+} mha_kv_pages;
+
+/*
+ * sdpa_paged -- attention of each sequence's newest tokens over its paged
+ * cache: one token each while decoding, a few, or a long chunk of a prompt,
+ * mixed in one call.  Query heads may share key/value heads.
+ *   Q : bf16, T packed tokens; head h of token t at t*q_token_stride + h*d
+ *       (0 selects the dense H*d).  q_token_stride is a multiple of 8.
+ *   q_offsets : device int32 [B+1]; sequence b's queries are the tokens
+ *       [q_offsets[b], q_offsets[b+1]), the newest n_b of the kv_lengths[b]
+ *       tokens its pages hold (their own keys and values among them).  A
+ *       sequence without queries is passed over.
+ *   O : [T, H, d] (the concatenated heads), out_dtype BF16 or F32.  Rows of
+ *       tokens that belong to no sequence are left as they were.
+ *   H : a multiple of kv_heads; head h reads kv head h / (H / kv_heads), and
+ *       H / kv_heads <= 128.
+ *   max_new : the largest n_b, 1 <= max_new.
+ *   scale : as for sdpa_forward (0 selects 1/sqrt(d)).
+ *   mask_kind : MHA_MASK_CAUSAL_BOTTOM_RIGHT (query i of n_b sees the tokens
+ *       j <= kv_lengths[b] - n_b + i) or MHA_MASK_NONE (it sees all).
+ *   num_splits : CTAs that share one block's keys, 1..16, merged exactly
+ *       through one thread-block cluster; 0 picks a default.
+ * The cache is pages->dtype BF16 with d in {64, 128}; `layer` picks the pool.
+ * Rows of a page that lie behind the sequence's length may hold anything;
+ * the rows a sequence holds must be finite.
+ * Checked on the device (MHA_ERR_DEVICE from mha_check): kv_lengths[b] in
+ * [max(1, n_b), table_cols*page_size] (from 1 without the causal bit) and
+ * page numbers in [0, num_pages) -- every row that would read through the bad
+ * entry is written as zeros, and other rows of that sequence may be;
+ * q_offsets ascending in [0, T] and n_b <= max_new -- nothing is written for
+ * such a sequence.
+ * T or B may be 0.  The call allocates nothing and needs no workspace.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status sdpa_paged(const void *Q, int64_t q_token_stride,
+                      const mha_kv_pages *pages, int layer,
+                      const int32_t *q_offsets, void *O, int T, int H,
+                      int max_new, float scale, int mask_kind,
+                      mha_dtype out_dtype, int num_splits, mha_stream stream);
+
+/* How the rotation pairs a head's first rope_dim columns. */
+enum {
+    MHA_ROPE_INTERLEAVED = 0, /* (2i, 2i+1) */
+    MHA_ROPE_HALF = 1         /* (i, i + rope_dim/2) */
+};
+
+/*
+ * qk_norm_rope_forward -- the norm of every query and key head and the
+ * rotation by its position, in one pass:
+ *   z = x * rsqrt(mean(x^2) + eps) * gamma          over the d columns
+ *   (y_a, y_b) = (z_a cos - z_b sin, z_b cos + z_a sin)
+ * for the rope_dim/2 column pairs (a, b) of `pairing`; columns from rope_dim
+ * on are z.  The rotation turns relative position into the dot product: the
+ * shift-by-k property of the sinusoidal encoding ("How Transformers Work"
+ * (worksonmygpu.com), "Positional encoding").
+ *   Q : [B, L, H, d] with token stride q_token_stride (elements, 0 = H*d;
+ *       e.g. a slice of one projection's output); K : likewise, Hkv heads.
+ *   gamma_q, gamma_k : [d], of dtype.
+ *   pe : fp32 [pe_rows, rope_dim] in sinusoidal_pe's layout: row p holds
+ *        sin, cos of pair i at columns 2i, 2i+1 (sinusoidal_pe builds it
+ *        for base 10000; any table of that layout will do).  8-byte aligned.
+ *   positions : device int32 [B, L], each in [0, pe_rows) (checked on the
+ *        device: MHA_ERR_DEVICE, the token's rows written as zeros), or NULL:
+ *        token l is at pos_offset + l, and pos_offset + L <= pe_rows.
+ *   Qo [B, H, L, d], Ko [B, Hkv, L, d] : of dtype, as sdpa_forward takes them.
+ *   eps : finite, > 0.
+ * dtype BF16 or F32; the arithmetic is fp32, rounded once.  2 <= d <= 256,
+ * rope_dim even in [2, d].  H or Hkv may be 0 (that part is skipped).
+ * With d in {64, 128} and rope_dim a multiple of 16, Q, K (and their
+ * strides) are read as 16-byte vectors; every pointer is 16-byte aligned and
+ * token strides are multiples of 16 bytes there.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status qk_norm_rope_forward(const void *Q, int64_t q_token_stride,
+                                const void *K, int64_t k_token_stride,
+                                const void *gamma_q, const void *gamma_k,
+                                const float *pe, int pe_rows, int rope_dim,
+                                int pairing, void *Qo, void *Ko, int B, int L,
+                                int H, int Hkv, int d, int pos_offset,
+                                const int32_t *positions, float eps,
+                                mha_dtype dtype, mha_stream stream);
+
+/*
+ * qk_norm_rope_backward -- its gradient.  With dz the rotation of dQo by the
+ * opposite angle, xh = x * rstd and u = dz * gamma:
+ *   dQ = rstd * (u - xh * mean(u * xh)),   dgamma = sum over rows of dz * xh
+ *   dQo [B, H, L, d] of dq_dtype, dKo [B, Hkv, L, d] of dk_dtype (BF16 or
+ *       F32: sdpa_backward gives dQ in fp32).
+ *   dQ, dK : of dtype, laid out as Q and K with token strides of their own.
+ *   dgamma_q, dgamma_k : fp32 [d], overwritten; 16-byte aligned.
+ *   workspace : device, 16-byte aligned, at least
+ *       qk_norm_rope_backward_workspace_bytes(d) bytes.
+ * The sums run in a fixed order: equal calls give equal bits.  A token with a
+ * bad position gets zero rows and adds nothing to dgamma.
+ * Other arguments, support and errors as for qk_norm_rope_forward.
+ */
+mha_status qk_norm_rope_backward(const void *Q, int64_t q_token_stride,
+                                 const void *K, int64_t k_token_stride,
+                                 const void *gamma_q, const void *gamma_k,
+                                 const float *pe, int pe_rows, int rope_dim,
+                                 int pairing, const void *dQo, const void *dKo,
+                                 void *dQ, int64_t dq_token_stride, void *dK,
+                                 int64_t dk_token_stride, float *dgamma_q,
+                                 float *dgamma_k, int B, int L, int H, int Hkv,
+                                 int d, int pos_offset,
+                                 const int32_t *positions, float eps,
+                                 mha_dtype dtype, mha_dtype dq_dtype,
+                                 mha_dtype dk_dtype, void *workspace,
+                                 size_t workspace_bytes, mha_stream stream);
+
+/* Workspace qk_norm_rope_backward needs, in bytes (0 for a bad d). */
+size_t qk_norm_rope_backward_workspace_bytes(int d);
+
+/*
+ * qk_norm_rope_paged -- the serving form: norm and rotation of T packed new
+ * tokens, whose keys and values go straight into their pages.
+ *   Q [T, H, d], K and V [T, kv_heads, d] : bf16, token strides as above.
+ *   q_offsets, pages, layer : as for sdpa_paged, kv_lengths already counting
+ *       the new tokens; token i of sequence b's n_b is at position
+ *       kv_lengths[b] - n_b + i, which picks its row of pe and its page row.
+ *   Qo : [T, H, d], ready for sdpa_paged.
+ * Pages that receive rows must not be shared between sequences.  d is 64 or
+ * 128, rope_dim a multiple of 16.
+ * Checked on the device (MHA_ERR_DEVICE): kv_lengths[b] in [n_b,
+ * table_cols*page_size], positions below pe_rows, page numbers -- such a
+ * token's Qo rows are written as zeros and no page is touched for it.
+ * Tokens that belong to no sequence are passed over.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status qk_norm_rope_paged(const void *Q, int64_t q_token_stride,
+                              const void *K, int64_t k_token_stride,
+                              const void *V, int64_t v_token_stride,
+                              const void *gamma_q, const void *gamma_k,
+                              const float *pe, int pe_rows, int rope_dim,
+                              int pairing, void *Qo, const mha_kv_pages *pages,
+                              int layer, const int32_t *q_offsets, int T,
+                              int H, float eps, mha_stream stream);
+
+/*
+ * kv_pages_fork -- n sequences continue n others (parallel samples, beams):
+ * sequence children[i] takes parents[i]'s length and full pages (shared), and
+ * the rows of its last, partly filled page are copied into page fresh[i], in
+ * every layer.
+ *   parents, children, fresh : device int32 [n].  fresh[i] must be held by no
+ *       sequence; it is not read where the parent's last page is full.
+ *       One parent may have many children.
+ * The child's table entries behind its last page, and the rows of the fresh
+ * page behind its length, are left as they were.
+ * Checked on the device (MHA_ERR_DEVICE, that pair changes nothing): indexes
+ * outside [0, B), a child that is also a parent of this call or named twice,
+ * a needed fresh page outside [0, num_pages) or named twice, the parent's
+ * length outside [0, table_cols*page_size], its last page's number.
+ * Any dtype; d * element size must be a multiple of 16 bytes.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status kv_pages_fork(const mha_kv_pages *pages, const int32_t *parents,
+                         const int32_t *children, const int32_t *fresh, int n,
+                         mha_stream stream);
+
+/*
+ * kv_pages_compact -- the pages that some sequence holds, in increasing page
+ * number, become pages 0 .. n_live-1 of other pools (of another size, or as
+ * large), and the page tables are renumbered.  A shared page is moved once
+ * and stays shared.  Ending a sequence is setting its length to 0: its pages
+ * are then free unless another sequence holds them.
+ *   src : the cache.  dst : the pools and page table to fill; its dtype,
+ *       page_size, kv_heads, d, layers and B are src's, table_cols at least
+ *       src's; num_pages and strides are its own, kv_lengths is not used.
+ *       It must share no memory with src.
+ *   n_live : device int32, the number of pages held.
+ *   workspace : device, 16-byte aligned, at least
+ *       kv_pages_compact_workspace_bytes(src->num_pages) bytes.
+ * Entries of dst's table behind a sequence's last page, and pages from n_live
+ * on, are left as they were.
+ * Checked on the device (MHA_ERR_DEVICE): a length outside [0,
+ * table_cols*page_size] (the sequence counts as empty), a page number outside
+ * [0, num_pages) or a page without room in dst (its entry becomes -1).
+ * src->num_pages <= 2^20.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status kv_pages_compact(const mha_kv_pages *src, const mha_kv_pages *dst,
+                            int32_t *n_live, void *workspace,
+                            size_t workspace_bytes, mha_stream stream);
+
+/* Workspace kv_pages_compact needs, in bytes (0 for a bad num_pages). */
+size_t kv_pages_compact_workspace_bytes(int num_pages);
 
 /*
  * mha_create -- allocate a multi-head attention layer handle.

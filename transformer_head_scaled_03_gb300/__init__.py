@@ -13,6 +13,8 @@ _BINDING_NAMES = {
     "sdpa_forward", "sdpa_forward_host", "sdpa_decode", "decode_splits", "sinusoidal_pe",
     "sdpa_forward_lse", "sdpa_backward",
     "embed_pe",
+    "sdpa_paged", "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_paged", "kv_pages_fork",
+    "kv_pages_compact", "KvPages", "ROPE_INTERLEAVED", "ROPE_HALF",
     "MASK_CAUSAL_BOTTOM_RIGHT", "mha_create", "mha_forward", "mha_check",
     "mha_destroy", "MhaHandle", "MhaError", "EncoderLayer", "EncoderParams",
     "ENCODER_PARAM_NAMES", "set_wait_limit_ms", "selftest_wait_timeout", "status_string", "lib",

@@ -31,6 +31,9 @@ MASK_CAUSAL = 1
 MASK_KEY_PADDING = 2
 MASK_CAUSAL_BOTTOM_RIGHT = 4
 
+ROPE_INTERLEAVED = 0
+ROPE_HALF = 1
+
 LIB_PATH = _build.LIB
 
 _lock = threading.Lock()
@@ -44,6 +47,16 @@ ENCODER_PARAM_NAMES = ("Wq", "Wk", "Wv", "Wo", "bq", "bk", "bv", "bo", "ln1_gamm
 class EncoderParams(ctypes.Structure):
     """mha_encoder_params of include/mha.h (device pointers)."""
     _fields_ = [(n, ctypes.c_void_p) for n in ENCODER_PARAM_NAMES]
+
+
+class KvPages(ctypes.Structure):
+    """mha_kv_pages of include/mha.h."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("d", ctypes.c_int), ("layers", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("kv_lengths", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("table_cols", ctypes.c_int)]
 
 
 class MhaError(RuntimeError):
@@ -80,6 +93,27 @@ def _declare(lib):
     lib.sdpa_decode_splits.argtypes = [i32, i32, i32, i32]
     lib.sdpa_decode_splits.restype = i32
     i64 = ctypes.c_int64
+    kvp = ctypes.POINTER(KvPages)
+    lib.sdpa_paged.argtypes = [vp, i64, kvp, i32, vp, vp, i32, i32, i32, f32, i32, i32, i32, vp]
+    lib.sdpa_paged.restype = i32
+    lib.qk_norm_rope_forward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, i32,
+                                         i32, i32, i32, i32, i32, vp, f32, i32, vp]
+    lib.qk_norm_rope_forward.restype = i32
+    lib.qk_norm_rope_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp,
+                                          i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp,
+                                          f32, i32, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.qk_norm_rope_backward.restype = i32
+    lib.qk_norm_rope_backward_workspace_bytes.argtypes = [i32]
+    lib.qk_norm_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.qk_norm_rope_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, vp,
+                                       kvp, i32, vp, i32, i32, f32, vp]
+    lib.qk_norm_rope_paged.restype = i32
+    lib.kv_pages_fork.argtypes = [kvp, vp, vp, vp, i32, vp]
+    lib.kv_pages_fork.restype = i32
+    lib.kv_pages_compact_workspace_bytes.argtypes = [i32]
+    lib.kv_pages_compact_workspace_bytes.restype = ctypes.c_size_t
+    lib.kv_pages_compact.argtypes = [kvp, kvp, vp, vp, ctypes.c_size_t, vp]
+    lib.kv_pages_compact.restype = i32
     lib.sdpa_forward_float_mask.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32,
                                             vp, vp, i64, i64, i32, i32, vp]
     lib.sdpa_forward_float_mask.restype = i32
@@ -312,6 +346,250 @@ def embed_pe(ids, table, pe, pos_offset: int = 0, scale: float | None = None, ou
                                 _dtype_code(table.dtype), _stream(stream))
     _check(st, "embed_pe_forward")
     return out
+
+
+def _int32(name, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: every tensor must be there."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensor must be on a CUDA device")
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device (cuda:{here})")
+
+
+def _new(stream, shape, dtype, device):
+    """A tensor that `stream` (the current one when None) may use; the caching
+    allocator keeps its memory until that stream is past it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and stream != torch.cuda.current_stream():
+        # what freed this memory ran on the current stream, so the kernels
+        # start behind that
+        stream.wait_stream(torch.cuda.current_stream())
+        t.record_stream(stream)
+    return t
+
+
+def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
+    """The mha_kv_pages of pools [P, Hkv, page, d] or [layers, P, Hkv, page, d]
+    (pages and layers at any stride, a page itself contiguous)."""
+    shape, strides = K_pages.shape, K_pages.stride()
+    if len(shape) not in (4, 5) or V_pages.shape != shape or V_pages.dtype != K_pages.dtype:
+        raise ValueError("K_pages and V_pages must be alike, [P, Hkv, page, d] or "
+                         "[layers, P, Hkv, page, d]")
+    P, Hkv, ps, d = shape[-4:]
+    if strides[-3:] != (ps * d, d, 1) or V_pages.stride() != strides:
+        raise ValueError("a page must be contiguous, and K_pages and V_pages laid out alike")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages per sequence]")
+    B, cols = page_table.shape
+    _int32("page_table", page_table, (B, cols))
+    _int32("kv_lengths", kv_lengths, (B,))
+    layers = shape[0] if len(shape) == 5 else 1
+    return KvPages(K_pages.data_ptr(), V_pages.data_ptr(), _dtype_code(K_pages.dtype), P, ps, Hkv,
+                   d, layers, strides[-4], strides[0] if layers > 1 else 0,
+                   page_table.data_ptr(), kv_lengths.data_ptr(), B, cols)
+
+
+def _packed(name, x, heads, d, dtype):
+    """Token stride of packed rows [T, heads, d] (a slice of a wider tensor's
+    last dimension will do)."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or x.dtype != dtype:
+        raise ValueError(f"{name} must be [T, {heads}, {d}] {dtype}")
+    T, (st, sh, sc) = x.shape[0], x.stride()
+    if sc != 1 or (heads > 1 and sh != d):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    return st if T > 1 else heads * d
+
+
+def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: int | None = None,
+               causal: bool = True, scale: float | None = None,
+               out_dtype: torch.dtype | None = None, layer: int = 0, num_splits: int = 0, out=None,
+               stream=None):
+    """O [T, H, d] = attention of packed new tokens Q [T, H, d] (sequence b's
+    are q_offsets[b]..q_offsets[b+1], the newest of its kv_lengths[b] tokens)
+    over a paged cache K_pages, V_pages [P, Hkv, page, d] (or with a leading
+    layer dimension); bottom-right causal unless ``causal`` is False.
+    ``max_new`` bounds the new tokens of one sequence (default: T)."""
+    pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    if Q.dim() != 3 or K_pages.dtype != Q.dtype:
+        raise ValueError("Q must be [T, H, d] of the cache's dtype")
+    T, H, d = Q.shape
+    q_ts = _packed("Q", Q, H, pages.d, Q.dtype)
+    _int32("q_offsets", q_offsets, (pages.B + 1,))
+    odt = out_dtype or Q.dtype
+    _on_current_device(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, out)
+    if out is None:
+        out = _new(stream, (T, H, d), odt, Q.device)
+    elif out.shape != (T, H, d) or out.dtype != odt or not out.is_contiguous():
+        raise ValueError("out has the wrong shape, dtype or layout")
+    st = lib().sdpa_paged(Q.data_ptr(), q_ts, pages, int(layer), q_offsets.data_ptr(),
+                          out.data_ptr(), T, H, max(1, T) if max_new is None else int(max_new),
+                          float(scale or 0.0), MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE,
+                          _dtype_code(odt), int(num_splits), _stream(stream))
+    _check(st, "sdpa_paged")
+    return out
+
+
+def _token_rows(name, x, B, L, d, dtype):
+    """Heads and token stride of rows [B, L, heads, d] whose tokens are evenly
+    spaced (a dense tensor, or a slice of a projection's output)."""
+    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != L or x.shape[3] != d or x.dtype != dtype:
+        raise ValueError(f"{name} must be [{B}, {L}, heads, {d}] {dtype}")
+    heads, (sb, sl, sh, sc) = x.shape[2], x.stride()
+    ts = sl if L > 1 else sb if B > 1 else heads * d
+    if x.numel() and (sc != 1 and d > 1 or heads > 1 and sh != d or B > 1 and L > 1 and sb != L * ts):
+        raise ValueError(f"{name}'s tokens must be evenly spaced and its heads contiguous")
+    return heads, ts
+
+
+def _rope_args(Q, K, gamma_q, gamma_k, pe, positions):
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q and K must be [B, L, heads, d]")
+    B, L, _, d = Q.shape
+    H, q_ts = _token_rows("Q", Q, B, L, d, Q.dtype)
+    Hkv, k_ts = _token_rows("K", K, B, L, d, Q.dtype)
+    _gammas(gamma_q, gamma_k, pe, d, Q.dtype)
+    if positions is not None:
+        _int32("positions", positions, (B, L))
+    return B, L, H, Hkv, d, q_ts, k_ts
+
+
+def _gammas(gamma_q, gamma_k, pe, d, dtype):
+    for g in (gamma_q, gamma_k):
+        if tuple(g.shape) != (d,) or g.dtype != dtype or not g.is_contiguous():
+            raise ValueError("gamma_q and gamma_k must be contiguous [d] of the rows' dtype")
+    if pe.dtype != torch.float32 or pe.dim() != 2 or not pe.is_contiguous():
+        raise ValueError("pe must be contiguous float32 [rows, rope_dim]")
+
+
+def qk_norm_rope(Q, K, gamma_q, gamma_k, pe, pos_offset: int = 0, positions=None,
+                 pairing: int = ROPE_INTERLEAVED, eps: float = 1e-6, out=None, stream=None):
+    """(Q' [B, H, L, d], K' [B, Hkv, L, d]): every head of Q [B, L, H, d] and
+    K [B, L, Hkv, d] divided by its root mean square, times gamma [d], its
+    first pe.shape[1] columns rotated by the token's position (a row of pe, a
+    ``sinusoidal_pe`` table): ``positions`` int32 [B, L], or pos_offset + l."""
+    B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
+    given = out if out is not None else (None, None)
+    _on_current_device(Q, K, gamma_q, gamma_k, pe, positions, *given)
+    want = ((B, H, L, d), (B, Hkv, L, d))
+    if out is None:
+        out = tuple(_new(stream, s, Q.dtype, Q.device) for s in want)
+    for o, s in zip(out, want):
+        if tuple(o.shape) != s or o.dtype != Q.dtype or not o.is_contiguous():
+            raise ValueError("out has the wrong shapes, dtype or layout")
+    st = lib().qk_norm_rope_forward(
+        Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
+        pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), out[0].data_ptr(),
+        out[1].data_ptr(), B, L, H, Hkv, d, int(pos_offset),
+        None if positions is None else positions.data_ptr(), float(eps), _dtype_code(Q.dtype),
+        _stream(stream))
+    _check(st, "qk_norm_rope_forward")
+    return out
+
+
+def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int = 0,
+                          positions=None, pairing: int = ROPE_INTERLEAVED, eps: float = 1e-6,
+                          out=None, workspace=None, stream=None):
+    """(dQ [B, L, H, d], dK [B, L, Hkv, d], dgamma_q, dgamma_k fp32 [d]) of
+    qk_norm_rope for upstream dQo [B, H, L, d], dKo [B, Hkv, L, d] (bf16 or
+    fp32 each, as ``sdpa_backward`` returns them).  ``out``: (dQ, dK) to fill,
+    laid out as Q and K may be."""
+    B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
+    if tuple(dQo.shape) != (B, H, L, d) or tuple(dKo.shape) != (B, Hkv, L, d) \
+            or not dQo.is_contiguous() or not dKo.is_contiguous():
+        raise ValueError("dQo and dKo must be contiguous [B, heads, L, d]")
+    given = out if out is not None else (None, None)
+    _on_current_device(Q, K, gamma_q, gamma_k, pe, dQo, dKo, positions, workspace, *given)
+    if out is None:
+        out = (_new(stream, (B, L, H, d), Q.dtype, Q.device),
+               _new(stream, (B, L, Hkv, d), Q.dtype, Q.device))
+    (h0, dq_ts), (h1, dk_ts) = (_token_rows("out", o, B, L, d, Q.dtype) for o in out)
+    if h0 != H or h1 != Hkv:
+        raise ValueError("out has the wrong shapes")
+    dg = _new(stream, (2, d + -d % 4), torch.float32, Q.device)
+    dgamma_q, dgamma_k = dg[0, :d], dg[1, :d]
+    if workspace is None:
+        need = int(lib().qk_norm_rope_backward_workspace_bytes(d))
+        workspace = _new(stream, max(16, need), torch.uint8, Q.device)
+    st = lib().qk_norm_rope_backward(
+        Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
+        pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), dQo.data_ptr(), dKo.data_ptr(),
+        out[0].data_ptr(), dq_ts, out[1].data_ptr(), dk_ts, dgamma_q.data_ptr(),
+        dgamma_k.data_ptr(), B, L, H, Hkv, d, int(pos_offset),
+        None if positions is None else positions.data_ptr(), float(eps), _dtype_code(Q.dtype),
+        _dtype_code(dQo.dtype), _dtype_code(dKo.dtype), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "qk_norm_rope_backward")
+    return out[0], out[1], dgamma_q, dgamma_k
+
+
+def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
+                       q_offsets, pairing: int = ROPE_INTERLEAVED, eps: float = 1e-6,
+                       layer: int = 0, out=None, stream=None):
+    """Q' [T, H, d] for ``sdpa_paged``; the normed, rotated keys and the values
+    of the T packed new tokens go into their pages (``kv_lengths`` already
+    counts them)."""
+    pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    if Q.dim() != 3:
+        raise ValueError("Q must be [T, H, d]")
+    T, H, d = Q.shape
+    dt = K_pages.dtype
+    q_ts = _packed("Q", Q, H, pages.d, dt)
+    k_ts = _packed("K", K, pages.kv_heads, d, dt)
+    v_ts = _packed("V", V, pages.kv_heads, d, dt)
+    if K.shape[0] != T or V.shape[0] != T:
+        raise ValueError("Q, K and V must hold the same tokens")
+    _gammas(gamma_q, gamma_k, pe, d, dt)
+    _int32("q_offsets", q_offsets, (pages.B + 1,))
+    _on_current_device(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
+                       q_offsets, out)
+    if out is None:
+        out = _new(stream, (T, H, d), dt, Q.device)
+    elif out.shape != (T, H, d) or out.dtype != dt or not out.is_contiguous():
+        raise ValueError("out has the wrong shape, dtype or layout")
+    st = lib().qk_norm_rope_paged(
+        Q.data_ptr(), q_ts, K.data_ptr(), k_ts, V.data_ptr(), v_ts, gamma_q.data_ptr(),
+        gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), out.data_ptr(),
+        pages, int(layer), q_offsets.data_ptr(), T, H, float(eps), _stream(stream))
+    _check(st, "qk_norm_rope_paged")
+    return out
+
+
+def kv_pages_fork(K_pages, V_pages, page_table, kv_lengths, parents, children, fresh, stream=None):
+    """Sequences children[i] continue parents[i]: full pages shared, the last
+    partly filled one copied into page fresh[i] (every layer); page_table and
+    kv_lengths are updated in place."""
+    pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    n = parents.numel()
+    for name, t in (("parents", parents), ("children", children), ("fresh", fresh)):
+        _int32(name, t, (n,))
+    _on_current_device(K_pages, V_pages, page_table, kv_lengths, parents, children, fresh)
+    _check(lib().kv_pages_fork(pages, parents.data_ptr(), children.data_ptr(), fresh.data_ptr(), n,
+                               _stream(stream)), "kv_pages_fork")
+
+
+def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
+                     workspace=None, stream=None):
+    """The pages that some sequence holds become pages 0..n-1 of K_out, V_out,
+    in order; table_out is the renumbered page table.  Returns n (int32 [1])."""
+    src = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    dst = _kv_pages(K_out, V_out, table_out, kv_lengths)
+    _on_current_device(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out, workspace)
+    count = _new(stream, (1,), torch.int32, K_pages.device)
+    if workspace is None:
+        need = int(lib().kv_pages_compact_workspace_bytes(src.num_pages))
+        workspace = _new(stream, max(16, need), torch.uint8, K_pages.device)
+    _check(lib().kv_pages_compact(src, dst, count.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)),
+           "kv_pages_compact")
+    return count
 
 
 class MhaHandle:

@@ -95,6 +95,9 @@ cudaError_t launch_gemm_ln_bf16(const GemmLnArgs& g, const DeviceCtl& ctl);
 // holds the others).
 constexpr unsigned kErrTokenId = 4u;     // a token id outside [0, vocab)
 constexpr unsigned kErrSmemLayout = 8u;  // dynamic shared memory too misaligned for the layout
+// Device error bits of the paged cache and the rotation.
+constexpr unsigned kErrPages = 16u;     // a page number, length, offset or sequence index
+constexpr unsigned kErrPosition = 32u;  // a position outside the rotation table
 
 cudaError_t launch_sinusoidal_pe(float* pe, int first_pos, int n_pos, int D, cudaStream_t s);
 cudaError_t launch_embed_pe(const int32_t* ids, const void* table, int vocab, const float* pe,
@@ -133,6 +136,9 @@ bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t ran
 }  // namespace mha
 
 namespace mha {
+
+// The checks of an mha_kv_pages, for every entry point that takes one.
+mha_status validate_pages(const mha_kv_pages* p);
 
 // The current device's error word and wait limit (false if CUDA fails).
 bool device_ctl(DeviceCtl* ctl);
