@@ -287,8 +287,8 @@ mha_status embed_pe_forward(const int32_t *ids, const void *table, int vocab,
  *   K, V : pools.  Row s of page p, kv head g, layer y starts at element
  *          y*layer_stride + p*page_stride + (g*page_size + s)*d.
  *   page_stride  : 0 selects the dense kv_heads*page_size*d.
- *   layer_stride : 0 selects num_pages*page_stride.  Both are multiples of
- *          16 bytes and at least one page.
+ *   layer_stride : 0 selects num_pages*page_stride.  Both are multiples of d
+ *          and at least one page.
  *   page_table : device int32 [B, table_cols]; token j of sequence b lies in
  *          row j % page_size of page page_table[b][j / page_size].  Entries
  *          behind a sequence's last held page are never read.
@@ -310,7 +310,7 @@ typedef struct {
  * cache: one token each while decoding, a few, or a long chunk of a prompt,
  * mixed in one call.  Query heads may share key/value heads.
  *   Q : bf16, T packed tokens; head h of token t at t*q_token_stride + h*d
- *       (0 selects the dense H*d).  q_token_stride is a multiple of 8.
+ *       (0 selects the dense H*d).  q_token_stride is a multiple of d.
  *   q_offsets : device int32 [B+1]; sequence b's queries are the tokens
  *       [q_offsets[b], q_offsets[b+1]), the newest n_b of the kv_lengths[b]
  *       tokens its pages hold (their own keys and values among them).  A

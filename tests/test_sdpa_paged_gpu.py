@@ -70,6 +70,11 @@ CASES = [
     ([3, 256], [5, 1], 4, 2, 16, 128, False, 0, F32),           # more queries than keys
     ([260], [3], 128, 1, 64, 64, True, 0, BF),                  # 128 heads to one
     ([500, 30], [9, 4], 33, 1, 16, 64, True, 0, F32),           # an odd group
+    # enough blocks for two query tiles per CTA, the last ones with one or none
+    ([400, 0, 333], [350, 0, 300], 64, 8, 64, 128, True, 0, BF),
+    ([411, 333], [340, 301], 64, 8, 16, 64, True, 0, F32),
+    ([270, 333], [340, 300], 48, 8, 128, 64, False, 0, BF),
+    ([500], [481], 56, 8, 256, 128, True, 0, F32),
 ]
 
 
@@ -95,12 +100,13 @@ def test_every_split_count_merges_to_one_softmax(new):
         check(run(*x, num_splits=splits, out_dtype=F32, max_new=new), O, A, F32, f"{splits} splits")
 
 
-@pytest.mark.parametrize("new", [1, 30])
-def test_what_lies_behind_the_length_is_never_used(new):
+@pytest.mark.parametrize("new,H,Hkv,d", [(1, 4, 2, 64), (1, 4, 2, 128), (30, 4, 2, 64),
+                                         (30, 2, 2, 128), (64, 128, 8, 64), (64, 128, 8, 128)])
+def test_what_lies_behind_the_length_is_never_used(new, H, Hkv, d):
     """NaN and infinities in the rows behind the last one, in spare pages and
     behind table entries: the same bits as with zeros there."""
-    for ps, lens in ((16, [37, 65]), (64, [70, 129]), (256, [200, 300])):
-        Q, K, V, table, lens, offs = case(130, lens, [new, new], 4, 2, ps, 64, cols=9)
+    for ps, lens in ((16, [137, 65]), (64, [70, 129]), (256, [200, 300])):
+        Q, K, V, table, lens, offs = case(130, lens, [new, new], H, Hkv, ps, d, cols=9)
         outs = []
         for fill in (0.0, np.nan, np.inf):
             k, v = K.copy(), V.copy()

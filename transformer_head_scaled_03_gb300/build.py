@@ -22,7 +22,8 @@ SOURCES = ["mha_api.cu", "sdpa_bf16.cu", "gemm_bf16.cu", "gemm_ln_bf16.cu", "fp3
            "mha_noalloc.cu",
            "layernorm.cu", "encoder_api.cu", "sdpa_decode.cu",
            "embed_pe.cu", "sdpa_backward.cu", "host_pipeline.cu",
-           "sdpa_paged.cu", "qk_norm_rope.cu", "kv_pages.cu"]
+           "sdpa_paged.cu", "sdpa_paged_few.cu", "sdpa_paged_rows.cu",
+           "qk_norm_rope.cu", "kv_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -35,7 +35,7 @@ mha_status validate_pages(const mha_kv_pages* p) {
   const int64_t page = static_cast<int64_t>(p->kv_heads) * p->page_size * p->d;
   if (page > (int64_t{1} << 31)) return MHA_ERR_UNSUPPORTED;
   for (int64_t s : {p->page_stride, p->layer_stride})
-    if (s < 0 || (s > 0 && s < page) || (s * es) % 16) return MHA_ERR_INVALID_ARG;
+    if (s < 0 || (s > 0 && s < page) || s % p->d) return MHA_ERR_INVALID_ARG;
   return MHA_OK;
 }
 

@@ -1,0 +1,166 @@
+// sdpa_paged.cuh -- what the two forms of the paged attention share: their
+// arguments, a sequence's extent, and the loading of key/value tiles page by
+// page.
+#pragma once
+
+#include "internal.h"
+#include "kv_pages.cuh"
+#include "ptx_cluster.cuh"
+
+namespace mha {
+
+struct PagedSdpaArgs {
+  const void* Q;
+  int64_t q_stride;  // elements from token to token
+  PagesView pages;
+  const int32_t* q_offsets;
+  void* O;  // [T, H, d]
+  int T, H, G, max_new;
+  bool causal, out_f32;
+  float scale;
+  int splits;  // 0: choose
+  cudaStream_t stream;
+};
+
+constexpr int kPagedMaxSplits = 16;
+constexpr int kPagedFewRows = 16;  // query slots of the few-rows form
+
+cudaError_t launch_sdpa_paged_few(const PagedSdpaArgs& a, const DeviceCtl& ctl);
+cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl);
+
+// Kernel arguments.
+struct PagedParams {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* q_offsets;
+  void* O;
+  int B, cols, num_pages, page_shift, kv_heads;
+  int T, H, G, max_new, causal, out_f32, splits;
+  float scale_log2;  // scale * log2(e)
+  unsigned* err;
+  uint64_t limit_ns;
+};
+
+inline PagedParams paged_params(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
+  return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.B, a.pages.cols,
+                     a.pages.num_pages, a.pages.page_shift, a.pages.kv_heads, a.T, a.H, a.G,
+                     a.max_new, a.causal, a.out_f32, a.splits,
+                     static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634),
+                     ctl.err, ctl.limit_ns};
+}
+
+// The tensor maps of Q [T, H, d], of `tokens` tokens and one group of heads
+// per box, and of one layer's pools [P, Hkv * page, d], boxes of `rows` rows
+// that stay inside a page.
+inline bool paged_tensor_maps(const PagedSdpaArgs& a, int d, int tokens, int tile_rows,
+                              CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+  const uint64_t u2 = 2;
+  const uint64_t qd[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(a.H),
+                          static_cast<uint64_t>(a.T)};
+  const uint64_t qs[2] = {d * u2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(tokens)};
+  const int page = 1 << a.pages.page_shift;
+  const uint64_t pd[3] = {static_cast<uint64_t>(d),
+                          static_cast<uint64_t>(a.pages.kv_heads) << a.pages.page_shift,
+                          static_cast<uint64_t>(a.pages.num_pages)};
+  const uint64_t pst[2] = {d * u2, static_cast<uint64_t>(a.pages.page_stride) * 2};
+  const uint32_t pb[3] = {64, static_cast<uint32_t>(page < tile_rows ? page : tile_rows), 1};
+  return encode_tensor_map(q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.Q), qd, qs,
+                           qb, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_tensor_map(k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.pages.K, pd, pst, pb,
+                           CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_tensor_map(v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.pages.V, pd, pst, pb,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Sequence b's new tokens [q0, q0 + n) and length; bad: its length, its
+// offsets (then n = 0).
+struct PagedSeq {
+  int q0, n, len;
+  bool bad_len, bad_offsets;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  PagedSeq s{};
+  const int q0 = __ldg(p.q_offsets + b), q1 = __ldg(p.q_offsets + b + 1);
+  s.len = __ldg(p.kv_len + b);
+  s.bad_offsets = q0 < 0 || q1 < q0 || q1 > p.T || q1 - q0 > p.max_new;
+  s.q0 = q0;
+  s.n = s.bad_offsets ? 0 : q1 - q0;
+  const int64_t cap = static_cast<int64_t>(p.cols) << p.page_shift;
+  s.bad_len = s.n > 0 && (s.len < 1 || s.len > cap || (p.causal && s.len < s.n));
+  return s;
+}
+
+// The page boxes of one tile of ROWS keys, one per lane of the producer warp:
+// lane = page of the tile * KB + 64-column block.
+template <int ROWS, int KB>
+struct PageBoxes {
+  int page;      // this lane's page number (any value where !mine)
+  bool mine;     // this lane loads a box
+  bool bad;      // ... but its page number is out of range
+
+  // Read the page number of the tile that starts at key `key0`.
+  __device__ __forceinline__ void fetch(const PagedParams& p, int b, int key0, int len, int lane) {
+    const int slot = lane / KB;
+    const int in_tile = ROWS >> p.page_shift;  // 0: the tile is part of a page
+    const int entry = (key0 >> p.page_shift) + slot;
+    mine = slot < (in_tile > 0 ? in_tile : 1) &&
+           (static_cast<int64_t>(entry) << p.page_shift) < len;
+    page = 0;
+    if (mine) page = __ldg(p.table + static_cast<int64_t>(b) * p.cols + entry);
+    bad = mine && (page < 0 || page >= p.num_pages);
+    if (bad) mine = false;
+  }
+  // Bytes that the warp's boxes bring (warp-collective).
+  __device__ __forceinline__ uint32_t bytes(const PagedParams& p) const {
+    const uint32_t rows = min(ROWS, 1 << p.page_shift);
+    return __popc(__ballot_sync(0xffffffffu, mine)) * rows * 128u;
+  }
+  // Load this lane's box of head g into the tile at `dst` ([KB][ROWS][128 B]).
+  __device__ __forceinline__ void load(const PagedParams& p, const CUtensorMap* map, uint32_t dst,
+                                       uint32_t bar, int key0, int g, int lane) const {
+    if (!mine) return;
+    const int slot = lane / KB, kb = lane % KB;
+    const int row = (key0 & ((1 << p.page_shift) - 1)) + (g << p.page_shift);
+    tma_load_3d(dst + kb * (ROWS * 128) + (slot << p.page_shift) * 128, map, bar, kb * 64, row,
+                page);
+  }
+};
+
+// Store four consecutive outputs (fp32 or bf16) at element `at`.
+__device__ __forceinline__ void store_out4(const PagedParams& p, int64_t at, float4 o) {
+  if (p.out_f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = o;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
+  return v;
+}
+
+// Bounded wait that ignores the abort flag (copies and products in flight).
+__device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) return;
+  }
+}
+
+// Clusters of `splits` CTAs of a kernel with this block size and shared
+// memory that the device holds at once (0 when the query fails).
+int paged_max_active_clusters(int threads, int smem_bytes, int splits);
+
+// The largest split count whose `clusters` clusters are all resident at once
+// and that leaves no split without a key tile.
+int paged_default_splits(int64_t clusters, int key_tiles, int threads, int smem_bytes);
+
+}  // namespace mha

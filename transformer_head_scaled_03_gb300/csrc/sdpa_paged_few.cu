@@ -1,0 +1,559 @@
+// sdpa_paged_few.cu -- paged attention of few query rows: at most 16 rows
+// (new tokens x query heads per key/value head) per sequence and key/value
+// head, the decoding of one or a few tokens.
+//
+// One CTA = one split of one (sequence, kv head): tiles of 128 keys, each
+// gathered from its pages by TMA boxes of a page's rows, one lane of the
+// producer warp per box.
+//   S^T = K_tile Q^T      tcgen05, M = 128 keys, N = 16 query slots, K = d
+//   softmax over keys     warps 0-3, one key (TMEM lane) per thread
+//   O^T = V_tile^T P^T    tcgen05, M = d, N = 16, K = 128 keys
+//   merge (cluster)       o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
+// Keys are the M side because 16 query rows would fill an eighth of it.  The
+// query heads that share a key/value head are query slots of one CTA, so
+// every page is read once.  The rows of the last page behind the sequence's
+// length hold anything, NaN too: their scores are replaced and their V rows
+// zeroed in shared memory before the product, where 0 * NaN would reach the
+// sums.
+//
+// At 16 slots a byte of the cache meets at most 16 flops: bound by HBM, so
+// the pipeline is sized for bytes in flight (three stages of 64 KB per SM).
+#include <math.h>
+#include <stdint.h>
+
+#include <cuda_bf16.h>
+
+#include "sdpa_paged.cuh"
+
+namespace mha {
+namespace {
+
+constexpr int kKeys = 128;      // keys per tile: MMA M of S^T, MMA K of O^T
+constexpr int kSlots = kPagedFewRows;  // MMA N of both products
+constexpr int kSub = 16384;     // one 128-row x 64-column bf16 block
+constexpr int kQBox = 2048;     // 16 rows x 64 columns
+constexpr int kPBuf = 4096;     // P^T of one tile: 16 rows x 128 keys bf16
+constexpr int kThreads = 192;   // warps 0-3 softmax, 4 TMA, 5 MMA
+constexpr int kTmaWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr uint32_t kTmemCols = 64;  // S^T x 2 (cols 0-31), O^T x 2 (cols 32-63)
+constexpr int kMaxSortedBatch = 256;
+
+template <int D>
+struct FewCfg {
+  static_assert(D == 64 || D == 128, "head dim");
+  static constexpr int KB = D / 64;
+  // d = 128: three 64 KB stages, one CTA per SM; d = 64: three 32 KB stages,
+  // two CTAs per SM
+  static constexpr int NST = 3;
+  static constexpr int kCtasPerSm = D == 128 ? 1 : 2;
+  static constexpr int kTile = KB * kSub;
+  // V before K: the M = 128 operand of a d = 64 product reads the 16 KB after
+  // a V tile as its unused upper half
+  static constexpr int kOffV = 0;
+  static constexpr int kOffK = kOffV + NST * kTile;
+  static constexpr int kOffQ = kOffK + NST * kTile;
+  static constexpr int kOffP = kOffQ + KB * kQBox;
+  static constexpr int kOffRed = kOffP + 2 * kPBuf;  // [3][4 warps][16] f32
+  // the merge's m[16], l[16], o[16][D] and the weights [16 splits][16]: in
+  // the P^T buffers where they fit, which are free by then
+  static constexpr int kXBytes = (2 * kSlots + kSlots * D + kPagedMaxSplits * kSlots) * 4;
+  static constexpr bool kXInP = kXBytes <= 2 * kPBuf;
+  static constexpr int kOffX = kXInP ? kOffP : kOffRed + 3 * 4 * kSlots * 4;
+  static constexpr int kOffBar = kXInP ? kOffRed + 3 * 4 * kSlots * 4 : kOffX + kXBytes;
+  static constexpr int bQ = 0;
+  __host__ __device__ static constexpr int bKF(int s) { return 1 + s; }
+  __host__ __device__ static constexpr int bKE(int s) { return 1 + NST + s; }
+  __host__ __device__ static constexpr int bVF(int s) { return 1 + 2 * NST + s; }
+  __host__ __device__ static constexpr int bVE(int s) { return 1 + 3 * NST + s; }
+  __host__ __device__ static constexpr int bS(int i) { return 1 + 4 * NST + i; }
+  __host__ __device__ static constexpr int bP(int i) { return 3 + 4 * NST + i; }
+  __host__ __device__ static constexpr int bO(int i) { return 5 + 4 * NST + i; }
+  __host__ __device__ static constexpr int bRed(int i) { return 7 + 4 * NST + i; }
+  static constexpr int bDrain = 9 + 4 * NST;
+  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
+  static_assert(kOffP % 1024 == 0, "P^T swizzle atoms must be 1024-byte aligned");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kCtasPerSm == 1 || kSmemBytes + 1024 <= 114 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ void softmax_bar() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
+    sdpa_paged_few_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using C = FewCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc + 4);
+  volatile int* bad_page = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 8);
+  auto bar = [base](int i) -> uint32_t { return base + C::kOffBar + 8u * i; };
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const WaitCtl ctl{abort_flag, p.err, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::bQ), 1);
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(bar(C::bKF(s)), 1);
+      mbar_init(bar(C::bKE(s)), 1);
+      mbar_init(bar(C::bVF(s)), 1);
+      mbar_init(bar(C::bVE(s)), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::bS(i)), 1);
+      mbar_init(bar(C::bP(i)), 128);
+      mbar_init(bar(C::bO(i)), 1);
+      mbar_init(bar(C::bRed(i)), 128);
+    }
+    mbar_init(bar(C::bDrain), 1);
+    *abort_flag = 0;
+    *bad_page = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc<kTmemCols>(smem_u32(tmem_slot));
+    tmem_relinquish();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  float* red = reinterpret_cast<float*>(gbase + C::kOffRed);
+  float* xm = reinterpret_cast<float*>(gbase + C::kOffX);
+  float* xl = xm + kSlots;
+  float* xo = xl + kSlots;
+  float* xw = xo + kSlots * D;
+
+  // ---- this CTA's (sequence, kv head) and key tiles; the cluster spans the
+  // splits.  CTAs start roughly in grid order, so sequences are taken
+  // longest-first (up to kMaxSortedBatch of them), ranked by every CTA from
+  // its own copy of the lengths: long ones do not trail alone at the end.
+  const int split = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.splits));
+  const int slot = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.splits));
+  const int g = slot % p.kv_heads;
+  int b = slot / p.kv_heads;
+  if (p.B > 1 && p.B <= kMaxSortedBatch) {
+    int* lens_s = reinterpret_cast<int*>(xo);  // free until the merge
+    int* pick = reinterpret_cast<int*>(xm);
+    for (int i = threadIdx.x; i < p.B; i += kThreads) lens_s[i] = __ldg(p.kv_len + i);
+    __syncthreads();
+    const int want = b;
+    for (int c = threadIdx.x; c < p.B; c += kThreads) {
+      const int lc = lens_s[c];
+      int rank = 0;
+      for (int o = 0; o < p.B; ++o) {
+        const int lo = lens_s[o];
+        rank += (lo > lc || (lo == lc && o < c)) ? 1 : 0;
+      }
+      if (rank == want) *pick = c;
+    }
+    __syncthreads();
+    b = *pick;
+    __syncthreads();  // xm is written again only after the main loop
+  }
+  const PagedSeq seq = paged_seq(p, b);
+  const int rows = seq.n * p.G;  // query slots in use: slot = token * G + head of the group
+  const int len = seq.len;
+  const int n_tiles = seq.bad_len || rows == 0 ? 0 : (len + kKeys - 1) / kKeys;
+  const int t_begin = static_cast<int>(static_cast<long long>(n_tiles) * split / p.splits);
+  const int t_end = static_cast<int>(static_cast<long long>(n_tiles) * (split + 1) / p.splits);
+  const int T = t_end - t_begin;
+  if ((seq.bad_len || seq.bad_offsets) && split == 0 && threadIdx.x == 0)
+    atomicOr(p.err, kErrPages);
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ producer
+    if (T > 0) {
+      if (lane == 0) {
+        const int tokens = kSlots / p.G;
+        mbar_expect_tx(bar(C::bQ), C::KB * 128 * p.G * tokens);
+        for (int kb = 0; kb < C::KB; ++kb)
+          tma_load_3d(base + C::kOffQ + kb * kQBox, &tmQ, bar(C::bQ), kb * 64, g * p.G, seq.q0);
+      }
+      PageBoxes<kKeys, C::KB> cur, nxt;
+      cur.fetch(p, b, t_begin * kKeys, len, lane);
+      int k_issued = 0, v_issued = 0;
+      for (int j = 0; j < T; ++j) {
+        const int st = j % C::NST;
+        const uint32_t ph = (j / C::NST) & 1;
+        const int key0 = (t_begin + j) * kKeys;
+        // the next tile's page numbers arrive while this one waits for room
+        if (j + 1 < T) nxt.fetch(p, b, key0 + kKeys, len, lane);
+        if (cur.bad) {
+          *bad_page = 1;
+          atomicOr(p.err, kErrPages);
+        }
+        const uint32_t bytes = cur.bytes(p);
+        if (!mbar_wait_warp(bar(C::bKE(st)), ph ^ 1u, ctl)) break;
+        if (lane == 0) mbar_expect_tx(bar(C::bKF(st)), bytes);
+        __syncwarp();
+        cur.load(p, &tmK, base + C::kOffK + st * C::kTile, bar(C::bKF(st)), key0, g, lane);
+        k_issued = j + 1;
+        if (!mbar_wait_warp(bar(C::bVE(st)), ph ^ 1u, ctl)) break;
+        if (lane == 0) mbar_expect_tx(bar(C::bVF(st)), bytes);
+        __syncwarp();
+        cur.load(p, &tmV, base + C::kOffV + st * C::kTile, bar(C::bVF(st)), key0, g, lane);
+        v_issued = j + 1;
+        cur = nxt;
+      }
+      // let every issued copy land before the CTA can exit
+      if (lane == 0) {
+        paged_wait_drain(bar(C::bQ), 0, p.limit_ns);
+        for (int j = max(0, k_issued - C::NST); j < k_issued; ++j)
+          paged_wait_drain(bar(C::bKF(j % C::NST)), (j / C::NST) & 1, p.limit_ns);
+        for (int j = max(0, v_issued - C::NST); j < v_issued; ++j)
+          paged_wait_drain(bar(C::bVF(j % C::NST)), (j / C::NST) & 1, p.limit_ns);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    // Order: S(0), S(1), then per tile j: O(j) once P(j) is published, and
+    // S(j+2) into the S buffer that P(j)'s publication has just released.
+    if (lane == 0 && T > 0) {
+      constexpr uint32_t kIdS = idesc_bf16_f32(kKeys, kSlots, false, false);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, kSlots, true, false);
+      const uint64_t q_desc = sdesc_sw128(base + C::kOffQ, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(base + C::kOffK, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + C::kOffV, kSub, 1024);
+      const uint64_t p_desc = sdesc_sw128(base + C::kOffP, 16, 1024);
+      auto issue_s = [&](int st, int buf) {
+        const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::kTile) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t koff = static_cast<uint64_t>(((ks >> 2) * kSub + (ks & 3) * 32) >> 4);
+          const uint64_t qoff = static_cast<uint64_t>(((ks >> 2) * kQBox + (ks & 3) * 32) >> 4);
+          umma_ss(tmem + buf * kSlots, kd + koff, q_desc + qoff, kIdS, ks > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_o = [&](int st, int buf) {
+        const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::kTile) >> 4);
+        const uint64_t pd = p_desc + static_cast<uint64_t>((buf * kPBuf) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks) {
+          const uint64_t voff = static_cast<uint64_t>((ks * 16 * 128) >> 4);
+          const uint64_t poff = static_cast<uint64_t>(((ks >> 2) * 2048 + (ks & 3) * 32) >> 4);
+          umma_ss(tmem + 2 * kSlots + buf * kSlots, vd + voff, pd + poff, kIdO,
+                  ks > 0 ? 1u : 0u);
+        }
+      };
+      bool ok = mbar_wait(bar(C::bQ), 0, ctl);
+      for (int j = 0; ok && j < 2 && j < T; ++j) {
+        const int st = j % C::NST;
+        if (!(ok = mbar_wait(bar(C::bKF(st)), (j / C::NST) & 1, ctl))) break;
+        tc_fence_after();
+        issue_s(st, j);
+        umma_commit(bar(C::bS(j)));
+        umma_commit(bar(C::bKE(st)));
+      }
+      for (int j = 0; ok && j < T; ++j) {
+        const int st = j % C::NST;
+        const int buf = j & 1;
+        if (!(ok = mbar_wait(bar(C::bP(buf)), (j >> 1) & 1, ctl))) break;
+        if (!(ok = mbar_wait(bar(C::bVF(st)), (j / C::NST) & 1, ctl))) break;
+        tc_fence_after();
+        issue_o(st, buf);
+        umma_commit(bar(C::bO(buf)));
+        umma_commit(bar(C::bVE(st)));
+        if (j + 2 < T) {
+          const int st2 = (j + 2) % C::NST;
+          if (!(ok = mbar_wait(bar(C::bKF(st2)), ((j + 2) / C::NST) & 1, ctl))) break;
+          tc_fence_after();
+          issue_s(st2, buf);
+          umma_commit(bar(C::bS(buf)));
+          umma_commit(bar(C::bKE(st2)));
+        }
+      }
+      // every issued MMA completes before tensor memory is released
+      umma_commit(bar(C::bDrain));
+      paged_wait_drain(bar(C::bDrain), 0, p.limit_ns);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    // Thread r owns key r of every S^T tile and row r (output column r) of
+    // every O^T tile.
+    const int r = warp * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tS = tmem + lane_bits;
+    const uint32_t tO = tmem + lane_bits + 2 * kSlots;
+    const bool o_rows = warp * 32 < D;  // warp-uniform
+    const float sl2 = p.scale_log2;
+    // the last key each slot sees; -1 for a slot not in use
+    int last[kSlots];
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+      last[q] = q >= rows ? -1 : p.causal ? len - seq.n + q / p.G : len - 1;
+    float m[kSlots], l[kSlots], acc[kSlots], alpha_prev[kSlots];
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      m[q] = -INFINITY;
+      l[q] = 0.f;
+      acc[q] = 0.f;
+      alpha_prev[q] = 1.f;
+    }
+    // P^T store address of key r: 64-key atom, 16-byte chunk, 2-byte slot
+    const int kk = r & 63;
+    uint8_t* p_key = gbase + C::kOffP + (r >> 6) * 2048 + (kk & 7) * 2;
+    const int chunk = kk >> 3;
+    bool ok = true;
+    for (int j = 0; j < T; ++j) {
+      const int buf = j & 1;
+      const uint32_t par = (j >> 1) & 1;
+      const int key = (t_begin + j) * kKeys + r;
+      if (!(ok = mbar_wait_warp(bar(C::bS(buf)), par, ctl))) break;
+      tc_fence_after();
+      uint32_t sr[kSlots];
+      tmem_ld16_sync(tS + buf * kSlots, sr);
+      float s[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        s[q] = key <= last[q] ? __uint_as_float(sr[q]) * sl2 : -INFINITY;
+      float* rb = red + buf * 4 * kSlots;
+      {
+        float wm[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) wm[q] = warp_max_f32(s[q]);
+        if (lane == 0) {
+          float4* dst = reinterpret_cast<float4*>(rb + warp * kSlots);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_float4(wm[4 * i], wm[4 * i + 1], wm[4 * i + 2], wm[4 * i + 3]);
+        }
+      }
+      mbar_arrive(bar(C::bRed(buf)));
+      if (!(ok = mbar_wait_warp(bar(C::bRed(buf)), par, ctl))) break;
+      float alpha[kSlots];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 a0 = reinterpret_cast<const float4*>(rb)[i];
+        const float4 a1 = reinterpret_cast<const float4*>(rb + kSlots)[i];
+        const float4 a2 = reinterpret_cast<const float4*>(rb + 2 * kSlots)[i];
+        const float4 a3 = reinterpret_cast<const float4*>(rb + 3 * kSlots)[i];
+        const float t4[4] = {fmaxf(fmax3(a0.x, a1.x, a2.x), a3.x),
+                             fmaxf(fmax3(a0.y, a1.y, a2.y), a3.y),
+                             fmaxf(fmax3(a0.z, a1.z, a2.z), a3.z),
+                             fmaxf(fmax3(a0.w, a1.w, a2.w), a3.w)};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = 4 * i + u;
+          const float mn = fmaxf(m[q], t4[u]);
+          const float at = mn == -INFINITY ? 0.f : mn;  // a slot with no visible key yet
+          alpha[q] = ex2_approx(m[q] - at);
+          const float pq = ex2_approx(s[q] - at);
+          l[q] = fmaf(l[q], alpha[q], pq);
+          m[q] = mn;
+          s[q] = pq;
+        }
+      }
+      // P^T(j) in bf16 (half a step, 2^-8 of a weight, which the output's own
+      // rounding matches): row q, key r, 128-byte swizzle
+      uint8_t* pb = p_key + buf * kPBuf;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        *reinterpret_cast<__nv_bfloat16*>(pb + (q >> 3) * 1024 + (q & 7) * 128 +
+                                          ((chunk ^ (q & 7)) << 4)) = __float2bfloat16_rn(s[q]);
+      if ((t_begin + j + 1) * kKeys > len) {
+        // V rows behind the length: zero them once the tile has landed (it
+        // stays until this tile's product, which waits for the arrive below)
+        const int st = j % C::NST;
+        if (!(ok = mbar_wait_warp(bar(C::bVF(st)), (j / C::NST) & 1, ctl))) break;
+        if (key >= len) {
+          uint8_t* v_row = gbase + C::kOffV + st * C::kTile + r * 128;
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(v_row + kb * kSub + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar(C::bP(buf)));
+      if (j > 0) {
+        const int pj = j - 1;
+        if (!(ok = mbar_wait_warp(bar(C::bO(pj & 1)), (pj >> 1) & 1, ctl))) break;
+        tc_fence_after();
+        if (o_rows) {
+          uint32_t orr[kSlots];
+          tmem_ld16_sync(tO + (pj & 1) * kSlots, orr);
+#pragma unroll
+          for (int q = 0; q < kSlots; ++q)
+            acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(orr[q]));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) alpha_prev[q] = alpha[q];
+    }
+    if (ok && T > 0) {
+      const int pj = T - 1;
+      if ((ok = mbar_wait_warp(bar(C::bO(pj & 1)), (pj >> 1) & 1, ctl))) {
+        tc_fence_after();
+        if (o_rows) {
+          uint32_t orr[kSlots];
+          tmem_ld16_sync(tO + (pj & 1) * kSlots, orr);
+#pragma unroll
+          for (int q = 0; q < kSlots; ++q)
+            acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(orr[q]));
+        }
+      }
+    }
+    tc_fence_before();
+    // denominator: sum l over the 128 key lanes
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+#pragma unroll
+      for (int sh = 16; sh > 0; sh >>= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], sh);
+    }
+    float* lsum = red + 2 * 4 * kSlots;
+    if (lane == 0) {
+      float4* dst = reinterpret_cast<float4*>(lsum + warp * kSlots);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dst[i] = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+    }
+    softmax_bar();
+    const bool failed = *abort_flag != 0;
+    if (failed) *bad_page = 1;  // a failed split spoils the rows
+    if (threadIdx.x < kSlots) {
+      const int q = threadIdx.x;
+      xm[q] = failed ? -INFINITY : m[q];
+      xl[q] = failed ? 0.f
+                     : lsum[q] + lsum[kSlots + q] + lsum[2 * kSlots + q] + lsum[3 * kSlots + q];
+    }
+    if (o_rows && r < D) {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) xo[q * D + r] = acc[q];
+    }
+  }
+
+  // ---- merge the splits through distributed shared memory.  First each
+  // split's weight per slot, 2^(m_s - M) / sum, from one round of remote
+  // loads; then the outputs, four columns a thread, each another round.
+  __syncwarp();
+  cluster_sync();  // every split's m, l, O and bad-page flag are in its shared memory
+  if (warp < 4) {
+    const int S = p.splits;
+    const uint32_t xm_s = smem_u32(xm), xl_s = smem_u32(xl), xo_s = smem_u32(xo);
+    const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
+    if (threadIdx.x < kSlots) {
+      const int q = threadIdx.x;
+      float ms[kPagedMaxSplits], ls[kPagedMaxSplits], M = -INFINITY, den = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int s = 0; s < kPagedMaxSplits; ++s) {
+        if (s >= S) break;
+        const uint32_t rk = static_cast<uint32_t>(s);
+        ms[s] = ld_cluster_f32(cluster_map(xm_s + 4u * q, rk));
+        ls[s] = ld_cluster_f32(cluster_map(xl_s + 4u * q, rk));
+        bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_s, rk))) != 0u;
+      }
+#pragma unroll
+      for (int s = 0; s < kPagedMaxSplits; ++s)
+        if (s < S) M = fmaxf(M, ms[s]);
+      const bool none = bad || M == -INFINITY;
+#pragma unroll
+      for (int s = 0; s < kPagedMaxSplits; ++s)
+        if (s < S) {
+          ms[s] = none ? 0.f : ex2_approx(ms[s] - M);
+          den = fmaf(ms[s], ls[s], den);
+        }
+#pragma unroll
+      for (int s = 0; s < kPagedMaxSplits; ++s)
+        if (s < S) xw[s * kSlots + q] = none ? 0.f : ms[s] / den;
+    }
+    softmax_bar();
+    const int total = rows * (D / 4);
+    const int per = (total + S - 1) / S;
+    const int e0 = split * per;
+    const int e1 = min(total, e0 + per);
+    for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += 128) {
+      const int q = e / (D / 4);
+      const int c = (e - q * (D / 4)) * 4;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = 0; s < S; ++s) {
+        const float w = xw[s * kSlots + q];
+        const float4 v = ld_cluster_f32x4(
+            cluster_map(xo_s + 4u * (q * D + c), static_cast<uint32_t>(s)));
+        // a weight of 0 stands for nothing seen, and for rows to be zeroed,
+        // whose partial output may be anything
+        if (w != 0.f) {
+          o.x = fmaf(w, v.x, o.x);
+          o.y = fmaf(w, v.y, o.y);
+          o.z = fmaf(w, v.z, o.z);
+          o.w = fmaf(w, v.w, o.w);
+        }
+      }
+      const int i = q / p.G;
+      const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
+      store_out4(p, row * D + c, o);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another still reads its shared memory
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<kTmemCols>(tmem);
+  }
+}
+
+template <int D>
+cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
+  using C = FewCfg<D>;
+  CUtensorMap q, k, v;
+  if (!paged_tensor_maps(a, D, kSlots / a.G, kKeys, &q, &k, &v)) return cudaErrorInvalidValue;
+  const int64_t clusters = static_cast<int64_t>(a.pages.B) * a.pages.kv_heads;
+  if (a.splits == 0)
+    a.splits = paged_default_splits(
+        clusters, static_cast<int>(((static_cast<int64_t>(a.pages.cols) << a.pages.page_shift) +
+                                    kKeys - 1) / kKeys),
+        kThreads, C::kSmemBytes);
+  if (clusters * a.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  auto kern = sdpa_paged_few_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && a.splits > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * a.splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, q, k, v, paged_params(a, ctl));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sdpa_paged_few(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
+  return a.pages.d == 64 ? launch_impl<64>(a, ctl) : launch_impl<128>(a, ctl);
+}
+
+}  // namespace mha
