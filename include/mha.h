@@ -363,7 +363,7 @@ enum {
  *   gamma_q, gamma_k : [d], of dtype.
  *   pe : fp32 [pe_rows, rope_dim] in sinusoidal_pe's layout: row p holds
  *        sin, cos of pair i at columns 2i, 2i+1 (sinusoidal_pe builds it
- *        for base 10000; any table of that layout will do).  8-byte aligned.
+ *        for base 10000; any table of that layout will do).  16-byte aligned.
  *   positions : device int32 [B, L], each in [0, pe_rows) (checked on the
  *        device: MHA_ERR_DEVICE, the token's rows written as zeros), or NULL:
  *        token l is at pos_offset + l, and pos_offset + L <= pe_rows.

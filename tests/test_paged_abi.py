@@ -101,7 +101,7 @@ def rope(lib, Q=P, qts=0, K=P, kts=0, gq=P, gk=P, pe=P, rows=9, r=64, pairing=0,
 
 @pytest.mark.parametrize("kw,code", [
     (dict(Q=None), INVALID), (dict(K=MIS), INVALID), (dict(gq=None), INVALID),
-    (dict(gk=0x10004), INVALID), (dict(pe=None), INVALID), (dict(pe=0x10004), INVALID),
+    (dict(gk=0x10004), INVALID), (dict(pe=None), INVALID), (dict(pe=0x10008), INVALID),
     (dict(Qo=None), INVALID), (dict(Qo=P), INVALID), (dict(Ko=MIS), INVALID), (dict(B=-1), INVALID),
     (dict(L=10), INVALID), (dict(off=6), INVALID), (dict(off=-1), INVALID), (dict(r=0), INVALID),
     (dict(r=63), INVALID), (dict(r=66), INVALID), (dict(d=0), INVALID), (dict(d=300, r=64), UNSUPPORTED),

@@ -27,5 +27,6 @@ _BINDING_NAMES = {
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)   # later look-ups find it at once
+        return value
     raise AttributeError(name)

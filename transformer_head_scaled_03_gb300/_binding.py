@@ -348,20 +348,25 @@ def embed_pe(ids, table, pe, pos_offset: int = 0, scale: float | None = None, ou
     return out
 
 
-def _int32(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _int32(name, t, *shape):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor must be there."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensor must be on a CUDA device")
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors must be on the current device (cuda:{here})")
+def _launch_on(stream, *tensors):
+    """Check that every tensor is on the current device, where the library
+    launches; the raw stream to launch on.  (The paged calls take tens of
+    microseconds or less, so what the host does for each of them counts.)"""
+    if not all([t.is_cuda for t in tensors]):
+        raise ValueError("tensor must be on a CUDA device")
+    here = torch._C._cuda_getDevice()
+    if any([t.get_device() != here for t in tensors]):
+        raise ValueError(f"tensors must be on the current device (cuda:{here})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    if stream.device_index != here:
+        raise ValueError(f"stream must be on the current device (cuda:{here})")
+    return stream.cuda_stream
 
 
 def _new(stream, shape, dtype, device):
@@ -389,8 +394,8 @@ def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
     B, cols = page_table.shape
-    _int32("page_table", page_table, (B, cols))
-    _int32("kv_lengths", kv_lengths, (B,))
+    _int32("page_table", page_table, B, cols)
+    _int32("kv_lengths", kv_lengths, B)
     layers = shape[0] if len(shape) == 5 else 1
     return KvPages(K_pages.data_ptr(), V_pages.data_ptr(), _dtype_code(K_pages.dtype), P, ps, Hkv,
                    d, layers, strides[-4], strides[0] if layers > 1 else 0,
@@ -400,12 +405,13 @@ def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
 def _packed(name, x, heads, d, dtype):
     """Token stride of packed rows [T, heads, d] (a slice of a wider tensor's
     last dimension will do)."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or x.dtype != dtype:
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or x.dtype != dtype:
         raise ValueError(f"{name} must be [T, {heads}, {d}] {dtype}")
-    T, (st, sh, sc) = x.shape[0], x.stride()
+    st, sh, sc = x.stride()
     if sc != 1 or (heads > 1 and sh != d):
         raise ValueError(f"{name}'s heads must be contiguous")
-    return st if T > 1 else heads * d
+    return st if shape[0] > 1 else heads * d
 
 
 def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: int | None = None,
@@ -422,17 +428,18 @@ def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: 
         raise ValueError("Q must be [T, H, d] of the cache's dtype")
     T, H, d = Q.shape
     q_ts = _packed("Q", Q, H, pages.d, Q.dtype)
-    _int32("q_offsets", q_offsets, (pages.B + 1,))
+    _int32("q_offsets", q_offsets, pages.B + 1)
     odt = out_dtype or Q.dtype
-    _on_current_device(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, out)
+    on = _launch_on(stream, Q, K_pages, V_pages, page_table, kv_lengths, q_offsets,
+                    Q if out is None else out)
     if out is None:
         out = _new(stream, (T, H, d), odt, Q.device)
     elif out.shape != (T, H, d) or out.dtype != odt or not out.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
-    st = lib().sdpa_paged(Q.data_ptr(), q_ts, pages, int(layer), q_offsets.data_ptr(),
+    st = (_lib or lib()).sdpa_paged(Q.data_ptr(), q_ts, pages, int(layer), q_offsets.data_ptr(),
                           out.data_ptr(), T, H, max(1, T) if max_new is None else int(max_new),
                           float(scale or 0.0), MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE,
-                          _dtype_code(odt), int(num_splits), _stream(stream))
+                          _dtype_code(odt), int(num_splits), on)
     _check(st, "sdpa_paged")
     return out
 
@@ -440,11 +447,13 @@ def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: 
 def _token_rows(name, x, B, L, d, dtype):
     """Heads and token stride of rows [B, L, heads, d] whose tokens are evenly
     spaced (a dense tensor, or a slice of a projection's output)."""
-    if x.dim() != 4 or x.shape[0] != B or x.shape[1] != L or x.shape[3] != d or x.dtype != dtype:
+    shape = x.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != L or shape[3] != d or x.dtype != dtype:
         raise ValueError(f"{name} must be [{B}, {L}, heads, {d}] {dtype}")
-    heads, (sb, sl, sh, sc) = x.shape[2], x.stride()
+    heads, (sb, sl, sh, sc) = shape[2], x.stride()
     ts = sl if L > 1 else sb if B > 1 else heads * d
-    if x.numel() and (sc != 1 and d > 1 or heads > 1 and sh != d or B > 1 and L > 1 and sb != L * ts):
+    if (sc != 1 and d > 1 or heads > 1 and sh != d or B > 1 and L > 1 and sb != L * ts) \
+            and x.numel():
         raise ValueError(f"{name}'s tokens must be evenly spaced and its heads contiguous")
     return heads, ts
 
@@ -457,15 +466,15 @@ def _rope_args(Q, K, gamma_q, gamma_k, pe, positions):
     Hkv, k_ts = _token_rows("K", K, B, L, d, Q.dtype)
     _gammas(gamma_q, gamma_k, pe, d, Q.dtype)
     if positions is not None:
-        _int32("positions", positions, (B, L))
+        _int32("positions", positions, B, L)
     return B, L, H, Hkv, d, q_ts, k_ts
 
 
 def _gammas(gamma_q, gamma_k, pe, d, dtype):
     for g in (gamma_q, gamma_k):
-        if tuple(g.shape) != (d,) or g.dtype != dtype or not g.is_contiguous():
+        if g.shape != (d,) or g.dtype != dtype or not g.is_contiguous():
             raise ValueError("gamma_q and gamma_k must be contiguous [d] of the rows' dtype")
-    if pe.dtype != torch.float32 or pe.dim() != 2 or not pe.is_contiguous():
+    if pe.dtype is not torch.float32 or pe.dim() != 2 or not pe.is_contiguous():
         raise ValueError("pe must be contiguous float32 [rows, rope_dim]")
 
 
@@ -476,20 +485,21 @@ def qk_norm_rope(Q, K, gamma_q, gamma_k, pe, pos_offset: int = 0, positions=None
     first pe.shape[1] columns rotated by the token's position (a row of pe, a
     ``sinusoidal_pe`` table): ``positions`` int32 [B, L], or pos_offset + l."""
     B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
-    given = out if out is not None else (None, None)
-    _on_current_device(Q, K, gamma_q, gamma_k, pe, positions, *given)
+    on = _launch_on(stream, Q, K, gamma_q, gamma_k, pe, Q if positions is None else positions,
+                    *(() if out is None else out))
     want = ((B, H, L, d), (B, Hkv, L, d))
     if out is None:
-        out = tuple(_new(stream, s, Q.dtype, Q.device) for s in want)
-    for o, s in zip(out, want):
-        if tuple(o.shape) != s or o.dtype != Q.dtype or not o.is_contiguous():
-            raise ValueError("out has the wrong shapes, dtype or layout")
-    st = lib().qk_norm_rope_forward(
+        out = (_new(stream, want[0], Q.dtype, Q.device), _new(stream, want[1], Q.dtype, Q.device))
+    else:
+        for o, s in zip(out, want):
+            if o.shape != s or o.dtype != Q.dtype or not o.is_contiguous():
+                raise ValueError("out has the wrong shapes, dtype or layout")
+    rows, r = pe.shape
+    st = (_lib or lib()).qk_norm_rope_forward(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
-        pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), out[0].data_ptr(),
-        out[1].data_ptr(), B, L, H, Hkv, d, int(pos_offset),
-        None if positions is None else positions.data_ptr(), float(eps), _dtype_code(Q.dtype),
-        _stream(stream))
+        pe.data_ptr(), rows, r, int(pairing), out[0].data_ptr(), out[1].data_ptr(), B, L, H, Hkv,
+        d, int(pos_offset), None if positions is None else positions.data_ptr(), float(eps),
+        _dtype_code(Q.dtype), on)
     _check(st, "qk_norm_rope_forward")
     return out
 
@@ -502,30 +512,36 @@ def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int 
     fp32 each, as ``sdpa_backward`` returns them).  ``out``: (dQ, dK) to fill,
     laid out as Q and K may be."""
     B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
-    if tuple(dQo.shape) != (B, H, L, d) or tuple(dKo.shape) != (B, Hkv, L, d) \
+    if dQo.shape != (B, H, L, d) or dKo.shape != (B, Hkv, L, d) \
             or not dQo.is_contiguous() or not dKo.is_contiguous():
         raise ValueError("dQo and dKo must be contiguous [B, heads, L, d]")
-    given = out if out is not None else (None, None)
-    _on_current_device(Q, K, gamma_q, gamma_k, pe, dQo, dKo, positions, workspace, *given)
+    on = _launch_on(stream, Q, K, gamma_q, gamma_k, pe, dQo, dKo,
+                    Q if positions is None else positions, Q if workspace is None else workspace,
+                    *(() if out is None else out))
     if out is None:
         out = (_new(stream, (B, L, H, d), Q.dtype, Q.device),
                _new(stream, (B, L, Hkv, d), Q.dtype, Q.device))
-    (h0, dq_ts), (h1, dk_ts) = (_token_rows("out", o, B, L, d, Q.dtype) for o in out)
-    if h0 != H or h1 != Hkv:
-        raise ValueError("out has the wrong shapes")
-    dg = _new(stream, (2, d + -d % 4), torch.float32, Q.device)
-    dgamma_q, dgamma_k = dg[0, :d], dg[1, :d]
+        dq_ts, dk_ts = H * d, Hkv * d
+    else:
+        (h0, dq_ts), (h1, dk_ts) = (_token_rows("out", o, B, L, d, Q.dtype) for o in out)
+        if h0 != H or h1 != Hkv:
+            raise ValueError("out has the wrong shapes")
+    # each gamma's gradient starts on 16 bytes
+    dgamma_q, dgamma_k = _new(stream, (2, d + -d % 4), torch.float32, Q.device).unbind(0)
+    if d % 4:
+        dgamma_q, dgamma_k = dgamma_q[:d], dgamma_k[:d]
+    dev = _lib or lib()
     if workspace is None:
-        need = int(lib().qk_norm_rope_backward_workspace_bytes(d))
-        workspace = _new(stream, max(16, need), torch.uint8, Q.device)
-    st = lib().qk_norm_rope_backward(
+        workspace = _new(stream, (dev.qk_norm_rope_backward_workspace_bytes(d) or 16,),
+                         torch.uint8, Q.device)
+    rows, r = pe.shape
+    st = dev.qk_norm_rope_backward(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
-        pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), dQo.data_ptr(), dKo.data_ptr(),
-        out[0].data_ptr(), dq_ts, out[1].data_ptr(), dk_ts, dgamma_q.data_ptr(),
-        dgamma_k.data_ptr(), B, L, H, Hkv, d, int(pos_offset),
-        None if positions is None else positions.data_ptr(), float(eps), _dtype_code(Q.dtype),
-        _dtype_code(dQo.dtype), _dtype_code(dKo.dtype), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        pe.data_ptr(), rows, r, int(pairing), dQo.data_ptr(), dKo.data_ptr(), out[0].data_ptr(),
+        dq_ts, out[1].data_ptr(), dk_ts, dgamma_q.data_ptr(), dgamma_k.data_ptr(), B, L, H, Hkv,
+        d, int(pos_offset), None if positions is None else positions.data_ptr(), float(eps),
+        _dtype_code(Q.dtype), _dtype_code(dQo.dtype), _dtype_code(dKo.dtype),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), on)
     _check(st, "qk_norm_rope_backward")
     return out[0], out[1], dgamma_q, dgamma_k
 
@@ -547,17 +563,17 @@ def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_tab
     if K.shape[0] != T or V.shape[0] != T:
         raise ValueError("Q, K and V must hold the same tokens")
     _gammas(gamma_q, gamma_k, pe, d, dt)
-    _int32("q_offsets", q_offsets, (pages.B + 1,))
-    _on_current_device(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
-                       q_offsets, out)
+    _int32("q_offsets", q_offsets, pages.B + 1)
+    on = _launch_on(stream, Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
+                    q_offsets, Q if out is None else out)
     if out is None:
         out = _new(stream, (T, H, d), dt, Q.device)
     elif out.shape != (T, H, d) or out.dtype != dt or not out.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
-    st = lib().qk_norm_rope_paged(
+    st = (_lib or lib()).qk_norm_rope_paged(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, V.data_ptr(), v_ts, gamma_q.data_ptr(),
         gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), out.data_ptr(),
-        pages, int(layer), q_offsets.data_ptr(), T, H, float(eps), _stream(stream))
+        pages, int(layer), q_offsets.data_ptr(), T, H, float(eps), on)
     _check(st, "qk_norm_rope_paged")
     return out
 
@@ -569,10 +585,10 @@ def kv_pages_fork(K_pages, V_pages, page_table, kv_lengths, parents, children, f
     pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
     n = parents.numel()
     for name, t in (("parents", parents), ("children", children), ("fresh", fresh)):
-        _int32(name, t, (n,))
-    _on_current_device(K_pages, V_pages, page_table, kv_lengths, parents, children, fresh)
-    _check(lib().kv_pages_fork(pages, parents.data_ptr(), children.data_ptr(), fresh.data_ptr(), n,
-                               _stream(stream)), "kv_pages_fork")
+        _int32(name, t, n)
+    on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, parents, children, fresh)
+    _check((_lib or lib()).kv_pages_fork(pages, parents.data_ptr(), children.data_ptr(),
+                                         fresh.data_ptr(), n, on), "kv_pages_fork")
 
 
 def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
@@ -581,13 +597,15 @@ def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, tab
     in order; table_out is the renumbered page table.  Returns n (int32 [1])."""
     src = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
     dst = _kv_pages(K_out, V_out, table_out, kv_lengths)
-    _on_current_device(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out, workspace)
+    on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
+                    K_pages if workspace is None else workspace)
     count = _new(stream, (1,), torch.int32, K_pages.device)
+    dev = _lib or lib()
     if workspace is None:
-        need = int(lib().kv_pages_compact_workspace_bytes(src.num_pages))
-        workspace = _new(stream, max(16, need), torch.uint8, K_pages.device)
-    _check(lib().kv_pages_compact(src, dst, count.data_ptr(), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)),
+        workspace = _new(stream, (dev.kv_pages_compact_workspace_bytes(src.num_pages) or 16,),
+                         torch.uint8, K_pages.device)
+    _check(dev.kv_pages_compact(src, dst, count.data_ptr(), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), on),
            "kv_pages_compact")
     return count
 
