@@ -226,36 +226,65 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_any_bwd_kernel(const Tr
 
 // ------------------------------------------------------------- vector kernels
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+// Eight elements as loaded (requested early) and as four fp32 pairs.
+template <typename T>
+struct Raw8;
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+template <>
+struct Raw8<__nv_bfloat16> {
   uint4 u;
-  u.x = pack_bf16x2(v[0], v[1]);
-  u.y = pack_bf16x2(v[2], v[3]);
-  u.z = pack_bf16x2(v[4], v[5]);
-  u.w = pack_bf16x2(v[6], v[7]);
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __bfloat1622float2(h[i]);
+  }
+};
+
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float2 (&v)[4]) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(v);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2 (&v)[4]) {
+  uint4 u;
+  u.x = pack_bf16x2(v[0].x, v[0].y);
+  u.y = pack_bf16x2(v[1].x, v[1].y);
+  u.z = pack_bf16x2(v[2].x, v[2].y);
+  u.w = pack_bf16x2(v[3].x, v[3].y);
   *reinterpret_cast<uint4*>(p) = u;
 }
 
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 
 // A lane's place in a row of D columns: vectors `a` and `b` (in elements).
@@ -278,7 +307,7 @@ struct VecLane {
 // Sines and cosines of a lane's eight pairs: half-wise pairs (a + i, b + i),
 // or interleaved ones, four in each vector.
 struct Turns {
-  float sn[8], cs[8];
+  float2 sn[4], cs[4];
 
   __device__ __forceinline__ void load(const float* pe, int a, int b, bool turns, int half) {
 #pragma unroll
@@ -288,19 +317,29 @@ struct Turns {
       if (turns)
         v = __ldg(reinterpret_cast<const float4*>(half ? pe + 2 * a : k < 2 ? pe + a : pe + b - 8) +
                   k);
-      sn[2 * k] = v.x, cs[2 * k] = v.y, sn[2 * k + 1] = v.z, cs[2 * k + 1] = v.w;
+      sn[k] = make_float2(v.x, v.z);
+      cs[k] = make_float2(v.y, v.w);
     }
   }
 
-  // Rotate by the angle (sign 1) or its opposite (sign -1).
-  __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], int half, float sign) const {
+  // Rotate by the angle, or by its opposite.
+  template <int HALF, bool BACK>
+  __device__ __forceinline__ void turn(float2 (&x)[4], float2 (&y)[4]) const {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float& p = half ? x[k] : k < 4 ? x[2 * k] : y[2 * (k - 4)];
-      float& q = half ? y[k] : k < 4 ? x[2 * k + 1] : y[2 * (k - 4) + 1];
-      const float s = sign * sn[k], u = p, v = q;
-      p = u * cs[k] - v * s;
-      q = v * cs[k] + u * s;
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (HALF) {
+        const float2 s = BACK ? make_float2(-sn[k].x, -sn[k].y) : sn[k];
+        const float2 u = x[k], v = y[k];
+        x[k] = ffma2(v, make_float2(-s.x, -s.y), fmul2(u, cs[k]));
+        y[k] = ffma2(u, s, fmul2(v, cs[k]));
+      } else {
+        // pairs 2k and 2k + 1: those of x, then those of y
+        float2& p = k < 2 ? x[2 * k] : y[2 * k - 4];
+        float2& q = k < 2 ? x[2 * k + 1] : y[2 * k - 3];
+        const float s0 = BACK ? -sn[k].x : sn[k].x, s1 = BACK ? -sn[k].y : sn[k].y;
+        p = make_float2(fmaf(p.x, cs[k].x, -p.y * s0), fmaf(p.y, cs[k].x, p.x * s0));
+        q = make_float2(fmaf(q.x, cs[k].y, -q.y * s1), fmaf(q.y, cs[k].y, q.x * s1));
+      }
     }
   }
 };
@@ -312,164 +351,255 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// One row per group of lanes.  Every lane of the warp takes part; `live`
-// lanes hold x, the others zeros.
-template <int D, typename T>
-__device__ __forceinline__ void norm_rope_vec(float (&x)[8], float (&y)[8], const T* gamma,
-                                              const VecLane<D>& at, const Turns& turns, int half,
-                                              float eps) {
-  float ss = 0.f;
+// The sum of a lane's products.
+__device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]) {
+  float2 s = fmul2(a[0], b[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-  const float rstd = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
-  float ga[8], gb[8];
-  load8(gamma + at.a, ga);
-  load8(gamma + at.b, gb);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] *= rstd * ga[i];
-    y[i] *= rstd * gb[i];
-  }
-  turns.turn(x, y, half, 1.f);
+  for (int i = 1; i < 4; ++i) s = ffma2(a[i], b[i], s);
+  return s.x + s.y;
 }
 
-// Rows of one tensor, of `heads` heads a token.
-struct RowPlace {
-  uint32_t token, h, b, l;
-  __device__ __forceinline__ RowPlace(uint32_t row, uint32_t heads, uint32_t L) {
-    token = row / heads;
-    h = row - token * heads;
-    b = token / L;
-    l = token - b * L;
+__device__ __forceinline__ void scale8(float2 (&a)[4], const float2 (&g)[4], float s) {
+  const float2 s2 = make_float2(s, s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmul2(fmul2(a[i], s2), g[i]);
+}
+
+// One row per group of lanes.  Every lane of the warp takes part, those
+// without a row on zeros.
+template <int D, int HALF, typename T>
+__device__ __forceinline__ void norm_rope_vec(float2 (&x)[4], float2 (&y)[4], const T* gamma,
+                                              const VecLane<D>& at, const Turns& turns,
+                                              float eps) {
+  const float ss = row_sum<D>(dot8(x, x) + dot8(y, y));
+  const float rstd = rsqrtf(ss * (1.f / D) + eps);
+  float2 ga[4], gb[4];
+  load8(gamma + at.a, ga);
+  load8(gamma + at.b, gb);
+  scale8(x, ga, rstd);
+  scale8(y, gb, rstd);
+  turns.turn<HALF, false>(x, y);
+}
+
+// How a warp's row groups take the heads of tokens: as many whole tokens at a
+// time as fit, or one token over several rounds.  A row group keeps its token,
+// so its sines and cosines are loaded once for all of the token's heads.
+struct Rounds {
+  int tokens;  // tokens a warp takes at a time
+  int cols;    // row groups to a token
+  int rounds;  // rounds of heads to a token
+  __device__ __forceinline__ Rounds(int heads, int groups) {
+    tokens = heads < groups ? groups / heads : 1;
+    cols = heads < groups ? heads : groups;
+    rounds = (heads + groups - 1) / groups;
+  }
+};
+
+// A row group's walk over its tokens and, within a token, its rounds.
+// `parts` warps share a token's rounds (when there are few tokens).
+struct Walk {
+  uint32_t it, token, b, l;
+  int round;
+  bool here;        // the row group has a token
+  const float* pe;  // its table row, nullptr without one
+
+  __device__ __forceinline__ void enter(const TrainArgs& p, const Rounds& rd, int gt, int parts,
+                                        uint32_t tokens, uint32_t items) {
+    const uint32_t tg = it / parts;
+    round = static_cast<int>(it - tg * parts);
+    token = tg * rd.tokens + gt;
+    here = it < items && gt < rd.tokens && token < tokens;
+    if (!here) token = 0;
+    b = token / p.L;
+    l = token - b * p.L;
+    pe = here ? table_row(p, token, l) : nullptr;
+  }
+  // On to the next round; true when that is another token's.
+  __device__ __forceinline__ bool next(const TrainArgs& p, const Rounds& rd, int gt, int parts,
+                                       uint32_t tokens, uint32_t items) {
+    round += parts;
+    if (round < rd.rounds) return false;
+    it += gridDim.x * kWarps;
+    enter(p, rd, gt, parts, tokens, items);
+    return true;
   }
 };
 
 template <int D, typename T, int HALF>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_vec_kernel(const TrainArgs p) {
+__global__ void __launch_bounds__(32 * kWarps)
+    norm_rope_vec_kernel(const TrainArgs p, int parts) {
   using V = VecLane<D>;
   const V at(p.r);
-  const int lane = threadIdx.x & 31;
+  const int group = (threadIdx.x & 31) / V::kLanes;
+  const int heads = p.heads[0] + p.heads[1];
+  const Rounds rd(heads, V::kRows);
   const uint32_t tokens = static_cast<uint32_t>(p.B) * p.L;
-  const uint32_t rows[2] = {tokens * p.heads[0], tokens * p.heads[1]};
-  const uint32_t items0 = (rows[0] + V::kRows - 1) / V::kRows;
-  const uint32_t items = items0 + (rows[1] + V::kRows - 1) / V::kRows;
-  for (uint32_t it = blockIdx.x * kWarps + (threadIdx.x >> 5); it < items;
-       it += gridDim.x * kWarps) {
-    const int w = it >= items0;  // queries, then keys: uniform in a warp
-    const uint32_t row = (w ? it - items0 : it) * V::kRows + lane / V::kLanes;
-    const bool live = row < rows[w];
-    const RowPlace at_row(live ? row : 0, p.heads[w], p.L);
-    const T* x = static_cast<const T*>(p.x[w]) + at_row.token * p.ts[w] +
-                 static_cast<int64_t>(at_row.h) * D;
-    float a[8] = {}, b[8] = {};
+  const uint32_t items = (tokens + rd.tokens - 1) / rd.tokens * parts;
+  const int gt = group / rd.cols, h0 = group - gt * rd.cols;
+  Walk c;
+  c.it = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  c.enter(p, rd, gt, parts, tokens, items);
+  auto request = [&](const Walk& k, Raw8<T>& ra, Raw8<T>& rb) {
+    const int h = h0 + k.round * V::kRows;
+    ra.zero();
+    rb.zero();
+    if (!k.here || h >= heads) return;
+    const int w = h >= p.heads[0];
+    const T* x = static_cast<const T*>(p.x[w]) + k.token * p.ts[w] +
+                 static_cast<int64_t>(w ? h - p.heads[0] : h) * D;
+    ra.load(x + at.a);
+    rb.load(x + at.b);
+  };
+  Raw8<T> ra, rb;
+  request(c, ra, rb);
+  Turns turns;
+  turns.load(c.pe, at.a, at.b, at.turns && c.pe, HALF);
+  while (c.it < items) {
+    float2 x[4], y[4];
+    ra.get(x);
+    rb.get(y);
+    Walk n = c;
+    const bool other = n.next(p, rd, gt, parts, tokens, items);
+    request(n, ra, rb);  // the next rows, while these are computed
+    const int h = h0 + c.round * V::kRows;
+    const int w = h >= p.heads[0];
+    const int hw = w ? h - p.heads[0] : h;
+    const bool live = c.here && h < heads;
+    norm_rope_vec<D, HALF>(
+        x, y, static_cast<const T*>(live ? p.gamma[w] : p.gamma[h0 >= p.heads[0]]), at, turns,
+        p.eps);
     if (live) {
-      load8(x + at.a, a);
-      load8(x + at.b, b);
-    }
-    const float* pe = table_row(p, at_row.token, at_row.l);
-    if (live && !pe) atomicOr(p.err, kErrPosition);
-    Turns turns;
-    turns.load(pe, at.a, at.b, at.turns && pe, HALF);
-    norm_rope_vec<D>(a, b, static_cast<const T*>(p.gamma[w]), at, turns, HALF, p.eps);
-    if (live) {
-      T* y = static_cast<T*>(p.y[w]) +
-             ((static_cast<int64_t>(at_row.b) * p.heads[w] + at_row.h) * p.L + at_row.l) * D;
-      if (!pe) {
+      T* out = static_cast<T*>(p.y[w]) +
+               ((static_cast<int64_t>(c.b) * p.heads[w] + hw) * p.L + c.l) * D;
+      if (!c.pe) {
+        atomicOr(p.err, kErrPosition);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.f;
+        for (int i = 0; i < 4; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
       }
-      store8(y + at.a, a);
-      store8(y + at.b, b);
+      store8(out + at.a, x);
+      store8(out + at.b, y);
     }
+    c = n;
+    if (other) turns.load(c.pe, at.a, at.b, at.turns && c.pe, HALF);
   }
 }
 
 // dx of every row; per block the sums of dz * xh over its rows, first over a
 // lane's rows, then over the row groups of a warp, then over the warps: a
 // fixed order.
-template <int D, typename T, int HALF>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_vec_bwd_kernel(const TrainArgs p) {
+template <int D, typename T, typename TG, int HALF>
+__device__ __forceinline__ void norm_rope_vec_bwd_part(const TrainArgs& p, int w, int parts,
+                                                       float2 (&g0)[4], float2 (&g1)[4]) {
   using V = VecLane<D>;
-  __shared__ float sums[kWarps][D];
+  const V at(p.r);
+  const int group = (threadIdx.x & 31) / V::kLanes;
+  const int heads = p.heads[w];
+  const Rounds rd(heads, V::kRows);
+  const uint32_t tokens = static_cast<uint32_t>(p.B) * p.L;
+  const uint32_t items = (tokens + rd.tokens - 1) / rd.tokens * parts;
+  const int gt = group / rd.cols, h0 = group - gt * rd.cols;
+  Walk c;
+  c.it = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  c.enter(p, rd, gt, parts, tokens, items);
+  auto request = [&](const Walk& k, Raw8<T>& ra, Raw8<T>& rb, Raw8<TG>& ru, Raw8<TG>& rv) {
+    const int h = h0 + k.round * V::kRows;
+    ra.zero();
+    rb.zero();
+    ru.zero();
+    rv.zero();
+    if (!k.pe || h >= heads) return;
+    const T* x = static_cast<const T*>(p.x[w]) + k.token * p.ts[w] + static_cast<int64_t>(h) * D;
+    const TG* dy = static_cast<const TG*>(p.dy[w]) +
+                   ((static_cast<int64_t>(k.b) * heads + h) * p.L + k.l) * D;
+    ra.load(x + at.a);
+    rb.load(x + at.b);
+    ru.load(dy + at.a);
+    rv.load(dy + at.b);
+  };
+  Raw8<T> ra, rb;
+  Raw8<TG> ru, rv;
+  request(c, ra, rb, ru, rv);
+  Turns turns;
+  turns.load(c.pe, at.a, at.b, at.turns && c.pe, HALF);
+  while (c.it < items) {
+    float2 x[4], y[4], u[4], v[4];
+    ra.get(x);
+    rb.get(y);
+    ru.get(u);
+    rv.get(v);
+    Walk n = c;
+    const bool other = n.next(p, rd, gt, parts, tokens, items);
+    request(n, ra, rb, ru, rv);  // the next rows, while these are computed
+    turns.turn<HALF, true>(u, v);
+    const float ss = row_sum<D>(dot8(x, x) + dot8(y, y));
+    const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
+    const float2 rstd2 = make_float2(rstd, rstd);
+    float2 ga[4], gb[4];
+    load8(static_cast<const T*>(p.gamma[w]) + at.a, ga);
+    load8(static_cast<const T*>(p.gamma[w]) + at.b, gb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = fmul2(x[i], rstd2);
+      y[i] = fmul2(y[i], rstd2);
+      g0[i] = ffma2(u[i], x[i], g0[i]);
+      g1[i] = ffma2(v[i], y[i], g1[i]);
+      u[i] = fmul2(u[i], ga[i]);
+      v[i] = fmul2(v[i], gb[i]);
+    }
+    const float m = row_sum<D>(dot8(u, x) + dot8(v, y)) * (-1.f / D);
+    const float2 m2 = make_float2(m, m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = fmul2(rstd2, ffma2(x[i], m2, u[i]));
+      y[i] = fmul2(rstd2, ffma2(y[i], m2, v[i]));
+    }
+    const int h = h0 + c.round * V::kRows;
+    if (c.here && h < heads) {
+      if (!c.pe) atomicOr(p.err, kErrPosition);
+      T* dx = static_cast<T*>(p.dx[w]) + c.token * p.dts[w] + static_cast<int64_t>(h) * D;
+      store8(dx + at.a, x);
+      store8(dx + at.b, y);
+    }
+    c = n;
+    if (other) turns.load(c.pe, at.a, at.b, at.turns && c.pe, HALF);
+  }
+}
+
+template <int D, typename T, int HALF>
+__global__ void __launch_bounds__(32 * kWarps)
+    norm_rope_vec_bwd_kernel(const TrainArgs p, int parts) {
+  using V = VecLane<D>;
+  __shared__ float2 sums[kWarps][D / 2];
   const V at(p.r);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t tokens = static_cast<uint32_t>(p.B) * p.L;
   for (int w = 0; w < 2; ++w) {
-    float g0[8] = {}, g1[8] = {}, ga[8], gb[8];
-    const uint32_t rows = tokens * p.heads[w];
-    const uint32_t items = (rows + V::kRows - 1) / V::kRows;
-    if (rows) {
-      load8(static_cast<const T*>(p.gamma[w]) + at.a, ga);
-      load8(static_cast<const T*>(p.gamma[w]) + at.b, gb);
-    }
-    for (uint32_t it = blockIdx.x * kWarps + warp; it < items; it += gridDim.x * kWarps) {
-      const uint32_t row = it * V::kRows + lane / V::kLanes;
-      const RowPlace at_row(row < rows ? row : 0, p.heads[w], p.L);
-      const float* pe = table_row(p, at_row.token, at_row.l);
-      if (row < rows && !pe) atomicOr(p.err, kErrPosition);
-      const bool live = row < rows && pe;
-      const int64_t in = static_cast<int64_t>(at_row.h) * D;
-      const int64_t dy0 =
-          ((static_cast<int64_t>(at_row.b) * p.heads[w] + at_row.h) * p.L + at_row.l) * D;
-      float a[8] = {}, b[8] = {}, u[8] = {}, v[8] = {};
-      if (live) {
-        const T* x = static_cast<const T*>(p.x[w]) + at_row.token * p.ts[w] + in;
-        load8(x + at.a, a);
-        load8(x + at.b, b);
-        if (p.dy_f32[w]) {
-          load8(static_cast<const float*>(p.dy[w]) + dy0 + at.a, u);
-          load8(static_cast<const float*>(p.dy[w]) + dy0 + at.b, v);
-        } else {
-          load8(static_cast<const __nv_bfloat16*>(p.dy[w]) + dy0 + at.a, u);
-          load8(static_cast<const __nv_bfloat16*>(p.dy[w]) + dy0 + at.b, v);
-        }
-      }
-      Turns turns;
-      turns.load(pe, at.a, at.b, at.turns && pe, HALF);
-      turns.turn(u, v, HALF, -1.f);
-      float ss = 0.f, ux = 0.f;
+    float2 g0[4] = {}, g1[4] = {};
+    if (p.heads[w] && p.dy_f32[w])
+      norm_rope_vec_bwd_part<D, T, float, HALF>(p, w, parts, g0, g1);
+    else if (p.heads[w])
+      norm_rope_vec_bwd_part<D, T, __nv_bfloat16, HALF>(p, w, parts, g0, g1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-        ux = fmaf(u[i] * ga[i], a[i], fmaf(v[i] * gb[i], b[i], ux));
-      }
-      ss = row_sum<D>(ss);
-      ux = row_sum<D>(ux);
-      const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-      const float m = rstd * rstd * ux * (1.f / D);  // mean(u * xh) * rstd
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g0[i] = fmaf(u[i], a[i] * rstd, g0[i]);
-        g1[i] = fmaf(v[i], b[i] * rstd, g1[i]);
-        a[i] = rstd * (u[i] * ga[i] - a[i] * m);
-        b[i] = rstd * (v[i] * gb[i] - b[i] * m);
-      }
-      if (row < rows) {
-        T* dx = static_cast<T*>(p.dx[w]) + at_row.token * p.dts[w] + in;
-        store8(dx + at.a, a);
-        store8(dx + at.b, b);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int s = V::kLanes; s < 32; s <<= 1) {
-        g0[i] += __shfl_xor_sync(0xffffffffu, g0[i], s);
-        g1[i] += __shfl_xor_sync(0xffffffffu, g1[i], s);
+        g0[i].x += __shfl_xor_sync(0xffffffffu, g0[i].x, s);
+        g0[i].y += __shfl_xor_sync(0xffffffffu, g0[i].y, s);
+        g1[i].x += __shfl_xor_sync(0xffffffffu, g1[i].x, s);
+        g1[i].y += __shfl_xor_sync(0xffffffffu, g1[i].y, s);
       }
     }
     __syncthreads();  // the previous part's sums have been read
     if (lane < V::kLanes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[warp][at.a + i] = g0[i];
-        sums[warp][at.b + i] = g1[i];
+      for (int i = 0; i < 4; ++i) {
+        sums[warp][at.a / 2 + i] = g0[i];
+        sums[warp][at.b / 2 + i] = g1[i];
       }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += 32 * kWarps) {
       float s = 0.f;
-      for (int k = 0; k < kWarps; ++k) s += sums[k][c];
+      for (int k = 0; k < kWarps; ++k) s += reinterpret_cast<const float*>(sums[k])[c];
       p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + w) * D + c] = s;
     }
   }
@@ -512,9 +642,10 @@ struct PagedArgs {
 
 constexpr int kMaxBlockTokens = 8;  // one warp looks one token up
 
-// A block takes block_tokens tokens: their sequences, positions and page rows
-// are looked up once, a warp per token, then all warps take their rows,
-// queries, keys and values, kRows at a time.
+// A block takes block_tokens tokens (gridDim.y blocks share them when there
+// are few): their sequences, positions and page rows are looked up once, a
+// warp per token, then all warps take their rows, queries, keys and values,
+// kRows at a time.
 template <int D, int HALF>
 __global__ void __launch_bounds__(32 * kWarps)
     norm_rope_paged_kernel(const PagedArgs p, int block_tokens) {
@@ -557,45 +688,47 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   __syncthreads();
   const int head_rows = D << pg.page_shift;  // elements from kv head to kv head of a page
-  const int heads[3] = {p.H, pg.kv_heads, pg.kv_heads};
-#pragma unroll
-  for (int w = 0; w < 3; ++w) {  // queries, keys, values
-    const int rows = tokens * heads[w];
-    for (int r0 = warp * V::kRows; r0 < rows; r0 += kWarps * V::kRows) {
-      const int row = r0 + lane / V::kLanes;
-      const int k = row < rows ? row / heads[w] : 0;
-      const int h = row - k * heads[w];
-      const int pos = row < rows ? pos_of[k] : -1;
-      const int64_t t = t0 + k;
-      const __nv_bfloat16* x = (w == 0 ? p.q + t * p.qs : w == 1 ? p.k + t * p.ks : p.v + t * p.vs) +
-                               static_cast<int64_t>(h) * D;
-      const int64_t out = w == 0 ? (t * p.H + h) * D
-                                 : row_at[k] + static_cast<int64_t>(h) * head_rows;
-      if (w == 2) {
-        if (pos < 0) continue;
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(pg.V) + out;
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + at.a));
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(x + at.b));
-        *reinterpret_cast<uint4*>(y + at.a) = a;
-        *reinterpret_cast<uint4*>(y + at.b) = b;
-        continue;
-      }
-      float a[8] = {}, b[8] = {};
-      if (pos >= 0) {
-        load8(x + at.a, a);
-        load8(x + at.b, b);
-      }
-      Turns turns;
-      turns.load(p.pe + static_cast<int64_t>(max(pos, 0)) * p.r, at.a, at.b, at.turns && pos >= 0,
-                 HALF);
-      norm_rope_vec<D>(a, b, w == 0 ? p.gq : p.gk, at, turns, HALF, p.eps);
-      // a bad entry: the query row is zeros (a and b are), the page untouched
-      if (pos == -1 || (w == 1 && pos < 0)) continue;
-      __nv_bfloat16* y = w == 0 ? p.qo + out : static_cast<__nv_bfloat16*>(pg.K) + out;
-      store8(y + at.a, a);
-      store8(y + at.b, b);
+  const int q_items = (tokens * p.H + V::kRows - 1) / V::kRows;
+  const int kv_items = (tokens * pg.kv_heads + V::kRows - 1) / V::kRows;
+  for (int it = blockIdx.y * kWarps + warp; it < q_items + 2 * kv_items;
+       it += gridDim.y * kWarps) {
+    // queries, keys, values: uniform in a warp
+    const int w = it < q_items ? 0 : it < q_items + kv_items ? 1 : 2;
+    const int heads = w ? pg.kv_heads : p.H;
+    const int row = (w == 0 ? it : it - q_items - (w - 1) * kv_items) * V::kRows + lane / V::kLanes;
+    const int k = row < tokens * heads ? row / heads : 0;
+    const int h = row - k * heads;
+    const int pos = row < tokens * heads ? pos_of[k] : -1;
+    const int64_t t = t0 + k;
+    const __nv_bfloat16* x = (w == 0 ? p.q + t * p.qs : w == 1 ? p.k + t * p.ks : p.v + t * p.vs) +
+                             static_cast<int64_t>(h) * D;
+    __nv_bfloat16* y = w == 0 ? p.qo + (t * p.H + h) * D
+                              : static_cast<__nv_bfloat16*>(w == 1 ? pg.K : pg.V) + row_at[k] +
+                                    static_cast<int64_t>(h) * head_rows;
+    Raw8<__nv_bfloat16> ra, rb;
+    ra.zero();
+    rb.zero();
+    if (pos >= 0) {
+      ra.load(x + at.a);
+      rb.load(x + at.b);
     }
-    __syncwarp();
+    if (w == 2) {
+      if (pos < 0) continue;
+      *reinterpret_cast<uint4*>(y + at.a) = ra.u;
+      *reinterpret_cast<uint4*>(y + at.b) = rb.u;
+      continue;
+    }
+    float2 a[4], b[4];
+    ra.get(a);
+    rb.get(b);
+    Turns turns;
+    turns.load(p.pe + static_cast<int64_t>(max(pos, 0)) * p.r, at.a, at.b, at.turns && pos >= 0,
+               HALF);
+    norm_rope_vec<D, HALF>(a, b, w == 0 ? p.gq : p.gk, at, turns, p.eps);
+    // a bad entry: the query row is zeros (a and b are), the page untouched
+    if (pos == -1 || (w == 1 && pos < 0)) continue;
+    store8(y + at.a, a);
+    store8(y + at.b, b);
   }
 }
 
@@ -632,7 +765,23 @@ mha_status check_rope(const float* pe, int pe_rows, int rope_dim, int pairing, i
 // Head rows that can be read as 16-byte vectors of whole pairs.
 bool vector_rows(int d, int rope_dim) { return (d == 64 || d == 128) && rope_dim % 16 == 0; }
 
-int64_t vec_items(int64_t rows, int d) { return (rows + 512 / d - 1) / (512 / d); }
+// Warps' shares of the work of the vector kernels: a warp takes all heads of
+// its tokens, or, while that leaves fewer than eight warps to an SM, a part of
+// their rounds.
+struct VecShape {
+  int64_t items;
+  int parts;
+};
+
+VecShape vec_shape(int64_t tokens, int heads, int d) {
+  const int groups = 512 / d;  // rows a warp has in flight
+  const int64_t at_once = heads < groups && heads > 0 ? groups / heads : 1;
+  const int64_t items = (tokens + at_once - 1) / at_once;
+  const int rounds = (heads + groups - 1) / groups;
+  const int64_t want = items > 0 ? 8 * static_cast<int64_t>(num_sms()) / items : 1;
+  const int parts = want < 1 ? 1 : want < rounds ? static_cast<int>(want) : rounds < 1 ? 1 : rounds;
+  return {items * parts, parts};
+}
 
 struct ForwardKernels {
   template <int D, typename T, int HALF>
@@ -644,13 +793,13 @@ struct BackwardKernels {
 };
 
 template <typename K, typename T>
-void (*vec_kernel_of(int d, int half))(const TrainArgs) {
+void (*vec_kernel_of(int d, int half))(const TrainArgs, int) {
   if (d == 64) return half ? K::template get<64, T, 1>() : K::template get<64, T, 0>();
   return half ? K::template get<128, T, 1>() : K::template get<128, T, 0>();
 }
 
 template <typename K>
-void (*vec_kernel(int d, int dtype, int half))(const TrainArgs) {
+void (*vec_kernel(int d, int dtype, int half))(const TrainArgs, int) {
   return dtype == MHA_BF16 ? vec_kernel_of<K, __nv_bfloat16>(d, half)
                            : vec_kernel_of<K, float>(d, half);
 }
@@ -702,8 +851,9 @@ mha_status qk_norm_rope_forward(const void* Q, int64_t q_token_stride, const voi
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(B) * L * (H + Hkv);
   if (vec) {
-    const auto kern = vec_kernel<ForwardKernels>(d, dtype, pairing);
-    kern<<<grid_for(vec_items(rows, d), 8), 32 * kWarps, 0, s>>>(p);
+    const VecShape v = vec_shape(static_cast<int64_t>(B) * L, H + Hkv, d);
+    vec_kernel<ForwardKernels>(d, dtype, pairing)<<<grid_for(v.items, 3), 32 * kWarps, 0, s>>>(
+        p, v.parts);
   } else if (dtype == MHA_BF16) {
     norm_rope_any_kernel<__nv_bfloat16><<<grid_for(rows, 16), 32 * kWarps, 0, s>>>(p);
   } else {
@@ -761,11 +911,12 @@ mha_status qk_norm_rope_backward(const void* Q, int64_t q_token_stride, const vo
   p.err = ctl.err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(B) * L * (H > Hkv ? H : Hkv);
-  unsigned blocks = grid_for(vec ? vec_items(rows, d) : rows, 4);
+  const VecShape v = vec_shape(static_cast<int64_t>(B) * L, H > Hkv ? H : Hkv, d);
+  unsigned blocks = vec ? grid_for(v.items, 2) : grid_for(rows, 4);
   if (blocks > kMaxGradBlocks) blocks = kMaxGradBlocks;
   if (blocks) {
     if (vec)
-      vec_kernel<BackwardKernels>(d, dtype, pairing)<<<blocks, 32 * kWarps, 0, s>>>(p);
+      vec_kernel<BackwardKernels>(d, dtype, pairing)<<<blocks, 32 * kWarps, 0, s>>>(p, v.parts);
     else if (dtype == MHA_BF16)
       norm_rope_any_bwd_kernel<__nv_bfloat16><<<blocks, 32 * kWarps, 0, s>>>(p);
     else
@@ -810,7 +961,12 @@ mha_status qk_norm_rope_paged(const void* Q, int64_t q_token_stride, const void*
   const int block_tokens = per_block < 1 ? 1 : per_block < kMaxBlockTokens
                                                    ? static_cast<int>(per_block)
                                                    : kMaxBlockTokens;
-  const unsigned grid = static_cast<unsigned>((T + block_tokens - 1) / block_tokens);
+  // a round of rows for every warp, as long as the SMs have room
+  const int token_blocks = (T + block_tokens - 1) / block_tokens;
+  const int rounds = (H + 2 * Hkv + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
+  const int room = 2 * num_sms() / token_blocks;
+  const dim3 grid(static_cast<unsigned>(token_blocks),
+                  static_cast<unsigned>(room < 1 ? 1 : room < rounds ? room : rounds));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64 && pairing == MHA_ROPE_HALF)
     norm_rope_paged_kernel<64, 1><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
