@@ -44,10 +44,9 @@ int paged_max_active_clusters(int threads, int smem_bytes, int splits) {
   return n;
 }
 
-int paged_default_splits(int64_t clusters, int key_tiles, int threads, int smem_bytes) {
-  // A second, partial wave of clusters costs more than the SMs that a single
-  // wave leaves idle; how many fit depends on their size (a cluster sits
-  // inside one GPC), so the device is asked for every size, once.
+int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
+  // How many clusters of each size are resident at once (a cluster sits
+  // inside one GPC): the device is asked once per kernel.
   struct Entry {
     int dev, threads, smem;
     int fits[kPagedMaxSplits + 1];
@@ -64,14 +63,28 @@ int paged_default_splits(int64_t clusters, int key_tiles, int threads, int smem_
       e = &table[i];
   Entry fresh{dev, threads, smem_bytes, {}};
   if (!e) {
-    for (int s = 2; s <= kPagedMaxSplits; ++s)
+    for (int s = 1; s <= kPagedMaxSplits; ++s)
       fresh.fits[s] = paged_max_active_clusters(threads, smem_bytes, s);
     if (used < 64) table[used++] = fresh;
     e = &fresh;
   }
+  // Time in units of one 128-key tile: a CTA's tiles, its set-up and first
+  // loads (4), and the merge (3).  Waves of clusters: lengths differ and long
+  // sequences go first, so a partial last wave costs something between its
+  // share and a whole one.
+  const double tiles = static_cast<double>(capacity) / 128;
   int best = 1;
-  for (int s = 2; s <= kPagedMaxSplits && s <= key_tiles; ++s)
-    if (e->fits[s] >= clusters) best = s;
+  double least = 0;
+  for (int s = 1; s <= kPagedMaxSplits && (s == 1 || s <= tiles); ++s) {
+    if (e->fits[s] < 1) continue;
+    const double waves = static_cast<double>(blocks) / e->fits[s];
+    const double cost = (waves <= 1 ? 1 : 0.5 * (ceil(waves) + waves)) *
+                        (tiles / s + 4 + (s > 1 ? 3 : 0));
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
   return best;
 }
 

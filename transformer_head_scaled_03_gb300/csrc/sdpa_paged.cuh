@@ -80,16 +80,19 @@ struct PagedSeq {
   bool bad_len, bad_offsets;
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+__device__ __forceinline__ PagedSeq paged_seq_of(const PagedParams& p, int q0, int q1, int len) {
   PagedSeq s{};
-  const int q0 = __ldg(p.q_offsets + b), q1 = __ldg(p.q_offsets + b + 1);
-  s.len = __ldg(p.kv_len + b);
+  s.len = len;
   s.bad_offsets = q0 < 0 || q1 < q0 || q1 > p.T || q1 - q0 > p.max_new;
   s.q0 = q0;
   s.n = s.bad_offsets ? 0 : q1 - q0;
   const int64_t cap = static_cast<int64_t>(p.cols) << p.page_shift;
   s.bad_len = s.n > 0 && (s.len < 1 || s.len > cap || (p.causal && s.len < s.n));
   return s;
+}
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  return paged_seq_of(p, __ldg(p.q_offsets + b), __ldg(p.q_offsets + b + 1), __ldg(p.kv_len + b));
 }
 
 // The page boxes of one tile of ROWS keys, one per lane of the producer warp:
@@ -147,6 +150,36 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
   return v;
 }
 
+// Four columns of the merged output: sum over the cluster's splits of weight
+// times partial output (at the same shared address in every split).  All
+// loads are requested before the first is used.  A weight of 0 stands for
+// nothing seen, and for rows to be zeroed, whose partial output may be
+// anything.
+__device__ __forceinline__ float4 merge_splits(uint32_t from, const float* weight, int stride,
+                                               int splits) {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s0 = 0; s0 < kPagedMaxSplits; s0 += 8) {
+    if (s0 >= splits) break;
+    float4 v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < splits)
+        v[s] = ld_cluster_f32x4(cluster_map(from, static_cast<uint32_t>(s0 + s)));
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float w = s0 + s < splits ? weight[(s0 + s) * stride] : 0.f;
+      if (w != 0.f) {
+        o.x = fmaf(w, v[s].x, o.x);
+        o.y = fmaf(w, v[s].y, o.y);
+        o.z = fmaf(w, v[s].z, o.z);
+        o.w = fmaf(w, v[s].w, o.w);
+      }
+    }
+  }
+  return o;
+}
+
 // Bounded wait that ignores the abort flag (copies and products in flight).
 __device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
@@ -159,8 +192,7 @@ __device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, 
 // memory that the device holds at once (0 when the query fails).
 int paged_max_active_clusters(int threads, int smem_bytes, int splits);
 
-// The largest split count whose `clusters` clusters are all resident at once
-// and that leaves no split without a key tile.
-int paged_default_splits(int64_t clusters, int key_tiles, int threads, int smem_bytes);
+// Split count for `blocks` blocks over sequences of up to `capacity` keys.
+int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes);
 
 }  // namespace mha

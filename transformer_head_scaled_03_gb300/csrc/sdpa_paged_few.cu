@@ -17,7 +17,7 @@
 // sums.
 //
 // At 16 slots a byte of the cache meets at most 16 flops: bound by HBM, so
-// the pipeline is sized for bytes in flight (three stages of 64 KB per SM).
+// the pipeline is sized for bytes in flight (two CTAs of 96 KB per SM).
 #include <math.h>
 #include <stdint.h>
 
@@ -43,48 +43,50 @@ template <int D>
 struct FewCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int KB = D / 64;
-  // d = 128: three 64 KB stages, one CTA per SM; d = 64: three 32 KB stages,
-  // two CTAs per SM
-  static constexpr int NST = 3;
-  static constexpr int kCtasPerSm = D == 128 ? 1 : 2;
+  // Two CTAs share an SM: one's set-up, first loads and merge run under the
+  // other's stream.  K and V tiles go through one ring in the order in which
+  // the products take them (K0 K1 V0 K2 V1 K3 ...), so that three 32 KB slots
+  // (d = 128; five of 16 KB at d = 64) are all under way or in use.
+  static constexpr int NR = D == 128 ? 3 : 5;
   static constexpr int kTile = KB * kSub;
-  // V before K: the M = 128 operand of a d = 64 product reads the 16 KB after
-  // a V tile as its unused upper half
-  static constexpr int kOffV = 0;
-  static constexpr int kOffK = kOffV + NST * kTile;
-  static constexpr int kOffQ = kOffK + NST * kTile;
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffQ = kOffRing + NR * kTile;
   static constexpr int kOffP = kOffQ + KB * kQBox;
   static constexpr int kOffRed = kOffP + 2 * kPBuf;  // [3][4 warps][16] f32
-  // the merge's m[16], l[16], o[16][D] and the weights [16 splits][16]: in
-  // the P^T buffers where they fit, which are free by then
+  // the merge's m[16], l[16], o[16][D] and the weights [16 splits][16], in
+  // the first slot: written once every product has completed
+  static constexpr int kOffX = kOffRing;
   static constexpr int kXBytes = (2 * kSlots + kSlots * D + kPagedMaxSplits * kSlots) * 4;
-  static constexpr bool kXInP = kXBytes <= 2 * kPBuf;
-  static constexpr int kOffX = kXInP ? kOffP : kOffRed + 3 * 4 * kSlots * 4;
-  static constexpr int kOffBar = kXInP ? kOffRed + 3 * 4 * kSlots * 4 : kOffX + kXBytes;
+  static_assert(kXBytes <= kTile, "the merge fits a stage");
+  static constexpr int kOffBar = kOffRed + 3 * 4 * kSlots * 4;
   static constexpr int bQ = 0;
-  __host__ __device__ static constexpr int bKF(int s) { return 1 + s; }
-  __host__ __device__ static constexpr int bKE(int s) { return 1 + NST + s; }
-  __host__ __device__ static constexpr int bVF(int s) { return 1 + 2 * NST + s; }
-  __host__ __device__ static constexpr int bVE(int s) { return 1 + 3 * NST + s; }
-  __host__ __device__ static constexpr int bS(int i) { return 1 + 4 * NST + i; }
-  __host__ __device__ static constexpr int bP(int i) { return 3 + 4 * NST + i; }
-  __host__ __device__ static constexpr int bO(int i) { return 5 + 4 * NST + i; }
-  __host__ __device__ static constexpr int bRed(int i) { return 7 + 4 * NST + i; }
-  static constexpr int bDrain = 9 + 4 * NST;
+  __host__ __device__ static constexpr int bF(int s) { return 1 + s; }
+  __host__ __device__ static constexpr int bE(int s) { return 1 + NR + s; }
+  __host__ __device__ static constexpr int bS(int i) { return 1 + 2 * NR + i; }
+  __host__ __device__ static constexpr int bP(int i) { return bS(0) + 2 + i; }
+  __host__ __device__ static constexpr int bO(int i) { return bS(0) + 4 + i; }
+  __host__ __device__ static constexpr int bRed(int i) { return bS(0) + 6 + i; }
+  static constexpr int bDrain = 1 + 2 * NR + 8;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
+  // the M = 128 operand of a d = 64 product reads the 16 KB after a V tile as
+  // its unused upper half: there is that much after the last slot
+  static constexpr int kEnd = kOffMisc + 16 > kOffQ + kSub ? kOffMisc + 16 : kOffQ + kSub;
+  static constexpr int kSmemBytes = kEnd + 1024;  // + alignment slack
   static_assert(kOffP % 1024 == 0, "P^T swizzle atoms must be 1024-byte aligned");
-  static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(kCtasPerSm == 1 || kSmemBytes + 1024 <= 114 * 1024, "two CTAs per SM");
+  static_assert(kSmemBytes + 1024 <= 114 * 1024, "two CTAs per SM");
 };
+
+// Places of K(j) and V(j) in the ring's order, for T tiles.
+__device__ __forceinline__ int place_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int place_of_v(int j, int T) { return j + 1 < T ? 2 * j + 2 : 2 * j + 1; }
 
 __device__ __forceinline__ void softmax_bar() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, 2)
     sdpa_paged_few_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
@@ -104,11 +106,9 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::bQ), 1);
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar(C::bKF(s)), 1);
-      mbar_init(bar(C::bKE(s)), 1);
-      mbar_init(bar(C::bVF(s)), 1);
-      mbar_init(bar(C::bVE(s)), 1);
+    for (int s = 0; s < C::NR; ++s) {
+      mbar_init(bar(C::bF(s)), 1);
+      mbar_init(bar(C::bE(s)), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::bS(i)), 1);
@@ -130,11 +130,6 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-
   float* red = reinterpret_cast<float*>(gbase + C::kOffRed);
   float* xm = reinterpret_cast<float*>(gbase + C::kOffX);
   float* xl = xm + kSlots;
@@ -149,15 +144,29 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
   const int slot = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.splits));
   const int g = slot % p.kv_heads;
   int b = slot / p.kv_heads;
-  if (p.B > 1 && p.B <= kMaxSortedBatch) {
-    int* lens_s = reinterpret_cast<int*>(xo);  // free until the merge
-    int* pick = reinterpret_cast<int*>(xm);
-    for (int i = threadIdx.x; i < p.B; i += kThreads) lens_s[i] = __ldg(p.kv_len + i);
-    __syncthreads();
+  const bool sorted = p.B > 1 && p.B <= kMaxSortedBatch;
+  int* lens_s = reinterpret_cast<int*>(gbase + C::kOffX);  // no copy is under way yet
+  int* off_s = lens_s + kMaxSortedBatch;
+  int* pick = off_s + kMaxSortedBatch + 1;
+  PagedSeq seq{};
+  if (sorted) {
+    for (int i = threadIdx.x; i <= p.B; i += kThreads) {
+      off_s[i] = __ldg(p.q_offsets + i);
+      if (i < p.B) lens_s[i] = __ldg(p.kv_len + i);
+    }
+  } else {
+    seq = paged_seq(p, b);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  if (sorted) {
     const int want = b;
     for (int c = threadIdx.x; c < p.B; c += kThreads) {
       const int lc = lens_s[c];
       int rank = 0;
+#pragma unroll 8
       for (int o = 0; o < p.B; ++o) {
         const int lo = lens_s[o];
         rank += (lo > lc || (lo == lc && o < c)) ? 1 : 0;
@@ -166,9 +175,10 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
     }
     __syncthreads();
     b = *pick;
-    __syncthreads();  // xm is written again only after the main loop
+    seq = paged_seq_of(p, off_s[b], off_s[b + 1], lens_s[b]);
+    fence_proxy_async_smem();  // the copies that follow write there
+    __syncthreads();
   }
-  const PagedSeq seq = paged_seq(p, b);
   const int rows = seq.n * p.G;  // query slots in use: slot = token * G + head of the group
   const int len = seq.len;
   const int n_tiles = seq.bad_len || rows == 0 ? 0 : (len + kKeys - 1) / kKeys;
@@ -189,37 +199,39 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
       }
       PageBoxes<kKeys, C::KB> cur, nxt;
       cur.fetch(p, b, t_begin * kKeys, len, lane);
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < T; ++j) {
-        const int st = j % C::NST;
-        const uint32_t ph = (j / C::NST) & 1;
-        const int key0 = (t_begin + j) * kKeys;
-        // the next tile's page numbers arrive while this one waits for room
-        if (j + 1 < T) nxt.fetch(p, b, key0 + kKeys, len, lane);
+      int issued = 0;
+      // the box of every lane into the ring's next slot; false: gave up
+      auto load = [&](const PageBoxes<kKeys, C::KB>& boxes, const CUtensorMap* map, int key0) {
+        const int s = issued % C::NR;
+        const uint32_t bytes = boxes.bytes(p);
+        if (!mbar_wait_warp(bar(C::bE(s)), ((issued / C::NR) & 1) ^ 1u, ctl)) return false;
+        if (lane == 0) mbar_expect_tx(bar(C::bF(s)), bytes);
+        __syncwarp();
+        boxes.load(p, map, base + C::kOffRing + s * C::kTile, bar(C::bF(s)), key0, g, lane);
+        ++issued;
+        return true;
+      };
+      const int first = t_begin * kKeys;
+      bool ok = load(cur, &tmK, first);
+      for (int j = 0; ok && j < T; ++j) {
         if (cur.bad) {
           *bad_page = 1;
           atomicOr(p.err, kErrPages);
         }
-        const uint32_t bytes = cur.bytes(p);
-        if (!mbar_wait_warp(bar(C::bKE(st)), ph ^ 1u, ctl)) break;
-        if (lane == 0) mbar_expect_tx(bar(C::bKF(st)), bytes);
-        __syncwarp();
-        cur.load(p, &tmK, base + C::kOffK + st * C::kTile, bar(C::bKF(st)), key0, g, lane);
-        k_issued = j + 1;
-        if (!mbar_wait_warp(bar(C::bVE(st)), ph ^ 1u, ctl)) break;
-        if (lane == 0) mbar_expect_tx(bar(C::bVF(st)), bytes);
-        __syncwarp();
-        cur.load(p, &tmV, base + C::kOffV + st * C::kTile, bar(C::bVF(st)), key0, g, lane);
-        v_issued = j + 1;
+        // the next tile's keys go before this tile's values
+        const int key0 = first + j * kKeys;
+        if (j + 1 < T) {
+          nxt.fetch(p, b, key0 + kKeys, len, lane);
+          if (!(ok = load(nxt, &tmK, key0 + kKeys))) break;
+        }
+        ok = load(cur, &tmV, key0);
         cur = nxt;
       }
       // let every issued copy land before the CTA can exit
       if (lane == 0) {
         paged_wait_drain(bar(C::bQ), 0, p.limit_ns);
-        for (int j = max(0, k_issued - C::NST); j < k_issued; ++j)
-          paged_wait_drain(bar(C::bKF(j % C::NST)), (j / C::NST) & 1, p.limit_ns);
-        for (int j = max(0, v_issued - C::NST); j < v_issued; ++j)
-          paged_wait_drain(bar(C::bVF(j % C::NST)), (j / C::NST) & 1, p.limit_ns);
+        for (int x = max(0, issued - C::NR); x < issued; ++x)
+          paged_wait_drain(bar(C::bF(x % C::NR)), (x / C::NR) & 1, p.limit_ns);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -230,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
       constexpr uint32_t kIdS = idesc_bf16_f32(kKeys, kSlots, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, kSlots, true, false);
       const uint64_t q_desc = sdesc_sw128(base + C::kOffQ, 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(base + C::kOffK, 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(base + C::kOffV, kSub, 1024);
+      const uint64_t k_desc = sdesc_sw128(base + C::kOffRing, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + C::kOffRing, kSub, 1024);
       const uint64_t p_desc = sdesc_sw128(base + C::kOffP, 16, 1024);
       auto issue_s = [&](int st, int buf) {
         const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::kTile) >> 4);
@@ -253,31 +265,34 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
                   ks > 0 ? 1u : 0u);
         }
       };
+      auto wait_full = [&](int x) {
+        return mbar_wait(bar(C::bF(x % C::NR)), (x / C::NR) & 1, ctl);
+      };
       bool ok = mbar_wait(bar(C::bQ), 0, ctl);
       for (int j = 0; ok && j < 2 && j < T; ++j) {
-        const int st = j % C::NST;
-        if (!(ok = mbar_wait(bar(C::bKF(st)), (j / C::NST) & 1, ctl))) break;
+        const int x = place_of_k(j);
+        if (!(ok = wait_full(x))) break;
         tc_fence_after();
-        issue_s(st, j);
+        issue_s(x % C::NR, j);
         umma_commit(bar(C::bS(j)));
-        umma_commit(bar(C::bKE(st)));
+        umma_commit(bar(C::bE(x % C::NR)));
       }
       for (int j = 0; ok && j < T; ++j) {
-        const int st = j % C::NST;
+        const int x = place_of_v(j, T);
         const int buf = j & 1;
         if (!(ok = mbar_wait(bar(C::bP(buf)), (j >> 1) & 1, ctl))) break;
-        if (!(ok = mbar_wait(bar(C::bVF(st)), (j / C::NST) & 1, ctl))) break;
+        if (!(ok = wait_full(x))) break;
         tc_fence_after();
-        issue_o(st, buf);
+        issue_o(x % C::NR, buf);
         umma_commit(bar(C::bO(buf)));
-        umma_commit(bar(C::bVE(st)));
+        umma_commit(bar(C::bE(x % C::NR)));
         if (j + 2 < T) {
-          const int st2 = (j + 2) % C::NST;
-          if (!(ok = mbar_wait(bar(C::bKF(st2)), ((j + 2) / C::NST) & 1, ctl))) break;
+          const int y = place_of_k(j + 2);
+          if (!(ok = wait_full(y))) break;
           tc_fence_after();
-          issue_s(st2, buf);
+          issue_s(y % C::NR, buf);
           umma_commit(bar(C::bS(buf)));
-          umma_commit(bar(C::bKE(st2)));
+          umma_commit(bar(C::bE(y % C::NR)));
         }
       }
       // every issued MMA completes before tensor memory is released
@@ -371,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
       if ((t_begin + j + 1) * kKeys > len) {
         // V rows behind the length: zero them once the tile has landed (it
         // stays until this tile's product, which waits for the arrive below)
-        const int st = j % C::NST;
-        if (!(ok = mbar_wait_warp(bar(C::bVF(st)), (j / C::NST) & 1, ctl))) break;
+        const int x = place_of_v(j, T);
+        if (!(ok = mbar_wait_warp(bar(C::bF(x % C::NR)), (x / C::NR) & 1, ctl))) break;
         if (key >= len) {
-          uint8_t* v_row = gbase + C::kOffV + st * C::kTile + r * 128;
+          uint8_t* v_row = gbase + C::kOffRing + x % C::NR * C::kTile + r * 128;
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
@@ -485,21 +500,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D>::kCtasPerSm)
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += 128) {
       const int q = e / (D / 4);
       const int c = (e - q * (D / 4)) * 4;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int s = 0; s < S; ++s) {
-        const float w = xw[s * kSlots + q];
-        const float4 v = ld_cluster_f32x4(
-            cluster_map(xo_s + 4u * (q * D + c), static_cast<uint32_t>(s)));
-        // a weight of 0 stands for nothing seen, and for rows to be zeroed,
-        // whose partial output may be anything
-        if (w != 0.f) {
-          o.x = fmaf(w, v.x, o.x);
-          o.y = fmaf(w, v.y, o.y);
-          o.z = fmaf(w, v.z, o.z);
-          o.w = fmaf(w, v.w, o.w);
-        }
-      }
+      const float4 o = merge_splits(xo_s + 4u * (q * D + c), xw + q, kSlots, S);
       const int i = q / p.G;
       const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
       store_out4(p, row * D + c, o);
@@ -521,9 +522,7 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
   const int64_t clusters = static_cast<int64_t>(a.pages.B) * a.pages.kv_heads;
   if (a.splits == 0)
     a.splits = paged_default_splits(
-        clusters, static_cast<int>(((static_cast<int64_t>(a.pages.cols) << a.pages.page_shift) +
-                                    kKeys - 1) / kKeys),
-        kThreads, C::kSmemBytes);
+        clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads, C::kSmemBytes);
   if (clusters * a.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = sdpa_paged_few_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -10,9 +10,9 @@
 //   P_t  = 2^(S_t*c - m*c)     softmax warps, thread r owns query row r; P in
 //                              bf16 over S's columns
 //   O_t += P_t V_j             tcgen05.mma, A = P_t from TMEM
-// CTAs take NQT tiles, which share the key tiles; or, when there are few
-// tiles, one tile and a share of its keys, merged exactly through a
-// thread-block cluster (o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s).
+// A CTA takes NQT tiles, which share the key tiles, and, when there are few
+// CTAs, only a share of the keys: the CTAs of a thread-block cluster split
+// them and merge exactly (o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s).
 //
 // The rows of the last page behind the sequence's length hold anything, NaN
 // too: their scores are replaced, and their V rows zeroed in shared memory
@@ -29,14 +29,14 @@ namespace {
 
 constexpr int kBlockM = 128;    // query rows per tile = TMEM lanes
 constexpr int kSub = 128 * 128;  // bytes of a 128-row x 64-column bf16 block
+constexpr int kMaxSorted = 256;  // sequences that a CTA ranks by length
 
 // BN = keys per K/V tile (128, or 64 to fit two CTAs of two d = 64 tiles in
-// tensor memory).  kSplit: one tile per CTA, keys shared by a cluster.
+// tensor memory).
 template <int D, int NQT, int NST, int BN>
 struct RowsCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static_assert(BN == 64 || BN == 128, "key tile");
-  static constexpr bool kSplit = NQT == 1;
   static constexpr int KB = D / 64;
   static constexpr int kQTileBytes = KB * kSub;
   static constexpr int kKVBlock = BN * 128;
@@ -48,7 +48,9 @@ struct RowsCfg {
   static constexpr int kTmemNeed = NQT * (BN + D);
   static constexpr uint32_t kTmemCols = kTmemNeed <= 128 ? 128u : kTmemNeed <= 256 ? 256u : 512u;
   static_assert(kTmemNeed <= 512, "TMEM budget");
-  static constexpr int kMinBlocks = D == 64 ? 2 : 1;
+  // two CTAs per SM where tensor memory and shared memory allow: one's set-up
+  // and merge run under the other's products
+  static constexpr int kMinBlocks = D == 64 || NQT == 1 ? 2 : 1;
   __host__ __device__ static constexpr uint32_t tS(int t) { return static_cast<uint32_t>(t * BN); }
   __host__ __device__ static constexpr uint32_t tO(int t) { return static_cast<uint32_t>(NQT * BN + t * D); }
   static constexpr int bQ = 0;
@@ -65,18 +67,18 @@ struct RowsCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + NQT * kQTileBytes;
   static constexpr int kOffV = kOffK + NST * kKVTileBytes;
-  // the merge's partial outputs [128][D + 4] f32, over Q and the key/value
+  // the merge's partial outputs [NQT * 128][D + 4] f32, over Q and the key/value
   // stages once every product has completed (rows 16 bytes apart modulo 128:
   // no bank conflicts)
   static constexpr int kXRow = D + 4;
-  static constexpr int kXBytes = kBlockM * kXRow * 4;
+  static constexpr int kXBytes = NQT * kBlockM * kXRow * 4;
   static constexpr int kOffBar = kOffV + NST * kKVTileBytes;
-  static_assert(!kSplit || kXBytes <= kOffBar, "the merge fits the stages");
+  static_assert(kXBytes <= kOffBar, "the merge fits the stages");
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kOffM = kOffMisc + 32;               // m[128], l[128] f32
-  static constexpr int kOffW = kOffM + (kSplit ? 2 * kBlockM * 4 : 0);
+  static constexpr int kOffM = kOffMisc + 32;  // m, l of every row, f32
+  static constexpr int kOffW = kOffM + 2 * NQT * kBlockM * 4;
   // the weights of this CTA's share of the rows, for every split
-  static constexpr int kWBytes = kSplit ? (kBlockM + kPagedMaxSplits) * 4 : 0;
+  static constexpr int kWBytes = (NQT * kBlockM + kPagedMaxSplits) * 4;
   static constexpr int kSmemBytes = kOffW + kWBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -133,16 +135,47 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     tma_prefetch_desc(&tmV);
   }
   // ---- which (sequence, kv head, block of tokens) this CTA computes: blocks
-  // are numbered sequence by sequence, in it head by head (a head's blocks
-  // run at about the same time and share its pages in L2), and in a head
-  // from the last tokens to the first, which see fewer keys.
-  const int split = C::kSplit ? static_cast<int>(blockIdx.x % static_cast<unsigned>(p.splits)) : 0;
+  // are numbered sequence by sequence, longest first (CTAs start in grid
+  // order, so long ones do not trail alone at the end; up to kMaxSorted
+  // sequences, ranked by every CTA itself); in a sequence head by head (a
+  // head's blocks run at about the same time and share its pages in L2), in a
+  // head from the last tokens to the first, which see fewer keys.
+  int* lens_s = reinterpret_cast<int*>(gbase);  // Q's place, before it is loaded
+  int* off_s = lens_s + kMaxSorted;
+  int* order_s = off_s + kMaxSorted + 1;
+  const bool sorted = p.B > 1 && p.B <= kMaxSorted;
+  if (sorted) {
+    for (int i = threadIdx.x; i <= p.B; i += C::kThreads) {
+      off_s[i] = __ldg(p.q_offsets + i);
+      if (i < p.B) lens_s[i] = __ldg(p.kv_len + i);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.B; c += C::kThreads) {
+      const int lc = lens_s[c];
+      int rank = 0;
+#pragma unroll 8
+      for (int o = 0; o < p.B; ++o) {
+        const int lo = lens_s[o];
+        rank += (lo > lc || (lo == lc && o < c)) ? 1 : 0;
+      }
+      order_s[rank] = c;
+    }
+    __syncthreads();
+  }
+  auto seq_of = [&](int i) {
+    return sorted ? paged_seq_of(p, off_s[i], off_s[i + 1], lens_s[i]) : paged_seq(p, i);
+  };
+  const int split = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.splits));
   if (warp == 0) {
-    int64_t rest = C::kSplit ? blockIdx.x / static_cast<unsigned>(p.splits) : blockIdx.x;
+    int64_t rest = blockIdx.x / static_cast<unsigned>(p.splits);
     int found = -1, head = 0, blk = 0;
     for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
+      int seq_b = b0 + lane;
       int n = 0;
-      if (b0 + lane < p.B) n = paged_seq(p, b0 + lane).n;
+      if (seq_b < p.B) {
+        if (sorted) seq_b = order_s[seq_b];
+        n = seq_of(seq_b).n;
+      }
       const int blocks = (n + block_tokens - 1) / block_tokens;
       const int64_t mine = static_cast<int64_t>(blocks) * p.kv_heads;
       int64_t incl = mine;
@@ -156,7 +189,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         const int src = __ffs(in) - 1;
         const int64_t off = __shfl_sync(0xffffffffu, rest - (incl - mine), src);
         const int nb = __shfl_sync(0xffffffffu, blocks, src);
-        found = b0 + src;
+        found = __shfl_sync(0xffffffffu, seq_b, src);
         head = static_cast<int>(off / nb);
         blk = nb - 1 - static_cast<int>(off - static_cast<int64_t>(head) * nb);
       } else {
@@ -166,7 +199,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     // the first CTA reports bad offsets and lengths, for all sequences
     if (blockIdx.x == 0) {
       for (int b = lane; b < p.B; b += 32) {
-        const PagedSeq s = paged_seq(p, b);
+        const PagedSeq s = seq_of(b);
         if (s.bad_offsets || s.bad_len) atomicOr(p.err, kErrPages);
       }
     }
@@ -184,7 +217,11 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
   const int g = pick[1];
   const int i0 = pick[2] * block_tokens;  // the block's first token of the sequence
   PagedSeq seq{};
-  if (b >= 0) seq = paged_seq(p, b);
+  if (b >= 0) seq = seq_of(b);
+  if (sorted) {
+    fence_proxy_async_smem();  // the copies that follow write over the sequences
+    __syncthreads();
+  }
   const int len = seq.len;
   // key tiles that query tile t needs: up to its last token's own key
   auto tiles_of = [&](int t) -> int {
@@ -194,17 +231,13 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         p.causal ? len - seq.n + min(seq.n, i + tile_tokens) : len;
     return (stop + BN - 1) / BN;
   };
-  // this CTA walks the key tiles [j0, j0 + count_of(t))
-  int j0 = 0;
-  if constexpr (C::kSplit)
-    j0 = static_cast<int>(static_cast<long long>(tiles_of(0)) * split / p.splits);
-  auto count_of = [&](int t) -> int {
-    if constexpr (C::kSplit)
-      return static_cast<int>(static_cast<long long>(tiles_of(0)) * (split + 1) / p.splits) - j0;
-    return tiles_of(t);
-  };
-  int n_kv = 0;
-  for (int t = 0; t < NQT; ++t) n_kv = max(n_kv, count_of(t));
+  // this CTA walks the key tiles [j0, j1), query tile t as far as it needs them
+  int n_all = 0;
+  for (int t = 0; t < NQT; ++t) n_all = max(n_all, tiles_of(t));
+  const int j0 = static_cast<int>(static_cast<int64_t>(n_all) * split / p.splits);
+  const int j1 = static_cast<int>(static_cast<int64_t>(n_all) * (split + 1) / p.splits);
+  const int n_kv = j1 - j0;
+  auto count_of = [&](int t) -> int { return max(0, min(tiles_of(t), j1) - j0); };
 
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ producer
@@ -462,12 +495,16 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
       if (!mbar_wait_warp(bar(C::bLoaded), 0, ctl)) zero = true;
       if (*bad_page) zero = true;
     }
-    if constexpr (C::kSplit) {
-      float* xo = reinterpret_cast<float*>(gbase) + r * C::kXRow;
+    if (p.splits > 1) {
+      // the partial outputs go where Q and the stages were: not before every
+      // product of the CTA has read them
+      for (int o = 0; o < NQT; ++o)
+        if (o != t && count_of(o) > 0) ok = mbar_wait_warp(bar(C::bO(o)), 0, ctl) && ok;
+      float* xo = reinterpret_cast<float*>(gbase) + (t * kBlockM + r) * C::kXRow;
       float* xm = reinterpret_cast<float*>(gbase + C::kOffM);
       if (!ok || (n_t > 0 && !have)) *bad_page = 1;  // a failed split spoils the row
-      xm[r] = have ? (m_ref == -INFINITY ? -INFINITY : m_ref * sl2) : -INFINITY;
-      xm[kBlockM + r] = have ? l : 0.f;
+      xm[t * kBlockM + r] = have && m_ref != -INFINITY ? m_ref * sl2 : -INFINITY;
+      xm[(NQT + t) * kBlockM + r] = have ? l : 0.f;
       if (have && warp_in_use) {
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -525,14 +562,16 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     }
   }
 
-  if constexpr (C::kSplit) {
+  if (p.splits > 1) {
     // ---- merge the splits: every CTA of the cluster takes a share of the
     // rows, its first threads one row's weights each, then all of its softmax
     // threads four columns at a time.
     __syncwarp();
     cluster_sync();  // every split's m, l, O and bad-page flag are in its shared memory
     const int S = p.splits;
-    const int rows = min(tile_tokens, max(0, seq.n - i0)) * p.G;
+    const int tile_rows = tile_tokens * p.G;  // those of a full tile
+    const int rows = min(block_tokens, max(0, seq.n - i0)) * p.G;
+    auto smem_row = [&](int row) { return row + (row / tile_rows) * (kBlockM - tile_rows); };
     const int per = (rows + S - 1) / S;
     const int r0 = split * per;
     const int mine = max(0, min(rows, r0 + per) - r0);
@@ -540,7 +579,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     const uint32_t xo_s = base, xm_s = base + C::kOffM;
     const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
     if (static_cast<int>(threadIdx.x) < mine) {
-      const int row = r0 + threadIdx.x;
+      const int row = smem_row(r0 + threadIdx.x);
       float ms[kPagedMaxSplits], ls[kPagedMaxSplits], M = -INFINITY, den = 0.f;
       bool bad = false;
 #pragma unroll
@@ -548,7 +587,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         if (s < S) {
           const uint32_t rk = static_cast<uint32_t>(s);
           ms[s] = ld_cluster_f32(cluster_map(xm_s + 4u * row, rk));
-          ls[s] = ld_cluster_f32(cluster_map(xm_s + 4u * (kBlockM + row), rk));
+          ls[s] = ld_cluster_f32(cluster_map(xm_s + 4u * (NQT * kBlockM + row), rk));
           bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_s, rk))) != 0u;
         }
 #pragma unroll
@@ -566,24 +605,12 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         if (s < S) weights[threadIdx.x * S + s] = none ? 0.f : ms[s] / den;
     }
     __syncthreads();
+#pragma unroll 2
     for (int e = threadIdx.x; e < mine * (D / 4); e += C::kThreads) {
       const int row = e / (D / 4);
       const int c = (e - row * (D / 4)) * 4;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int s = 0; s < S; ++s) {
-        const float w = weights[row * S + s];
-        const float4 v = ld_cluster_f32x4(
-            cluster_map(xo_s + 4u * ((r0 + row) * C::kXRow + c), static_cast<uint32_t>(s)));
-        // a weight of 0 stands for nothing seen, and for rows to be zeroed,
-        // whose partial output may be anything
-        if (w != 0.f) {
-          o.x = fmaf(w, v.x, o.x);
-          o.y = fmaf(w, v.y, o.y);
-          o.z = fmaf(w, v.z, o.z);
-          o.w = fmaf(w, v.w, o.w);
-        }
-      }
+      const float4 o = merge_splits(xo_s + 4u * (smem_row(r0 + row) * C::kXRow + c),
+                                    weights + row * S, 1, S);
       const int i = (r0 + row) / p.G;
       const int64_t at =
           (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D + c;
@@ -598,10 +625,14 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
   if (warp == C::kMmaWarp) tmem_dealloc<C::kTmemCols>(tmem);
 }
 
-// Blocks that T packed tokens of B sequences can make, for every kv head.
+// Blocks that T packed tokens of B sequences, max_new each, can make, for
+// every kv head: a block per block_tokens tokens and a partial one per
+// sequence, and no more than each sequence can have.
 int64_t block_bound(const PagedSdpaArgs& a, int block_tokens) {
-  return (a.T / block_tokens + static_cast<int64_t>(a.T < a.pages.B ? a.T : a.pages.B)) *
-         a.pages.kv_heads;
+  const int64_t seqs = a.T < a.pages.B ? a.T : a.pages.B;
+  const int64_t each = (a.max_new + block_tokens - 1) / block_tokens;
+  const int64_t packed = a.T / block_tokens + seqs;
+  return (seqs * each < packed ? seqs * each : packed) * a.pages.kv_heads;
 }
 
 template <int D, int NQT, int NST, int BN>
@@ -610,18 +641,16 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
   CUtensorMap q, k, v;
   if (!paged_tensor_maps(a, D, kBlockM / a.G, BN, &q, &k, &v)) return cudaErrorInvalidValue;
   const int64_t blocks = block_bound(a, NQT * (kBlockM / a.G));
-  if constexpr (!C::kSplit) {
-    a.splits = 1;
-  } else if (a.splits == 0) {
+  if (a.splits == 0)
     a.splits = paged_default_splits(
-        blocks, static_cast<int>(((static_cast<int64_t>(a.pages.cols) << a.pages.page_shift) +
-                                  BN - 1) / BN),
-        C::kThreads, C::kSmemBytes);
-  }
+        blocks, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, C::kThreads, C::kSmemBytes);
   if (blocks * a.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = sdpa_paged_rows_kernel<D, NQT, NST, BN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess && a.splits > 8)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -641,25 +670,16 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-int num_sms() {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-    return v;
-  return 1;
-}
-
 }  // namespace
 
 cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
   // Two query tiles per CTA halve the key/value traffic per row and keep the
-  // tensor core busy during one tile's softmax: taken when they make a CTA
-  // for every SM.  Fewer tiles run one per CTA with their keys split.
-  const bool two = a.splits <= 1 && a.max_new > kBlockM / a.G &&
-                   block_bound(a, 2 * (kBlockM / a.G)) >= num_sms();
+  // tensor core busy during one tile's softmax: taken when a sequence can
+  // have two tiles of new tokens.
+  const bool two = a.max_new > kBlockM / a.G;
   if (a.pages.d == 64)
     return two ? launch_impl<64, 2, 3, 64>(a, ctl) : launch_impl<64, 1, 2, 128>(a, ctl);
-  return two ? launch_impl<128, 2, 2, 128>(a, ctl) : launch_impl<128, 1, 3, 128>(a, ctl);
+  return two ? launch_impl<128, 2, 2, 128>(a, ctl) : launch_impl<128, 1, 1, 128>(a, ctl);
 }
 
 }  // namespace mha
