@@ -99,11 +99,10 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
 // lane = page of the tile * KB + 64-column block.
 template <int ROWS, int KB>
 struct PageBoxes {
-  int page;      // this lane's page number (any value where !mine)
-  bool mine;     // this lane loads a box
-  bool bad;      // ... but its page number is out of range
+  int page;   // this lane's page number
+  bool mine;  // this lane has a box of the tile
 
-  // Read the page number of the tile that starts at key `key0`.
+  // Request the page number of the tile that starts at key `key0`.
   __device__ __forceinline__ void fetch(const PagedParams& p, int b, int key0, int len, int lane) {
     const int slot = lane / KB;
     const int in_tile = ROWS >> p.page_shift;  // 0: the tile is part of a page
@@ -112,18 +111,22 @@ struct PageBoxes {
            (static_cast<int64_t>(entry) << p.page_shift) < len;
     page = 0;
     if (mine) page = __ldg(p.table + static_cast<int64_t>(b) * p.cols + entry);
-    bad = mine && (page < 0 || page >= p.num_pages);
-    if (bad) mine = false;
   }
+  __device__ __forceinline__ bool in_range(const PagedParams& p) const {
+    return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+  }
+  // The box is to be loaded, or its page number is out of range.
+  __device__ __forceinline__ bool good(const PagedParams& p) const { return mine && in_range(p); }
+  __device__ __forceinline__ bool bad(const PagedParams& p) const { return mine && !in_range(p); }
   // Bytes that the warp's boxes bring (warp-collective).
   __device__ __forceinline__ uint32_t bytes(const PagedParams& p) const {
     const uint32_t rows = min(ROWS, 1 << p.page_shift);
-    return __popc(__ballot_sync(0xffffffffu, mine)) * rows * 128u;
+    return __popc(__ballot_sync(0xffffffffu, good(p))) * rows * 128u;
   }
   // Load this lane's box of head g into the tile at `dst` ([KB][ROWS][128 B]).
   __device__ __forceinline__ void load(const PagedParams& p, const CUtensorMap* map, uint32_t dst,
                                        uint32_t bar, int key0, int g, int lane) const {
-    if (!mine) return;
+    if (!good(p)) return;
     const int slot = lane / KB, kb = lane % KB;
     const int row = (key0 & ((1 << p.page_shift) - 1)) + (g << p.page_shift);
     tma_load_3d(dst + kb * (ROWS * 128) + (slot << p.page_shift) * 128, map, bar, kb * 64, row,
@@ -150,34 +153,39 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
   return v;
 }
 
-// Four columns of the merged output: sum over the cluster's splits of weight
-// times partial output (at the same shared address in every split).  All
-// loads are requested before the first is used.  A weight of 0 stands for
-// nothing seen, and for rows to be zeroed, whose partial output may be
-// anything.
-__device__ __forceinline__ float4 merge_splits(uint32_t from, const float* weight, int stride,
-                                               int splits) {
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+// Merged outputs of N places, four columns each: sum over the cluster's splits
+// of weight times partial output (at the same shared address in every split),
+// the loads of U splits at a time under way together: a remote load takes
+// about a thousand clocks.  A weight of 0 stands for nothing seen, and for
+// rows to be zeroed, whose partial output may be anything.
+template <int N, int U>
+__device__ __forceinline__ void merge_splits(const uint32_t (&from)[N],
+                                             const float* const (&weight)[N], int stride,
+                                             int splits, float4 (&o)[N]) {
 #pragma unroll
-  for (int s0 = 0; s0 < kPagedMaxSplits; s0 += 8) {
-    if (s0 >= splits) break;
-    float4 v[8];
+  for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < splits; s0 += U) {
+    float4 v[N][U];
 #pragma unroll
-    for (int s = 0; s < 8; ++s)
-      if (s0 + s < splits)
-        v[s] = ld_cluster_f32x4(cluster_map(from, static_cast<uint32_t>(s0 + s)));
+    for (int u = 0; u < U; ++u)
+      if (s0 + u < splits)
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const float w = s0 + s < splits ? weight[(s0 + s) * stride] : 0.f;
-      if (w != 0.f) {
-        o.x = fmaf(w, v[s].x, o.x);
-        o.y = fmaf(w, v[s].y, o.y);
-        o.z = fmaf(w, v[s].z, o.z);
-        o.w = fmaf(w, v[s].w, o.w);
-      }
-    }
+        for (int i = 0; i < N; ++i)
+          v[i][u] = ld_cluster_f32x4(cluster_map(from[i], static_cast<uint32_t>(s0 + u)));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s0 + u < splits)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float w = weight[i][(s0 + u) * stride];
+          if (w != 0.f) {
+            o[i].x = fmaf(w, v[i][u].x, o[i].x);
+            o[i].y = fmaf(w, v[i][u].y, o[i].y);
+            o[i].z = fmaf(w, v[i][u].z, o[i].z);
+            o[i].w = fmaf(w, v[i][u].w, o[i].w);
+          }
+        }
   }
-  return o;
 }
 
 // Bounded wait that ignores the abort flag (copies and products in flight).

@@ -69,9 +69,13 @@ struct FewCfg {
   static constexpr int bDrain = 1 + 2 * NR + 8;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  // lengths and offsets of the sequences, while they are ranked
+  static constexpr int kOffSeq = kOffMisc + 16;
+  static constexpr int kSeqBytes = (2 * kMaxSortedBatch + 2) * 4;
   // the M = 128 operand of a d = 64 product reads the 16 KB after a V tile as
   // its unused upper half: there is that much after the last slot
-  static constexpr int kEnd = kOffMisc + 16 > kOffQ + kSub ? kOffMisc + 16 : kOffQ + kSub;
+  static constexpr int kEnd =
+      kOffSeq + kSeqBytes > kOffQ + kSub ? kOffSeq + kSeqBytes : kOffQ + kSub;
   static constexpr int kSmemBytes = kEnd + 1024;  // + alignment slack
   static_assert(kOffP % 1024 == 0, "P^T swizzle atoms must be 1024-byte aligned");
   static_assert(kSmemBytes + 1024 <= 114 * 1024, "two CTAs per SM");
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = slot % p.kv_heads;
   int b = slot / p.kv_heads;
   const bool sorted = p.B > 1 && p.B <= kMaxSortedBatch;
-  int* lens_s = reinterpret_cast<int*>(gbase + C::kOffX);  // no copy is under way yet
+  int* lens_s = reinterpret_cast<int*>(gbase + C::kOffSeq);
   int* off_s = lens_s + kMaxSortedBatch;
   int* pick = off_s + kMaxSortedBatch + 1;
   PagedSeq seq{};
@@ -176,8 +180,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     b = *pick;
     seq = paged_seq_of(p, off_s[b], off_s[b + 1], lens_s[b]);
-    fence_proxy_async_smem();  // the copies that follow write there
-    __syncthreads();
   }
   const int rows = seq.n * p.G;  // query slots in use: slot = token * G + head of the group
   const int len = seq.len;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int first = t_begin * kKeys;
       bool ok = load(cur, &tmK, first);
       for (int j = 0; ok && j < T; ++j) {
-        if (cur.bad) {
+        if (cur.bad(p)) {
           *bad_page = 1;
           atomicOr(p.err, kErrPages);
         }
@@ -499,11 +501,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int e1 = min(total, e0 + per);
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += 128) {
       const int q = e / (D / 4);
-      const int c = (e - q * (D / 4)) * 4;
-      const float4 o = merge_splits(xo_s + 4u * (q * D + c), xw + q, kSlots, S);
+      const uint32_t from[1] = {xo_s + 16u * e};  // slot * D + column
+      const float* const weight[1] = {xw + q};
+      float4 o[1];
+      merge_splits<1, 8>(from, weight, kSlots, S, o);
       const int i = q / p.G;
       const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
-      store_out4(p, row * D + c, o);
+      store_out4(p, row * D + (e - q * (D / 4)) * 4, o[0]);
     }
   }
   __syncwarp();

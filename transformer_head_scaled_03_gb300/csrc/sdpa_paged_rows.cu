@@ -20,6 +20,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "sdpa_paged.cuh"
@@ -256,9 +258,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         const int st = j % NST;
         const uint32_t ph = (j / NST) & 1;
         const int key0 = (j0 + j) * BN;
-        // the next tile's page numbers arrive while this one waits for room
-        if (j + 1 < n_kv) nxt.fetch(p, b, key0 + BN, len, lane);
-        if (cur.bad) {
+        if (cur.bad(p)) {
           *bad_page = 1;
           atomicOr(p.err, kErrPages);
         }
@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         __syncwarp();
         cur.load(p, &tmK, base + C::kOffK + st * C::kKVTileBytes, bar(C::bKF(st)), key0, g, lane);
         k_issued = j + 1;
+        if (j + 1 < n_kv) nxt.fetch(p, b, key0 + BN, len, lane);
         if (!mbar_wait_warp(bar(C::bVE(st)), ph ^ 1u, ctl)) break;
         if (lane == 0) mbar_expect_tx(bar(C::bVF(st)), bytes);
         __syncwarp();
@@ -519,44 +520,64 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
       }
     } else if (warp_in_use) {
       const float inv_l = !zero && l > 0.f ? 1.f / l : 0.f;
-      const int h = g * p.G + r % p.G;
-      const int64_t at = (static_cast<int64_t>(seq.q0 + i) * p.H + h) * D;
-#pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t o[32];
-        if (!zero) {
-          tmem_ld32(tO + cb * 32, o);
-          tmem_ld_wait(o);
-        } else {
+      const int rows_here = min(32, tile_rows - quarter * 32);
+      const int64_t row0 = static_cast<int64_t>(seq.q0 + i0 + t * tile_tokens) * p.H + g * p.G;
+      // where tile row x goes, in rows of the output
+      auto out_row = [&](int x) {
+        const int k = x / p.G;
+        return row0 + static_cast<int64_t>(k) * p.H + (x - k * p.G);
+      };
+      auto columns = [&](int cb, uint32_t (&o)[32]) {
+        if (zero) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
+          return;
         }
-        if (in_use) {
-          if (p.out_f32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + at + cb * 32);
+        tmem_ld32(tO + cb * 32, o);
+        tmem_ld_wait(o);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(__uint_as_float(o[4 * c]) * inv_l,
-                                   __uint_as_float(o[4 * c + 1]) * inv_l,
-                                   __uint_as_float(o[4 * c + 2]) * inv_l,
-                                   __uint_as_float(o[4 * c + 3]) * inv_l);
-          } else {
-            uint4* dst =
-                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + at + cb * 32);
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
+      };
+      if (p.out_f32) {
+        const int64_t at = out_row(in_use ? r : quarter * 32) * D;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 v;
-              v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * inv_l,
-                                __uint_as_float(o[8 * c + 1]) * inv_l);
-              v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * inv_l,
-                                __uint_as_float(o[8 * c + 3]) * inv_l);
-              v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * inv_l,
-                                __uint_as_float(o[8 * c + 5]) * inv_l);
-              v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * inv_l,
-                                __uint_as_float(o[8 * c + 7]) * inv_l);
-              dst[c] = v;
-            }
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          columns(cb, o);
+          if (!in_use) continue;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.O) + at + cb * 32);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      } else {
+        // bf16 rows go through this warp's part of the tile's Q block, which
+        // its products have read, so that a store writes whole rows: 16-byte
+        // piece c of row x at place c ^ (x & 7)
+        constexpr int kPieces = D / 8;
+        uint4* stg = reinterpret_cast<uint4*>(gbase + C::kOffQ + t * C::kQTileBytes) +
+                     quarter * 32 * kPieces;
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          columns(cb, o);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]), __uint_as_float(o[8 * c + 1]));
+            v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]), __uint_as_float(o[8 * c + 3]));
+            v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]), __uint_as_float(o[8 * c + 5]));
+            v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]), __uint_as_float(o[8 * c + 7]));
+            stg[lane * kPieces + ((cb * 4 + c) ^ (lane & 7))] = v;
           }
+        }
+        __syncwarp();
+        const int piece = lane % kPieces;
+#pragma unroll 4
+        for (int x = lane / kPieces; x < rows_here; x += 32 / kPieces) {
+          const uint4 v = stg[x * kPieces + (piece ^ (x & 7))];
+          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) +
+                                   out_row(quarter * 32 + x) * D)[piece] = v;
         }
       }
     }
@@ -605,17 +626,38 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         if (s < S) weights[threadIdx.x * S + s] = none ? 0.f : ms[s] / den;
     }
     __syncthreads();
-#pragma unroll 2
-    for (int e = threadIdx.x; e < mine * (D / 4); e += C::kThreads) {
-      const int row = e / (D / 4);
-      const int c = (e - row * (D / 4)) * 4;
-      const float4 o = merge_splits(xo_s + 4u * (smem_row(r0 + row) * C::kXRow + c),
-                                    weights + row * S, 1, S);
-      const int i = (r0 + row) / p.G;
-      const int64_t at =
-          (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D + c;
-      store_out4(p, at, o);
-    }
+    const int total = mine * (D / 4);
+    // N places a thread at a time: four while a CTA's share is many rows
+    auto merge = [&](auto n_const, auto u_const) {
+      constexpr int N = decltype(n_const)::value, U = decltype(u_const)::value;
+      for (int f0 = threadIdx.x; f0 < total; f0 += C::kThreads * N) {
+        uint32_t from[N];
+        const float* weight[N];
+        float4 o[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int e = min(f0 + C::kThreads * k, total - 1);
+          const int row = e / (D / 4);
+          from[k] = xo_s + 4u * (smem_row(r0 + row) * C::kXRow + (e - row * (D / 4)) * 4);
+          weight[k] = weights + row * S;
+        }
+        merge_splits<N, U>(from, weight, 1, S, o);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int e = f0 + C::kThreads * k;
+          if (e >= total) continue;
+          const int row = e / (D / 4);
+          const int i = (r0 + row) / p.G;
+          const int64_t at =
+              (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D;
+          store_out4(p, at + (e - row * (D / 4)) * 4, o[k]);
+        }
+      }
+    };
+    if (total >= 4 * C::kThreads)
+      merge(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    else
+      merge(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
     __syncwarp();
     cluster_sync();  // no CTA leaves while another still reads its shared memory
   }
