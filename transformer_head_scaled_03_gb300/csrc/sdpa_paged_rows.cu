@@ -721,7 +721,7 @@ cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl)
   const bool two = a.max_new > kBlockM / a.G;
   if (a.pages.d == 64)
     return two ? launch_impl<64, 2, 3, 64>(a, ctl) : launch_impl<64, 1, 2, 128>(a, ctl);
-  return two ? launch_impl<128, 2, 2, 128>(a, ctl) : launch_impl<128, 1, 1, 128>(a, ctl);
+  return two ? launch_impl<128, 2, 2, 128>(a, ctl) : launch_impl<128, 1, 2, 64>(a, ctl);
 }
 
 }  // namespace mha
