@@ -357,11 +357,12 @@ def _launch_on(stream, *tensors):
     """Check that every tensor is on the current device, where the library
     launches; the raw stream to launch on.  (The paged calls take tens of
     microseconds or less, so what the host does for each of them counts.)"""
-    if not all([t.is_cuda for t in tensors]):
+    if not tensors[0].is_cuda:
         raise ValueError("tensor must be on a CUDA device")
     here = torch._C._cuda_getDevice()
-    if any([t.get_device() != here for t in tensors]):
-        raise ValueError(f"tensors must be on the current device (cuda:{here})")
+    for t in tensors:
+        if t.get_device() != here:
+            raise ValueError(f"tensors must be on the current CUDA device (cuda:{here})")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(here)
     if stream.device_index != here:
@@ -448,7 +449,7 @@ def _token_rows(name, x, B, L, d, dtype):
     """Heads and token stride of rows [B, L, heads, d] whose tokens are evenly
     spaced (a dense tensor, or a slice of a projection's output)."""
     shape = x.shape
-    if len(shape) != 4 or shape[0] != B or shape[1] != L or shape[3] != d or x.dtype != dtype:
+    if len(shape) != 4 or shape[0] != B or shape[1] != L or shape[3] != d or x.dtype is not dtype:
         raise ValueError(f"{name} must be [{B}, {L}, heads, {d}] {dtype}")
     heads, (sb, sl, sh, sc) = shape[2], x.stride()
     ts = sl if L > 1 else sb if B > 1 else heads * d
@@ -459,7 +460,7 @@ def _token_rows(name, x, B, L, d, dtype):
 
 
 def _rope_args(Q, K, gamma_q, gamma_k, pe, positions):
-    if Q.dim() != 4 or K.dim() != 4:
+    if Q.dim() != 4:
         raise ValueError("Q and K must be [B, L, heads, d]")
     B, L, _, d = Q.shape
     H, q_ts = _token_rows("Q", Q, B, L, d, Q.dtype)
@@ -472,7 +473,7 @@ def _rope_args(Q, K, gamma_q, gamma_k, pe, positions):
 
 def _gammas(gamma_q, gamma_k, pe, d, dtype):
     for g in (gamma_q, gamma_k):
-        if g.shape != (d,) or g.dtype != dtype or not g.is_contiguous():
+        if g.numel() != d or g.dim() != 1 or g.dtype is not dtype or not g.is_contiguous():
             raise ValueError("gamma_q and gamma_k must be contiguous [d] of the rows' dtype")
     if pe.dtype is not torch.float32 or pe.dim() != 2 or not pe.is_contiguous():
         raise ValueError("pe must be contiguous float32 [rows, rope_dim]")

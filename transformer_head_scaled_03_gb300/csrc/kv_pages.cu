@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "kv_pages.cuh"
+#include "ptx_pdl.cuh"
 
 namespace mha {
 
@@ -115,53 +116,70 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ compaction
 
-// One bit per page that some sequence holds.
-__global__ void __launch_bounds__(kThreads)
-    kv_mark_kernel(const int32_t* __restrict__ table, const int32_t* __restrict__ kv_len, int B,
-                   int cols, int page_shift, int num_pages, unsigned* __restrict__ bits,
+constexpr int kRankThreads = 1024;
+
+// Which pages some sequence holds (one bit each), the held pages before each
+// word of 32, and their number.  One block: the bits are set in its shared
+// memory, 128 KB for the 2^20 pages that a pool may have, so nothing has to
+// be cleared beforehand and nothing but the result is written; a warp takes a
+// sequence at a time.
+__global__ void __launch_bounds__(kRankThreads)
+    kv_rank_kernel(const int32_t* __restrict__ table, const int32_t* __restrict__ kv_len, int B,
+                   int cols, int page_shift, int num_pages, unsigned* __restrict__ bits_out,
+                   int32_t* __restrict__ rank, int32_t* __restrict__ n_live, int room,
                    unsigned* err) {
-  const int b = blockIdx.x;
-  const int len = kv_len[b];
-  if (len < 0 || len > (static_cast<int64_t>(cols) << page_shift)) {
-    if (threadIdx.x == 0) atomicOr(err, kErrPages);
-    return;
-  }
-  const int held = (len + (1 << page_shift) - 1) >> page_shift;
-  for (int j = blockIdx.y * kThreads + threadIdx.x; j < held; j += gridDim.y * kThreads) {
-    const int page = table[static_cast<int64_t>(b) * cols + j];
-    if (page < 0 || page >= num_pages) {
-      atomicOr(err, kErrPages);
-    } else {
-      atomicOr(bits + (page >> 5), 1u << (page & 31));
+  extern __shared__ unsigned bits[];
+  __shared__ int sums[32];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int words = (num_pages + 31) / 32;
+  for (int w = threadIdx.x; w < words; w += kRankThreads) bits[w] = 0u;
+  __syncthreads();
+  for (int b = warp; b < B; b += kRankThreads / 32) {
+    const int len = kv_len[b];
+    if (len < 0 || len > (static_cast<int64_t>(cols) << page_shift)) {
+      if (lane == 0) atomicOr(err, kErrPages);
+      continue;
+    }
+    const int held = (len + (1 << page_shift) - 1) >> page_shift;
+    const int32_t* row = table + static_cast<int64_t>(b) * cols;
+#pragma unroll 4
+    for (int j = lane; j < held; j += 32) {
+      const int page = __ldg(row + j);
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(num_pages))
+        atomicOr(bits + (page >> 5), 1u << (page & 31));
+      else
+        atomicOr(err, kErrPages);
     }
   }
-}
-
-// rank[w] = held pages before word w; n_live.  One block.
-__global__ void __launch_bounds__(1024)
-    kv_rank_kernel(const unsigned* __restrict__ bits, int words, int32_t* __restrict__ rank,
-                   int32_t* __restrict__ n_live, int room, unsigned* err) {
-  __shared__ int sums[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
   int base = 0;
-  for (int w0 = 0; w0 < words; w0 += 1024) {
+  for (int w0 = 0; w0 < words; w0 += kRankThreads) {
     const int w = w0 + threadIdx.x;
-    const int c = w < words ? __popc(bits[w]) : 0;
+    const unsigned word = w < words ? bits[w] : 0u;
+    const int c = __popc(word);
     int incl = c;
+#pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, s);
       if (lane >= s) incl += up;
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int before = 0, total = 0;
-    for (int k = 0; k < 32; ++k) {
-      if (k < warp) before += sums[k];
-      total += sums[k];
+    // every warp sums up the warps before it, and all of them
+    int up_to = sums[lane];
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, up_to, s);
+      if (lane >= s) up_to += up;
     }
-    if (w < words) rank[w] = base + before + incl - c;
-    base += total;
-    __syncthreads();
+    const int before = warp ? __shfl_sync(0xffffffffu, up_to, warp - 1) : 0;
+    if (w < words) {
+      bits_out[w] = word;
+      rank[w] = base + before + incl - c;
+    }
+    base += __shfl_sync(0xffffffffu, up_to, 31);
+    __syncthreads();  // the sums have been read
   }
   if (threadIdx.x == 0) {
     *n_live = base;
@@ -173,10 +191,35 @@ __device__ __forceinline__ int rank_of(const unsigned* bits, const int32_t* rank
   return rank[page >> 5] + __popc(bits[page >> 5] & ((1u << (page & 31)) - 1u));
 }
 
-// Copy the held pages; blockIdx.y picks the layer and K or V.
+struct Renumber {
+  const int32_t* table;
+  const int32_t* kv_len;
+  int B, cols, page_shift;
+  int32_t* out;
+  int out_cols;
+};
+
+// Copy the held pages, blockIdx.y picking the layer and K or V; the last
+// blockIdx.y renumbers the page tables, a sequence per block at a time.
 __global__ void __launch_bounds__(kThreads)
     kv_move_kernel(const Pools src, const Pools dst, const unsigned* __restrict__ bits,
-                   const int32_t* __restrict__ rank, int page_vecs) {
+                   const int32_t* __restrict__ rank, int page_vecs, const Renumber tables) {
+  pdl_wait();
+  if (blockIdx.y == gridDim.y - 1) {
+    for (int b = blockIdx.x; b < tables.B; b += gridDim.x) {
+      const int len = tables.kv_len[b];
+      if (len < 0 || len > (static_cast<int64_t>(tables.cols) << tables.page_shift)) continue;
+      const int held = (len + (1 << tables.page_shift) - 1) >> tables.page_shift;
+      for (int j = threadIdx.x; j < held; j += kThreads) {
+        const int page = tables.table[static_cast<int64_t>(b) * tables.cols + j];
+        int r = -1;
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(src.num_pages))
+          r = rank_of(bits, rank, page);
+        tables.out[static_cast<int64_t>(b) * tables.out_cols + j] = r < dst.num_pages ? r : -1;
+      }
+    }
+    return;
+  }
   const int kv = blockIdx.y & 1, y = blockIdx.y >> 1;
   const uint4* from0 = (kv ? src.V : src.K) + y * src.layer_stride;
   uint4* to0 = (kv ? dst.V : dst.K) + y * dst.layer_stride;
@@ -187,23 +230,6 @@ __global__ void __launch_bounds__(kThreads)
     const uint4* from = from0 + page * src.page_stride;
     uint4* to = to0 + r * dst.page_stride;
     for (int v = threadIdx.x; v < page_vecs; v += kThreads) to[v] = from[v];
-  }
-}
-
-__global__ void __launch_bounds__(kThreads)
-    kv_renumber_kernel(const int32_t* __restrict__ table, const int32_t* __restrict__ kv_len,
-                       int cols, int page_shift, int num_pages, const unsigned* __restrict__ bits,
-                       const int32_t* __restrict__ rank, int32_t* __restrict__ out, int out_cols,
-                       int room) {
-  const int b = blockIdx.x;
-  const int len = kv_len[b];
-  if (len < 0 || len > (static_cast<int64_t>(cols) << page_shift)) return;
-  const int held = (len + (1 << page_shift) - 1) >> page_shift;
-  for (int j = blockIdx.y * kThreads + threadIdx.x; j < held; j += gridDim.y * kThreads) {
-    const int page = table[static_cast<int64_t>(b) * cols + j];
-    int r = -1;
-    if (page >= 0 && page < num_pages) r = rank_of(bits, rank, page);
-    out[static_cast<int64_t>(b) * out_cols + j] = r < room ? r : -1;
   }
 }
 
@@ -274,23 +300,28 @@ mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, in
   const int shift = page_shift_of(src->page_size);
   const int es = src->dtype == MHA_BF16 ? 2 : 4;
   const int page_vecs = src->kv_heads * src->page_size * (src->d * es / 16);
-  if (cudaMemsetAsync(bits, 0, static_cast<size_t>(words) * 4, s) != cudaSuccess)
-    return MHA_ERR_CUDA;
-  const int by = (src->table_cols + kThreads - 1) / kThreads;
-  const dim3 grid_t(src->B, by < 64 ? by : 64);
-  if (src->B > 0)
-    kv_mark_kernel<<<grid_t, kThreads, 0, s>>>(src->page_table, src->kv_lengths, src->B,
-                                               src->table_cols, shift, src->num_pages, bits,
-                                               ctl.err);
-  kv_rank_kernel<<<1, 1024, 0, s>>>(bits, words, rank, n_live, dst->num_pages, ctl.err);
-  const dim3 grid_m(src->num_pages < 2048 ? src->num_pages : 2048, src->layers * 2);
-  kv_move_kernel<<<grid_m, kThreads, 0, s>>>(pools_of(*src), pools_of(*dst), bits, rank,
-                                             page_vecs);
-  if (src->B > 0)
-    kv_renumber_kernel<<<grid_t, kThreads, 0, s>>>(src->page_table, src->kv_lengths,
-                                                   src->table_cols, shift, src->num_pages, bits,
-                                                   rank, dst->page_table, dst->table_cols,
-                                                   dst->num_pages);
+  cudaError_t e = cudaFuncSetAttribute(kv_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMaxPages / 8);
+  if (e != cudaSuccess) return MHA_ERR_CUDA;
+  kv_rank_kernel<<<1, kRankThreads, static_cast<size_t>(words) * 4, s>>>(
+      src->page_table, src->kv_lengths, src->B, src->table_cols, shift, src->num_pages, bits, rank,
+      n_live, dst->num_pages, ctl.err);
+  // the copies' blocks are placed while the ranks are computed, and wait
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(src->num_pages < 2048 ? src->num_pages : 2048, src->layers * 2 + 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const Renumber tables{src->page_table, src->kv_lengths, src->B, src->table_cols, shift,
+                        dst->page_table, dst->table_cols};
+  e = cudaLaunchKernelEx(&cfg, kv_move_kernel, pools_of(*src), pools_of(*dst),
+                         static_cast<const unsigned*>(bits), static_cast<const int32_t*>(rank),
+                         page_vecs, tables);
+  if (e != cudaSuccess) return MHA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 

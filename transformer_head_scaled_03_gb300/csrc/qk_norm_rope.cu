@@ -24,6 +24,7 @@
 
 #include "internal.h"
 #include "kv_pages.cuh"
+#include "ptx_pdl.cuh"
 
 namespace mha {
 namespace {
@@ -126,6 +127,7 @@ __device__ __forceinline__ float load_grad(const void* dy, int f32, int64_t i) {
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) norm_rope_any_bwd_kernel(const TrainArgs p) {
   __shared__ float sums[kWarps][kMaxD];
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = p.r / 2;
   for (int w = 0; w < 2; ++w) {
@@ -570,6 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     norm_rope_vec_bwd_kernel(const TrainArgs p, int parts) {
   using V = VecLane<D>;
   __shared__ float2 sums[kWarps][D / 2];
+  pdl_launch_dependents();
   const V at(p.r);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int w = 0; w < 2; ++w) {
@@ -611,6 +614,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 __global__ void __launch_bounds__(1024)
     dgamma_kernel(const float* __restrict__ partial, int blocks, int d, float* gq, float* gk) {
   __shared__ double sums[32][33];
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;  // of 2 * d
   double s = 0.;
@@ -922,8 +926,19 @@ mha_status qk_norm_rope_backward(const void* Q, int64_t q_token_stride, const vo
     else
       norm_rope_any_bwd_kernel<float><<<blocks, 32 * kWarps, 0, s>>>(p);
   }
-  dgamma_kernel<<<(2 * d + 31) / 32, 1024, 0, s>>>(p.partial, static_cast<int>(blocks), d,
-                                                   dgamma[0], dgamma[1]);
+  // placed while the rows are still worked on, and waits for them
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((2 * d + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, dgamma_kernel, static_cast<const float*>(p.partial),
+                         static_cast<int>(blocks), d, dgamma[0], dgamma[1]) != cudaSuccess)
+    return MHA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 
