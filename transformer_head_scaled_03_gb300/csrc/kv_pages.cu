@@ -61,6 +61,22 @@ Pools pools_of(const mha_kv_pages& p) {
                p.num_pages};
 }
 
+// Copy n 16-byte vectors with a block, four loads of a thread under way at a
+// time (the compiler may not move a load over a store that could alias it).
+__device__ __forceinline__ void block_copy(uint4* __restrict__ to, const uint4* __restrict__ from,
+                                           int n) {
+  constexpr int kAtOnce = 4;
+  for (int v0 = threadIdx.x; v0 < n; v0 += kThreads * kAtOnce) {
+    uint4 x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (v0 + k * kThreads < n) x[k] = from[v0 + k * kThreads];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (v0 + k * kThreads < n) to[v0 + k * kThreads] = x[k];
+  }
+}
+
 __global__ void __launch_bounds__(kThreads)
     kv_fork_kernel(const Pools pool, int32_t* __restrict__ table, int32_t* kv_len,
                    const int32_t* __restrict__ parents, const int32_t* __restrict__ children,
@@ -108,9 +124,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int s = blockIdx.y; s < slabs; s += gridDim.y) {
     const int g = s % kv_heads, kv = (s / kv_heads) & 1, y = s / (2 * kv_heads);
     uint4* base = (kv ? pool.V : pool.K) + y * pool.layer_stride + static_cast<int64_t>(g) * slab_stride;
-    const uint4* from = base + src * pool.page_stride;
-    uint4* to = base + fr * pool.page_stride;
-    for (int v = threadIdx.x; v < vecs; v += kThreads) to[v] = from[v];
+    block_copy(base + fr * pool.page_stride, base + src * pool.page_stride, vecs);
   }
 }
 
@@ -227,13 +241,19 @@ __global__ void __launch_bounds__(kThreads)
     if (!((bits[page >> 5] >> (page & 31)) & 1u)) continue;
     const int r = rank_of(bits, rank, page);
     if (r >= dst.num_pages) continue;
-    const uint4* from = from0 + page * src.page_stride;
-    uint4* to = to0 + r * dst.page_stride;
-    for (int v = threadIdx.x; v < page_vecs; v += kThreads) to[v] = from[v];
+    block_copy(to0 + r * dst.page_stride, from0 + page * src.page_stride, page_vecs);
   }
 }
 
 constexpr int kMaxPages = 1 << 20;
+
+int num_sms() {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+    return v;
+  return 1;
+}
 
 int words_of(int num_pages) { return (num_pages + 31) / 32; }
 
@@ -256,7 +276,10 @@ mha_status kv_pages_fork(const mha_kv_pages* pages, const int32_t* parents,
   if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
   const int es = pages->dtype == MHA_BF16 ? 2 : 4;
   const int64_t slabs = static_cast<int64_t>(pages->layers) * 2 * pages->kv_heads;
-  const dim3 grid(n, static_cast<unsigned>(slabs < 65535 ? slabs : 65535));
+  // every block checks its pair against all others first: no more blocks than
+  // keep the SMs full (about sixteen each)
+  const int64_t want = (16 * static_cast<int64_t>(num_sms()) + n - 1) / n;
+  const dim3 grid(n, static_cast<unsigned>(slabs < want ? slabs : want));
   kv_fork_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       pools_of(*pages), pages->page_table, pages->kv_lengths, parents, children, fresh, n,
       pages->B, pages->table_cols, page_shift_of(pages->page_size), pages->kv_heads,
