@@ -319,15 +319,19 @@ typedef struct {
  *       tokens that belong to no sequence are left as they were.
  *   H : a multiple of kv_heads; head h reads kv head h / (H / kv_heads), and
  *       H / kv_heads <= 128.
- *   max_new : the largest n_b, 1 <= max_new.
+ *   max_new : the largest n_b, 1 <= max_new.  Up to 16 rows (max_new times the
+ *       query heads of a kv head) take a kernel of their own, so a tight
+ *       bound matters while decoding.
  *   scale : as for sdpa_forward (0 selects 1/sqrt(d)).
  *   mask_kind : MHA_MASK_CAUSAL_BOTTOM_RIGHT (query i of n_b sees the tokens
  *       j <= kv_lengths[b] - n_b + i) or MHA_MASK_NONE (it sees all).
  *   num_splits : CTAs that share one block's keys, 1..16, merged exactly
  *       through one thread-block cluster; 0 picks a default.
  * The cache is pages->dtype BF16 with d in {64, 128}; `layer` picks the pool.
- * Rows of a page that lie behind the sequence's length may hold anything;
- * the rows a sequence holds must be finite.
+ * Rows of a page that lie behind the sequence's length may hold anything.
+ * The keys and values that a sequence holds must be finite, those of new
+ * tokens that a query does not see among them.  A NaN in a query reaches that
+ * query's row alone.
  * Checked on the device (MHA_ERR_DEVICE from mha_check): kv_lengths[b] in
  * [max(1, n_b), table_cols*page_size] (from 1 without the causal bit) and
  * page numbers in [0, num_pages) -- every row that would read through the bad

@@ -190,6 +190,33 @@ def test_bad_tables_lengths_and_offsets_are_reported(new):
     call(offs=[-4, offs[1], offs[2], T], max_new=T)
 
 
+@pytest.mark.parametrize("new,splits", [(1, 1), (1, 5), (40, 1), (40, 4), (200, 1), (200, 3)])
+def test_nan_queries_give_nan_and_stay_in_their_rows(new, splits):
+    x = case(155, [300, 260], [new, new], 4, 2, 16, 64)
+    want = run(*x, num_splits=splits, max_new=new)
+    Q = x[0].copy()
+    Q[new // 2, 1, 5] = np.nan
+    got = mha.sdpa_paged(dev(Q, BF), *(dev(v, BF) for v in x[1:3]), *(i32(v) for v in x[3:]),
+                         num_splits=splits, max_new=new)
+    assert mha.mha_check() == mha.MHA_OK
+    got = got.float().cpu().numpy()
+    assert np.all(np.isnan(got[new // 2, 1]))
+    got[new // 2, 1] = want[new // 2, 1]
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("new,G", [(1, 2), (2, 16)])
+def test_more_sequences_than_are_ranked(new, G):
+    """300 sequences, one in seven of them idle, in both kernels."""
+    rng = np.random.default_rng(156)
+    lens = rng.integers(new, 60, 300)
+    news = np.where(np.arange(300) % 7, new, 0)
+    x = case(157, list(lens), list(news), G, 1, 16, 64)
+    O, A = ref.sdpa_paged(*x)
+    for splits in (1, 2):
+        check(run(*x, num_splits=splits, max_new=new, out_dtype=F32), O, A, F32)
+
+
 def test_no_tokens_and_no_sequences():
     Q, K, V, table, lens, offs = case(160, [20], [1], 4, 2, 16, 64)
     O = mha.sdpa_paged(dev(Q[:0], BF), dev(K, BF), dev(V, BF), i32(table), i32(lens), i32([0, 0]))

@@ -153,6 +153,39 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
   return v;
 }
 
+// The splits' weights of one row, 2^(m_s - max m) / sum, into
+// weight[s * stride], from the row's maxima at `m_at`, sums at `l_at` and the
+// bad-page flags of the cluster's CTAs.  All 0 where no split saw a key (the
+// sum is 0) or a page number was bad; a NaN among the scores has made the sum
+// NaN and reaches the output.
+__device__ __forceinline__ void split_weights(uint32_t m_at, uint32_t l_at, uint32_t bad_at,
+                                              int splits, float* weight, int stride) {
+  float m[kPagedMaxSplits], l[kPagedMaxSplits], top = -INFINITY, sum = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int s = 0; s < kPagedMaxSplits; ++s)
+    if (s < splits) {
+      const uint32_t rk = static_cast<uint32_t>(s);
+      m[s] = ld_cluster_f32(cluster_map(m_at, rk));
+      l[s] = ld_cluster_f32(cluster_map(l_at, rk));
+      bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_at, rk))) != 0u;
+    }
+#pragma unroll
+  for (int s = 0; s < kPagedMaxSplits; ++s)
+    if (s < splits) top = fmaxf(top, m[s]);
+  if (top == -INFINITY) top = 0.f;
+#pragma unroll
+  for (int s = 0; s < kPagedMaxSplits; ++s)
+    if (s < splits) {
+      m[s] = ex2_approx(m[s] - top);
+      sum = fmaf(m[s], l[s], sum);
+    }
+  const bool none = bad || sum == 0.f;
+#pragma unroll
+  for (int s = 0; s < kPagedMaxSplits; ++s)
+    if (s < splits) weight[s * stride] = none ? 0.f : m[s] / sum;
+}
+
 // Merged outputs of N places, four columns each: sum over the cluster's splits
 // of weight times partial output (at the same shared address in every split),
 // the loads of U splits at a time under way together: a remote load takes

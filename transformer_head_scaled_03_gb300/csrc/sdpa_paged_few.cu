@@ -468,32 +468,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int S = p.splits;
     const uint32_t xm_s = smem_u32(xm), xl_s = smem_u32(xl), xo_s = smem_u32(xo);
     const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
-    if (threadIdx.x < kSlots) {
-      const int q = threadIdx.x;
-      float ms[kPagedMaxSplits], ls[kPagedMaxSplits], M = -INFINITY, den = 0.f;
-      bool bad = false;
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s) {
-        if (s >= S) break;
-        const uint32_t rk = static_cast<uint32_t>(s);
-        ms[s] = ld_cluster_f32(cluster_map(xm_s + 4u * q, rk));
-        ls[s] = ld_cluster_f32(cluster_map(xl_s + 4u * q, rk));
-        bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_s, rk))) != 0u;
-      }
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) M = fmaxf(M, ms[s]);
-      const bool none = bad || M == -INFINITY;
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) {
-          ms[s] = none ? 0.f : ex2_approx(ms[s] - M);
-          den = fmaf(ms[s], ls[s], den);
-        }
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) xw[s * kSlots + q] = none ? 0.f : ms[s] / den;
-    }
+    if (threadIdx.x < kSlots)
+      split_weights(xm_s + 4u * threadIdx.x, xl_s + 4u * threadIdx.x, bad_s, S, xw + threadIdx.x,
+                    kSlots);
     softmax_bar();
     const int total = rows * (D / 4);
     const int per = (total + S - 1) / S;

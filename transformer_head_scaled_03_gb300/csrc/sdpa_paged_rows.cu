@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         }
       }
     } else if (warp_in_use) {
-      const float inv_l = !zero && l > 0.f ? 1.f / l : 0.f;
+      const float inv_l = !zero && l != 0.f ? 1.f / l : 0.f;  // NaN stays NaN
       const int rows_here = min(32, tile_rows - quarter * 32);
       const int64_t row0 = static_cast<int64_t>(seq.q0 + i0 + t * tile_tokens) * p.H + g * p.G;
       // where tile row x goes, in rows of the output
@@ -600,30 +600,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     const uint32_t xo_s = base, xm_s = base + C::kOffM;
     const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
     if (static_cast<int>(threadIdx.x) < mine) {
-      const int row = smem_row(r0 + threadIdx.x);
-      float ms[kPagedMaxSplits], ls[kPagedMaxSplits], M = -INFINITY, den = 0.f;
-      bool bad = false;
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) {
-          const uint32_t rk = static_cast<uint32_t>(s);
-          ms[s] = ld_cluster_f32(cluster_map(xm_s + 4u * row, rk));
-          ls[s] = ld_cluster_f32(cluster_map(xm_s + 4u * (NQT * kBlockM + row), rk));
-          bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_s, rk))) != 0u;
-        }
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) M = fmaxf(M, ms[s]);
-      const bool none = bad || M == -INFINITY;
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) {
-          ms[s] = none ? 0.f : ex2_approx(ms[s] - M);
-          den = fmaf(ms[s], ls[s], den);
-        }
-#pragma unroll
-      for (int s = 0; s < kPagedMaxSplits; ++s)
-        if (s < S) weights[threadIdx.x * S + s] = none ? 0.f : ms[s] / den;
+      const uint32_t row = smem_row(r0 + threadIdx.x);
+      split_weights(xm_s + 4u * row, xm_s + 4u * (NQT * kBlockM + row), bad_s, S,
+                    weights + threadIdx.x * S, 1);
     }
     __syncthreads();
     const int total = mine * (D / 4);
