@@ -5,7 +5,8 @@ a fused tcgen05/TMEM attention kernel for bf16, tcgen05 projection GEMMs
 whose store layouts do the head split and the concat, and fp32 CUDA-core
 kernels.  This package is the thin Python binding over that ABI
 (``sdpa_forward``, ``mha_create``, ``mha_forward``, ``mha_check``,
-``mha_destroy``), the in-tree build (``build``) and the seeded input
+``mha_destroy``; over a paged cache ``qk_norm_rope_paged``, ``sdpa_paged``,
+``kv_pages_fork``, ``kv_pages_compact``), the in-tree build (``build``) and the seeded input
 generators (``inputs``).  Attribute access loads the binding lazily, so
 importing the package (e.g. for ``inputs``) needs neither torch nor a GPU.
 """
