@@ -37,16 +37,24 @@ struct PagedParams {
   int B, cols, num_pages, page_shift, kv_heads;
   int T, H, G, max_new, causal, out_f32, splits;
   float scale_log2;  // scale * log2(e)
+  float inv_G;       // 1 / G
   unsigned* err;
   uint64_t limit_ns;
 };
+
+// x / G for 0 <= x < 512: the quotient's fraction is a multiple of 1/G, and
+// half a unit of G keeps the product away from whole numbers by at least
+// 1/256, far above its rounding (a division takes about 35 instructions).
+__device__ __forceinline__ int div_by_group(const PagedParams& p, int x) {
+  return static_cast<int>((static_cast<float>(x) + 0.5f) * p.inv_G);
+}
 
 inline PagedParams paged_params(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
   return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.B, a.pages.cols,
                      a.pages.num_pages, a.pages.page_shift, a.pages.kv_heads, a.T, a.H, a.G,
                      a.max_new, a.causal, a.out_f32, a.splits,
                      static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634),
-                     ctl.err, ctl.limit_ns};
+                     1.f / static_cast<float>(a.G), ctl.err, ctl.limit_ns};
 }
 
 // The tensor maps of Q [T, H, d], of `tokens` tokens and one group of heads

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int last[kSlots];
 #pragma unroll
     for (int q = 0; q < kSlots; ++q)
-      last[q] = q >= rows ? -1 : p.causal ? len - seq.n + q / p.G : len - 1;
+      last[q] = q >= rows ? -1 : p.causal ? len - seq.n + div_by_group(p, q) : len - 1;
     float m[kSlots], l[kSlots], acc[kSlots], alpha_prev[kSlots];
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) {
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float* const weight[1] = {xw + q};
       float4 o[1];
       merge_splits<1, 8>(from, weight, kSlots, S, o);
-      const int i = q / p.G;
+      const int i = div_by_group(p, q);
       const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
       store_out4(p, row * D + (e - q * (D / 4)) * 4, o[0]);
     }

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     const int t = warp >> 2;
     const int quarter = warp & 3;  // this warp may touch TMEM lanes [32q, 32q+32)
     const int r = quarter * 32 + lane;
-    const int i = i0 + t * tile_tokens + r / p.G;  // this row's token of the sequence
+    const int i = i0 + t * tile_tokens + div_by_group(p, r);  // this row's token of the sequence
     const int tile_rows = min(tile_tokens, seq.n - i0 - t * tile_tokens) * p.G;
     const bool in_use = r < tile_rows;
     // rows of this warp that stand for a token (warp-uniform): without any,
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
       const int64_t row0 = static_cast<int64_t>(seq.q0 + i0 + t * tile_tokens) * p.H + g * p.G;
       // where tile row x goes, in rows of the output
       auto out_row = [&](int x) {
-        const int k = x / p.G;
+        const int k = div_by_group(p, x);
         return row0 + static_cast<int64_t>(k) * p.H + (x - k * p.G);
       };
       auto columns = [&](int cb, uint32_t (&o)[32]) {
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     const int S = p.splits;
     const int tile_rows = tile_tokens * p.G;  // those of a full tile
     const int rows = min(block_tokens, max(0, seq.n - i0)) * p.G;
-    auto smem_row = [&](int row) { return row + (row / tile_rows) * (kBlockM - tile_rows); };
+    auto smem_row = [&](int row) { return row < tile_rows ? row : row + kBlockM - tile_rows; };
     const int per = (rows + S - 1) / S;
     const int r0 = split * per;
     const int mine = max(0, min(rows, r0 + per) - r0);
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
           const int e = f0 + C::kThreads * k;
           if (e >= total) continue;
           const int row = e / (D / 4);
-          const int i = (r0 + row) / p.G;
+          const int i = div_by_group(p, r0 + row);
           const int64_t at =
               (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D;
           store_out4(p, at + (e - row * (D / 4)) * 4, o[k]);
