@@ -161,71 +161,65 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
   return v;
 }
 
-// The splits' weights of one row, 2^(m_s - max m) / sum, into
-// weight[s * stride], from the row's maxima at `m_at`, sums at `l_at` and the
-// bad-page flags of the cluster's CTAs.  All 0 where no split saw a key (the
-// sum is 0) or a page number was bad; a NaN among the scores has made the sum
-// NaN and reaches the output.
-__device__ __forceinline__ void split_weights(uint32_t m_at, uint32_t l_at, uint32_t bad_at,
-                                              int splits, float* weight, int stride) {
-  float m[kPagedMaxSplits], l[kPagedMaxSplits], top = -INFINITY, sum = 0.f;
+// The merge of a cluster's splits runs once per CTA, on code that no earlier
+// instruction has brought near: its loops stay rolled, since fetching unrolled
+// ones took longer (9 us at sixteen splits) than the remote loads, about a
+// thousand clocks each, that they kept under way.
+
+// Whether any CTA of the cluster met a bad page number (warp-collective; flag
+// at the same shared address in every CTA).
+__device__ __forceinline__ bool any_bad(uint32_t flag_at, int splits) {
+  const int lane = threadIdx.x & 31;
   bool bad = false;
-#pragma unroll
-  for (int s = 0; s < kPagedMaxSplits; ++s)
-    if (s < splits) {
-      const uint32_t rk = static_cast<uint32_t>(s);
-      m[s] = ld_cluster_f32(cluster_map(m_at, rk));
-      l[s] = ld_cluster_f32(cluster_map(l_at, rk));
-      bad |= __float_as_uint(ld_cluster_f32(cluster_map(bad_at, rk))) != 0u;
-    }
-#pragma unroll
-  for (int s = 0; s < kPagedMaxSplits; ++s)
-    if (s < splits) top = fmaxf(top, m[s]);
-  if (top == -INFINITY) top = 0.f;
-#pragma unroll
-  for (int s = 0; s < kPagedMaxSplits; ++s)
-    if (s < splits) {
-      m[s] = ex2_approx(m[s] - top);
-      sum = fmaf(m[s], l[s], sum);
-    }
-  const bool none = bad || sum == 0.f;
-#pragma unroll
-  for (int s = 0; s < kPagedMaxSplits; ++s)
-    if (s < splits) weight[s * stride] = none ? 0.f : m[s] / sum;
+  if (lane < splits)
+    bad = __float_as_uint(ld_cluster_f32(cluster_map(flag_at, static_cast<uint32_t>(lane)))) != 0u;
+  return __any_sync(0xffffffffu, bad);
 }
 
-// Merged outputs of N places, four columns each: sum over the cluster's splits
-// of weight times partial output (at the same shared address in every split),
-// the loads of U splits at a time under way together: a remote load takes
-// about a thousand clocks.  A weight of 0 stands for nothing seen, and for
-// rows to be zeroed, whose partial output may be anything.
-template <int N, int U>
-__device__ __forceinline__ void merge_splits(const uint32_t (&from)[N],
-                                             const float* const (&weight)[N], int stride,
-                                             int splits, float4 (&o)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < splits; s0 += U) {
-    float4 v[N][U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s0 + u < splits)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          v[i][u] = ld_cluster_f32x4(cluster_map(from[i], static_cast<uint32_t>(s0 + u)));
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s0 + u < splits)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float w = weight[i][(s0 + u) * stride];
-          if (w != 0.f) {
-            o[i].x = fmaf(w, v[i][u].x, o[i].x);
-            o[i].y = fmaf(w, v[i][u].y, o[i].y);
-            o[i].z = fmaf(w, v[i][u].z, o[i].z);
-            o[i].w = fmaf(w, v[i][u].w, o[i].w);
-          }
-        }
+// One split's weight of a row, 2^(m_s - max m) / sum, from the row's maxima
+// and sums of all splits (s * stride apart).  0 where no split saw a key (the
+// sum is 0); a NaN among the scores has made the sum NaN and reaches the
+// output.
+__device__ __forceinline__ float split_weight(const float* m, const float* l, int stride,
+                                              int splits, int s) {
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < splits; ++k) top = fmaxf(top, m[k * stride]);
+  if (top == -INFINITY) top = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < splits; ++k) sum = fmaf(ex2_approx(m[k * stride] - top), l[k * stride], sum);
+  return sum == 0.f ? 0.f : ex2_approx(m[s * stride] - top) / sum;
+}
+
+// o += weight * partial output at `from` in split s.  A weight of 0 stands for
+// nothing seen, and for rows to be zeroed, whose partial output may be
+// anything.
+__device__ __forceinline__ void add_split(float4& o, uint32_t from, int s, float weight) {
+  const float4 v = ld_cluster_f32x4(cluster_map(from, static_cast<uint32_t>(s)));
+  if (weight != 0.f) {
+    o.x = fmaf(weight, v.x, o.x);
+    o.y = fmaf(weight, v.y, o.y);
+    o.z = fmaf(weight, v.z, o.z);
+    o.w = fmaf(weight, v.w, o.w);
+  }
+}
+
+// Threads that share one place of the merged output: a power of two, as many
+// as there are splits for and threads to spare.
+__device__ __forceinline__ int merge_sharers(int places, int splits, int threads) {
+  int n = 1;
+  while (n < 16 && 2 * n <= splits && 2 * n * places <= threads) n *= 2;
+  return n;
+}
+
+// Sum over the `sharers` neighbouring threads of a place, in a fixed order.
+__device__ __forceinline__ void sum_sharers(float4& o, int sharers) {
+#pragma unroll 1
+  for (int k = 1; k < sharers; k *= 2) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
   }
 }
 

@@ -53,10 +53,10 @@ struct FewCfg {
   static constexpr int kOffQ = kOffRing + NR * kTile;
   static constexpr int kOffP = kOffQ + KB * kQBox;
   static constexpr int kOffRed = kOffP + 2 * kPBuf;  // [3][4 warps][16] f32
-  // the merge's m[16], l[16], o[16][D] and the weights [16 splits][16], in
-  // the first slot: written once every product has completed
+  // the merge's m[16], l[16], o[16][D], then every split's m and l and the
+  // weights, [16 splits][16] each, in the first slot: written once every product has completed
   static constexpr int kOffX = kOffRing;
-  static constexpr int kXBytes = (2 * kSlots + kSlots * D + kPagedMaxSplits * kSlots) * 4;
+  static constexpr int kXBytes = (2 * kSlots + kSlots * D + 3 * kPagedMaxSplits * kSlots) * 4;
   static_assert(kXBytes <= kTile, "the merge fits a stage");
   static constexpr int kOffBar = kOffRed + 3 * 4 * kSlots * 4;
   static constexpr int bQ = 0;
@@ -459,32 +459,49 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
-  // ---- merge the splits through distributed shared memory.  First each
-  // split's weight per slot, 2^(m_s - M) / sum, from one round of remote
-  // loads; then the outputs, four columns a thread, each another round.
+  // ---- merge the splits through distributed shared memory: every split's m
+  // and l are fetched, each thread works out weights, 2^(m_s - M) / sum, then
+  // the outputs, four columns a place, each another remote load
   __syncwarp();
   cluster_sync();  // every split's m, l, O and bad-page flag are in its shared memory
   if (warp < 4) {
     const int S = p.splits;
+    float* lm = xw + kPagedMaxSplits * kSlots;
+    float* ll = lm + kPagedMaxSplits * kSlots;
     const uint32_t xm_s = smem_u32(xm), xl_s = smem_u32(xl), xo_s = smem_u32(xo);
-    const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
-    if (threadIdx.x < kSlots)
-      split_weights(xm_s + 4u * threadIdx.x, xl_s + 4u * threadIdx.x, bad_s, S, xw + threadIdx.x,
-                    kSlots);
+    const bool bad = any_bad(smem_u32(const_cast<int*>(bad_page)), S);
+#pragma unroll 1
+    for (int x = threadIdx.x; x < S * kSlots; x += 128) {
+      const uint32_t q = x % kSlots, s = x / kSlots;
+      lm[x] = ld_cluster_f32(cluster_map(xm_s + 4u * q, s));
+      ll[x] = ld_cluster_f32(cluster_map(xl_s + 4u * q, s));
+    }
+    softmax_bar();
+#pragma unroll 1
+    for (int x = threadIdx.x; x < S * kSlots; x += 128)
+      xw[x] = bad ? 0.f : split_weight(lm + x % kSlots, ll + x % kSlots, kSlots, S, x / kSlots);
     softmax_bar();
     const int total = rows * (D / 4);
     const int per = (total + S - 1) / S;
     const int e0 = split * per;
     const int e1 = min(total, e0 + per);
-    for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += 128) {
+    const int sharers = merge_sharers(per, S, 128);
+#pragma unroll 1
+    for (int f0 = e0; f0 < e1; f0 += 128 / sharers) {
+      const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
       const int q = e / (D / 4);
-      const uint32_t from[1] = {xo_s + 16u * e};  // slot * D + column
-      const float* const weight[1] = {xw + q};
-      float4 o[1];
-      merge_splits<1, 8>(from, weight, kSlots, S, o);
-      const int i = div_by_group(p, q);
-      const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
-      store_out4(p, row * D + (e - q * (D / 4)) * 4, o[0]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < e1) {
+#pragma unroll 2
+        for (int s = threadIdx.x % sharers; s < S; s += sharers)
+          add_split(o, xo_s + 16u * e, s, xw[s * kSlots + q]);
+      }
+      sum_sharers(o, sharers);
+      if (e < e1 && threadIdx.x % sharers == 0) {
+        const int i = div_by_group(p, q);
+        const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
+        store_out4(p, row * D + (e - q * (D / 4)) * 4, o);
+      }
     }
   }
   __syncwarp();

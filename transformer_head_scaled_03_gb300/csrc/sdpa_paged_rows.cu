@@ -20,8 +20,6 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include <cuda_bf16.h>
 
 #include "sdpa_paged.cuh"
@@ -79,8 +77,9 @@ struct RowsCfg {
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffM = kOffMisc + 32;  // m, l of every row, f32
   static constexpr int kOffW = kOffM + 2 * NQT * kBlockM * 4;
-  // the weights of this CTA's share of the rows, for every split
-  static constexpr int kWBytes = (NQT * kBlockM + kPagedMaxSplits) * 4;
+  // of this CTA's share of the rows, for every split: weights, m, l
+  static constexpr int kShare = NQT * kBlockM + kPagedMaxSplits;
+  static constexpr int kWBytes = 3 * kShare * 4;
   static constexpr int kSmemBytes = kOffW + kWBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -598,45 +597,45 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     const int mine = max(0, min(rows, r0 + per) - r0);
     float* weights = reinterpret_cast<float*>(gbase + C::kOffW);  // [row of mine][S]
     const uint32_t xo_s = base, xm_s = base + C::kOffM;
-    const uint32_t bad_s = smem_u32(const_cast<int*>(bad_page));
-    if (static_cast<int>(threadIdx.x) < mine) {
-      const uint32_t row = smem_row(r0 + threadIdx.x);
-      split_weights(xm_s + 4u * row, xm_s + 4u * (NQT * kBlockM + row), bad_s, S,
-                    weights + threadIdx.x * S, 1);
+    float* lm = weights + C::kShare;
+    float* ll = lm + C::kShare;
+    const bool bad = any_bad(smem_u32(const_cast<int*>(bad_page)), S);
+#pragma unroll 1
+    for (int x = threadIdx.x; x < mine * S; x += C::kThreads) {
+      const int k = x / S;
+      const uint32_t s = x - k * S, row = smem_row(r0 + k);
+      lm[x] = ld_cluster_f32(cluster_map(xm_s + 4u * row, s));
+      ll[x] = ld_cluster_f32(cluster_map(xm_s + 4u * (NQT * kBlockM + row), s));
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = threadIdx.x; x < mine * S; x += C::kThreads) {
+      const int k = x / S;
+      weights[x] = bad ? 0.f : split_weight(lm + k * S, ll + k * S, 1, S, x - k * S);
     }
     __syncthreads();
     const int total = mine * (D / 4);
-    // N places a thread at a time: four while a CTA's share is many rows
-    auto merge = [&](auto n_const, auto u_const) {
-      constexpr int N = decltype(n_const)::value, U = decltype(u_const)::value;
-      for (int f0 = threadIdx.x; f0 < total; f0 += C::kThreads * N) {
-        uint32_t from[N];
-        const float* weight[N];
-        float4 o[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int e = min(f0 + C::kThreads * k, total - 1);
-          const int row = e / (D / 4);
-          from[k] = xo_s + 4u * (smem_row(r0 + row) * C::kXRow + (e - row * (D / 4)) * 4);
-          weight[k] = weights + row * S;
-        }
-        merge_splits<N, U>(from, weight, 1, S, o);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int e = f0 + C::kThreads * k;
-          if (e >= total) continue;
-          const int row = e / (D / 4);
-          const int i = div_by_group(p, r0 + row);
-          const int64_t at =
-              (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D;
-          store_out4(p, at + (e - row * (D / 4)) * 4, o[k]);
-        }
+    const int sharers = merge_sharers(total, S, C::kThreads);
+#pragma unroll 1
+    for (int f0 = 0; f0 < total; f0 += C::kThreads / sharers) {
+      const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
+      const int row = e / (D / 4);
+      const int c = (e - row * (D / 4)) * 4;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < total) {
+        const uint32_t from = xo_s + 4u * (smem_row(r0 + row) * C::kXRow + c);
+#pragma unroll 2
+        for (int s = threadIdx.x % sharers; s < S; s += sharers)
+          add_split(o, from, s, weights[row * S + s]);
       }
-    };
-    if (total >= 4 * C::kThreads)
-      merge(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    else
-      merge(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+      sum_sharers(o, sharers);
+      if (e < total && threadIdx.x % sharers == 0) {
+        const int i = div_by_group(p, r0 + row);
+        const int64_t at =
+            (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D + c;
+        store_out4(p, at, o);
+      }
+    }
     __syncwarp();
     cluster_sync();  // no CTA leaves while another still reads its shared memory
   }
