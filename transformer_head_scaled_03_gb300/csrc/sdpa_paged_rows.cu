@@ -526,27 +526,25 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         const int k = div_by_group(p, x);
         return row0 + static_cast<int64_t>(k) * p.H + (x - k * p.G);
       };
-      auto columns = [&](int cb, uint32_t (&o)[32]) {
-        if (zero) {
+      // the whole row at once: one wait for tensor memory
+      uint32_t o[D];
+      if (zero) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0u;
-          return;
-        }
-        tmem_ld32(tO + cb * 32, o);
+        for (int c = 0; c < D; ++c) o[c] = 0u;
+      } else {
+#pragma unroll
+        for (int cb = 0; cb < D; cb += 32)
+          tmem_ld32(tO + cb, *reinterpret_cast<uint32_t(*)[32]>(&o[cb]));
         tmem_ld_wait(o);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
-      };
+        for (int c = 0; c < D; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
+      }
       if (p.out_f32) {
-        const int64_t at = out_row(in_use ? r : quarter * 32) * D;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.O) +
+                                              out_row(in_use ? r : quarter * 32) * D);
+        if (in_use) {
 #pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          columns(cb, o);
-          if (!in_use) continue;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.O) + at + cb * 32);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int c = 0; c < D / 4; ++c)
             dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       } else {
@@ -557,18 +555,13 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         uint4* stg = reinterpret_cast<uint4*>(gbase + C::kOffQ + t * C::kQTileBytes) +
                      quarter * 32 * kPieces;
 #pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          columns(cb, o);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]), __uint_as_float(o[8 * c + 1]));
-            v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]), __uint_as_float(o[8 * c + 3]));
-            v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]), __uint_as_float(o[8 * c + 5]));
-            v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]), __uint_as_float(o[8 * c + 7]));
-            stg[lane * kPieces + ((cb * 4 + c) ^ (lane & 7))] = v;
-          }
+        for (int c = 0; c < kPieces; ++c) {
+          uint4 v;
+          v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]), __uint_as_float(o[8 * c + 1]));
+          v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]), __uint_as_float(o[8 * c + 3]));
+          v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]), __uint_as_float(o[8 * c + 5]));
+          v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]), __uint_as_float(o[8 * c + 7]));
+          stg[lane * kPieces + (c ^ (lane & 7))] = v;
         }
         __syncwarp();
         const int piece = lane % kPieces;
@@ -615,25 +608,65 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
     }
     __syncthreads();
     const int total = mine * (D / 4);
-    const int sharers = merge_sharers(total, S, C::kThreads);
+    // place e of this CTA's share: its shared address, its output element
+    auto place_from = [&](int row, int c) {
+      return xo_s + 4u * (smem_row(r0 + row) * C::kXRow + c);
+    };
+    auto place_to = [&](int row, int c) {
+      const int i = div_by_group(p, r0 + row);
+      return (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D + c;
+    };
+    if (total < 4 * C::kThreads) {
+      // few places: several threads to one where there are threads to spare
+      const int sharers = merge_sharers(total, S, C::kThreads);
 #pragma unroll 1
-    for (int f0 = 0; f0 < total; f0 += C::kThreads / sharers) {
-      const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
-      const int row = e / (D / 4);
-      const int c = (e - row * (D / 4)) * 4;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e < total) {
-        const uint32_t from = xo_s + 4u * (smem_row(r0 + row) * C::kXRow + c);
-#pragma unroll 2
-        for (int s = threadIdx.x % sharers; s < S; s += sharers)
-          add_split(o, from, s, weights[row * S + s]);
+      for (int f0 = 0; f0 < total; f0 += C::kThreads / sharers) {
+        const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
+        const int row = e / (D / 4), c = e % (D / 4) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < total) {
+          const uint32_t from = place_from(row, c);
+#pragma unroll 4
+          for (int s = threadIdx.x % sharers; s < S; s += sharers)
+            add_split(o, from, s, weights[row * S + s]);
+        }
+        sum_sharers(o, sharers);
+        if (e < total && threadIdx.x % sharers == 0) store_out4(p, place_to(row, c), o);
       }
-      sum_sharers(o, sharers);
-      if (e < total && threadIdx.x % sharers == 0) {
-        const int i = div_by_group(p, r0 + row);
-        const int64_t at =
-            (static_cast<int64_t>(seq.q0 + i0 + i) * p.H + g * p.G + (r0 + row - i * p.G)) * D + c;
-        store_out4(p, at, o);
+    } else {
+      // many: eight places of a thread at a time, a remote load each under way
+      constexpr int N = 8;
+#pragma unroll 1
+      for (int f0 = threadIdx.x; f0 < total; f0 += N * C::kThreads) {
+        float4 o[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
+          float4 v[N];
+          const uint32_t there = cluster_map(xo_s, static_cast<uint32_t>(s));
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int e = min(f0 + k * C::kThreads, total - 1);
+            v[k] = ld_cluster_f32x4(there + (place_from(e / (D / 4), e % (D / 4) * 4) - xo_s));
+          }
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int e = min(f0 + k * C::kThreads, total - 1);
+            const float w = weights[e / (D / 4) * S + s];
+            if (w != 0.f) {  // as in add_split
+              o[k].x = fmaf(w, v[k].x, o[k].x);
+              o[k].y = fmaf(w, v[k].y, o[k].y);
+              o[k].z = fmaf(w, v[k].z, o[k].z);
+              o[k].w = fmaf(w, v[k].w, o[k].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int e = f0 + k * C::kThreads;
+          if (e < total) store_out4(p, place_to(e / (D / 4), e % (D / 4) * 4), o[k]);
+        }
       }
     }
     __syncwarp();
