@@ -8,7 +8,9 @@
 // sequence's table names it within that sequence's length.
 //
 // Both are copies, bound by HBM: every byte that has to move is read and
-// written once.
+// written once.  Measured: 96 forks of 24 parents over eight layers, 400 MB
+// moved, 47 us (parents' pages come from L2 again); 1,600 pages of four layers
+// compacted, 3.2 GB moved, 474 us, 6.8 TB/s; small ones 3 and 4 us.
 #include <stdint.h>
 
 #include "internal.h"

@@ -15,9 +15,9 @@ namespace {
 // tensor memory the runtime's calculator answers one CTA per SM).
 __global__ void paged_occupancy_proxy_kernel() {}
 
-}  // namespace
-
-int paged_max_active_clusters(int threads, int smem_bytes, int splits) {
+// Clusters of `splits` CTAs of a kernel with this block size and shared
+// memory that the device holds at once (0 when the query fails).
+int max_active_clusters(int threads, int smem_bytes, int splits) {
   auto kern = paged_occupancy_proxy_kernel;
   int n = 0;
   cudaLaunchConfig_t cfg = {};
@@ -44,6 +44,8 @@ int paged_max_active_clusters(int threads, int smem_bytes, int splits) {
   return n;
 }
 
+}  // namespace
+
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
   // How many clusters of each size are resident at once (a cluster sits
   // inside one GPC): the device is asked once per kernel.
@@ -64,14 +66,17 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
   Entry fresh{dev, threads, smem_bytes, {}};
   if (!e) {
     for (int s = 1; s <= kPagedMaxSplits; ++s)
-      fresh.fits[s] = paged_max_active_clusters(threads, smem_bytes, s);
+      fresh.fits[s] = max_active_clusters(threads, smem_bytes, s);
     if (used < 64) table[used++] = fresh;
     e = &fresh;
   }
   // Time in units of one 128-key tile: a CTA's tiles, its set-up and first
   // loads (4), and the merge (3).  Waves of clusters: lengths differ and long
   // sequences go first, so a partial last wave costs something between its
-  // share and a whole one.
+  // share and a whole one.  Measured against every split count: within 5 % of
+  // the best for one to 64 sequences of 200 to 32 K tokens, but for chunks of
+  // very unequal sequences (20 tokens over 2 to 9 K keys: 94 us at the chosen
+  // two, 86 at four).
   const double tiles = static_cast<double>(capacity) / 128;
   int best = 1;
   double least = 0;

@@ -231,10 +231,6 @@ __device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, 
   }
 }
 
-// Clusters of `splits` CTAs of a kernel with this block size and shared
-// memory that the device holds at once (0 when the query fails).
-int paged_max_active_clusters(int threads, int smem_bytes, int splits);
-
 // Split count for `blocks` blocks over sequences of up to `capacity` keys.
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes);
 
