@@ -319,9 +319,9 @@ typedef struct {
  *       tokens that belong to no sequence are left as they were.
  *   H : a multiple of kv_heads; head h reads kv head h / (H / kv_heads), and
  *       H / kv_heads <= 128.
- *   max_new : the largest n_b, 1 <= max_new.  Up to 16 rows (max_new times the
- *       query heads of a kv head) take a kernel of their own, so a tight
- *       bound matters while decoding.
+ *   max_new : the largest n_b, 1 <= max_new (0 will do for T = 0).  Up to 16
+ *       rows (max_new times the query heads of a kv head) take a kernel of
+ *       their own, so a tight bound matters while decoding.
  *   scale : as for sdpa_forward (0 selects 1/sqrt(d)).
  *   mask_kind : MHA_MASK_CAUSAL_BOTTOM_RIGHT (query i of n_b sees the tokens
  *       j <= kv_lengths[b] - n_b + i) or MHA_MASK_NONE (it sees all).

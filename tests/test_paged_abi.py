@@ -86,6 +86,7 @@ def test_sdpa_paged_unsupported_caches(lib, kw):
 
 def test_empty_calls_are_no_ops(lib):
     assert paged(lib, T=0, Q=None, O=None) == OK
+    assert paged(lib, T=0, Q=None, O=None, max_new=0) == OK
     assert paged(lib, pg=pages(B=0), offs=None) == OK
     assert lib.kv_pages_fork(pages(), None, None, None, 0, None) == OK
     assert rope(lib, B=0, Q=None, K=None) == OK

@@ -600,15 +600,17 @@ def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, tab
     dst = _kv_pages(K_out, V_out, table_out, kv_lengths)
     on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
                     K_pages if workspace is None else workspace)
-    count = _new(stream, (1,), torch.int32, K_pages.device)
     dev = _lib or lib()
+    need = dev.kv_pages_compact_workspace_bytes(src.num_pages)
+    # n, and the workspace 16 bytes behind it
+    own = 0 if workspace is not None else need // 4
+    count = _new(stream, (4 + own,), torch.int32, K_pages.device)
     if workspace is None:
-        workspace = _new(stream, (dev.kv_pages_compact_workspace_bytes(src.num_pages) or 16,),
-                         torch.uint8, K_pages.device)
-    _check(dev.kv_pages_compact(src, dst, count.data_ptr(), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), on),
-           "kv_pages_compact")
-    return count
+        at, size = count.data_ptr() + 16, need
+    else:
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(dev.kv_pages_compact(src, dst, count.data_ptr(), at, size, on), "kv_pages_compact")
+    return count[:1]
 
 
 class MhaHandle:

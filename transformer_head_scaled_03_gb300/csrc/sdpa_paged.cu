@@ -46,6 +46,23 @@ int max_active_clusters(int threads, int smem_bytes, int splits) {
 
 }  // namespace
 
+cudaError_t paged_kernel_attributes(const void* kernel, int smem_bytes,
+                                    std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
   // How many clusters of each size are resident at once (a cluster sits
   // inside one GPC): the device is asked once per kernel.
@@ -104,7 +121,7 @@ mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages*
                       int mask_kind, mha_dtype out_dtype, int num_splits, mha_stream stream) {
   const mha_status st = validate_pages(pages);
   if (st != MHA_OK) return st;
-  if (T < 0 || H < 1 || max_new < 1 || layer < 0 || layer >= pages->layers ||
+  if (T < 0 || H < 1 || max_new < (T > 0 ? 1 : 0) || layer < 0 || layer >= pages->layers ||
       H % pages->kv_heads != 0)
     return MHA_ERR_INVALID_ARG;
   if (out_dtype != MHA_BF16 && out_dtype != MHA_F32) return MHA_ERR_INVALID_ARG;

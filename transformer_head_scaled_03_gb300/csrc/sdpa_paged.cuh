@@ -3,6 +3,8 @@
 // page.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 #include "kv_pages.cuh"
 #include "ptx_cluster.cuh"
@@ -230,6 +232,12 @@ __device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, 
     if (global_timer_ns() - t0 > limit_ns) return;
   }
 }
+
+// Let a kernel use `smem_bytes` of shared memory, all of the unified array for
+// it, and clusters of up to 16: set once per device and kernel (`done` holds a
+// bit per device; above 64 devices it is set every time).
+cudaError_t paged_kernel_attributes(const void* kernel, int smem_bytes,
+                                    std::atomic<uint64_t>* done);
 
 // Split count for `blocks` blocks over sequences of up to `capacity` keys.
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes);

@@ -709,13 +709,9 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
         blocks, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, C::kThreads, C::kSmemBytes);
   if (blocks * a.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = sdpa_paged_rows_kernel<D, NQT, NST, BN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess && a.splits > 8)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> attributes_set{0};
+  cudaError_t e = paged_kernel_attributes(reinterpret_cast<const void*>(kern), C::kSmemBytes,
+                                          &attributes_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * a.splits));
