@@ -15,8 +15,6 @@ namespace {
 // tensor memory the runtime's calculator answers one CTA per SM).
 __global__ void paged_occupancy_proxy_kernel() {}
 
-// Clusters of `splits` CTAs of a kernel with this block size and shared
-// memory that the device holds at once (0 when the query fails).
 int max_active_clusters(int threads, int smem_bytes, int splits) {
   auto kern = paged_occupancy_proxy_kernel;
   int n = 0;
@@ -63,9 +61,9 @@ cudaError_t paged_kernel_attributes(const void* kernel, int smem_bytes,
   return e;
 }
 
-int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
-  // How many clusters of each size are resident at once (a cluster sits
-  // inside one GPC): the device is asked once per kernel.
+int paged_resident_clusters(int threads, int smem_bytes, int splits) {
+  // a cluster sits inside one GPC, so the device is asked for every size, once
+  // per kernel
   struct Entry {
     int dev, threads, smem;
     int fits[kPagedMaxSplits + 1];
@@ -74,19 +72,18 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
   static Entry table[64];
   static int used = 0;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lock(mutex);
-  const Entry* e = nullptr;
   for (int i = 0; i < used; ++i)
     if (table[i].dev == dev && table[i].threads == threads && table[i].smem == smem_bytes)
-      e = &table[i];
-  Entry fresh{dev, threads, smem_bytes, {}};
-  if (!e) {
-    for (int s = 1; s <= kPagedMaxSplits; ++s)
-      fresh.fits[s] = max_active_clusters(threads, smem_bytes, s);
-    if (used < 64) table[used++] = fresh;
-    e = &fresh;
-  }
+      return table[i].fits[splits];
+  Entry e{dev, threads, smem_bytes, {}};
+  for (int s = 1; s <= kPagedMaxSplits; ++s) e.fits[s] = max_active_clusters(threads, smem_bytes, s);
+  if (used < 64) table[used++] = e;
+  return e.fits[splits];
+}
+
+int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
   // Time in units of one 128-key tile: a CTA's tiles, its set-up and first
   // loads (4), and the merge (3).  Waves of clusters: lengths differ and long
   // sequences go first, so a partial last wave costs something between its
@@ -98,8 +95,9 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kPagedMaxSplits && (s == 1 || s <= tiles); ++s) {
-    if (e->fits[s] < 1) continue;
-    const double waves = static_cast<double>(blocks) / e->fits[s];
+    const int fits = paged_resident_clusters(threads, smem_bytes, s);
+    if (fits < 1) continue;
+    const double waves = static_cast<double>(blocks) / fits;
     const double cost = (waves <= 1 ? 1 : 0.5 * (ceil(waves) + waves)) *
                         (tiles / s + 4 + (s > 1 ? 3 : 0));
     if (s == 1 || cost < least) {

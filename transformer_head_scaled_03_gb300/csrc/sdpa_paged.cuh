@@ -239,6 +239,10 @@ __device__ __forceinline__ void paged_wait_drain(uint32_t bar, uint32_t parity, 
 cudaError_t paged_kernel_attributes(const void* kernel, int smem_bytes,
                                     std::atomic<uint64_t>* done);
 
+// Clusters of `splits` CTAs of a kernel with this block size and shared
+// memory that the device holds at once (0 when it cannot be asked).
+int paged_resident_clusters(int threads, int smem_bytes, int splits);
+
 // Split count for `blocks` blocks over sequences of up to `capacity` keys.
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes);
 

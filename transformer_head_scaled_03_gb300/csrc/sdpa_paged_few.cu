@@ -19,8 +19,8 @@
 // At 16 slots a byte of the cache meets at most 16 flops: bound by HBM, so
 // the pipeline is sized for bytes in flight (two CTAs of 96 KB per SM).
 // Measured: 16 sequences of 16 to 32 K tokens, 32 heads on 8 kv heads, d = 128:
-// 226 us, 7.1 TB/s of cache (DRAM at 86 % of its nominal rate); 64 sequences of
-// 200 to 1000 tokens: 52 us, where a CTA lives for five tiles and its start
+// 226 us, 7.1 TB/s of cache (DRAM at 87 % of its nominal rate); 64 sequences of
+// 200 to 1000 tokens: 49 us, where a CTA lives for five tiles and its start
 // and merge count (one CTA per SM with 64 KB stages: 70 us); one token over
 // 700 keys: 8 us on the device.
 #include <math.h>
@@ -44,15 +44,19 @@ constexpr int kMmaWarp = 5;
 constexpr uint32_t kTmemCols = 64;  // S^T x 2 (cols 0-31), O^T x 2 (cols 32-63)
 constexpr int kMaxSortedBatch = 256;
 
-template <int D>
+// kAlone: the launch has a CTA per SM at most.
+template <int D, bool kAlone>
 struct FewCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int KB = D / 64;
-  // Two CTAs share an SM: one's set-up, first loads and merge run under the
-  // other's stream.  K and V tiles go through one ring in the order in which
-  // the products take them (K0 K1 V0 K2 V1 K3 ...), so that three 32 KB slots
-  // (d = 128; five of 16 KB at d = 64) are all under way or in use.
-  static constexpr int NR = D == 128 ? 3 : 5;
+  // K and V tiles go through one ring in the order in which the products take
+  // them (K0 K1 V0 K2 V1 K3 ...), so that its slots, 32 KB at d = 128 and 16 KB
+  // at d = 64, are all under way or in use.  Two CTAs share an SM, with three
+  // slots (five) each: one's set-up, first loads and merge run under the
+  // other's stream.  A CTA alone on its SM takes six (eleven): 64 CTAs of 32
+  // tiles 51 -> 46 us, 128 of 16 about the same.
+  static constexpr int NR = D == 128 ? (kAlone ? 6 : 3) : kAlone ? 11 : 5;
+  static constexpr int kCtas = kAlone ? 1 : 2;
   static constexpr int kTile = KB * kSub;
   static constexpr int kOffRing = 0;
   static constexpr int kOffQ = kOffRing + NR * kTile;
@@ -83,7 +87,7 @@ struct FewCfg {
       kOffSeq + kSeqBytes > kOffQ + kSub ? kOffSeq + kSeqBytes : kOffQ + kSub;
   static constexpr int kSmemBytes = kEnd + 1024;  // + alignment slack
   static_assert(kOffP % 1024 == 0, "P^T swizzle atoms must be 1024-byte aligned");
-  static_assert(kSmemBytes + 1024 <= 114 * 1024, "two CTAs per SM");
+  static_assert(kSmemBytes + 1024 <= 228 * 1024 / kCtas, "CTAs per SM");
 };
 
 // Places of K(j) and V(j) in the ring's order, for T tiles.
@@ -94,12 +98,41 @@ __device__ __forceinline__ void softmax_bar() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+// N query slots (of the products' 16) of this thread's lane in tensor memory.
+template <int N>
+__device__ __forceinline__ void tmem_ld_slots(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "slots");
+  if constexpr (N == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+  } else {
+    tmem_ld16_sync(taddr, r);
+  }
+}
+
+// U: query slots that the softmax works on (4, 8 or 16); the products have 16
+// all the same, those behind U with weights of 0.  At 16 a tile's softmax is
+// 2,200 clk, longer than its copies take a lone CTA; at four one sequence of
+// 32 K tokens on eight CTAs takes 240 us instead of 275, on 64 of them 43
+// instead of 46.
+template <int D, int U, bool kAlone>
+__global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
     sdpa_paged_few_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-  using C = FewCfg<D>;
+  using C = FewCfg<D, kAlone>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -317,13 +350,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool o_rows = warp * 32 < D;  // warp-uniform
     const float sl2 = p.scale_log2;
     // the last key each slot sees; -1 for a slot not in use
-    int last[kSlots];
+    int last[U];
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q)
+    for (int q = 0; q < U; ++q)
       last[q] = q >= rows ? -1 : p.causal ? len - seq.n + div_by_group(p, q) : len - 1;
-    float m[kSlots], l[kSlots], acc[kSlots], alpha_prev[kSlots];
+    float m[U], l[U], acc[U], alpha_prev[U];
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
+    for (int q = 0; q < U; ++q) {
       m[q] = -INFINITY;
       l[q] = 0.f;
       acc[q] = 0.f;
@@ -333,6 +366,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kk = r & 63;
     uint8_t* p_key = gbase + C::kOffP + (r >> 6) * 2048 + (kk & 7) * 2;
     const int chunk = kk >> 3;
+    if constexpr (U < kSlots) {
+      // weights of the slots behind U, published with the first tile's
+      for (int i = threadIdx.x; i < 2 * kPBuf / 16; i += 128)
+        *reinterpret_cast<uint4*>(gbase + C::kOffP + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      softmax_bar();
+    }
     bool ok = true;
     for (int j = 0; j < T; ++j) {
       const int buf = j & 1;
@@ -340,29 +379,29 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int key = (t_begin + j) * kKeys + r;
       if (!(ok = mbar_wait_warp(bar(C::bS(buf)), par, ctl))) break;
       tc_fence_after();
-      uint32_t sr[kSlots];
-      tmem_ld16_sync(tS + buf * kSlots, sr);
-      float s[kSlots];
+      uint32_t sr[U];
+      tmem_ld_slots<U>(tS + buf * kSlots, sr);
+      float s[U];
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q)
+      for (int q = 0; q < U; ++q)
         s[q] = key <= last[q] ? __uint_as_float(sr[q]) * sl2 : -INFINITY;
       float* rb = red + buf * 4 * kSlots;
       {
-        float wm[kSlots];
+        float wm[U];
 #pragma unroll
-        for (int q = 0; q < kSlots; ++q) wm[q] = warp_max_f32(s[q]);
+        for (int q = 0; q < U; ++q) wm[q] = warp_max_f32(s[q]);
         if (lane == 0) {
           float4* dst = reinterpret_cast<float4*>(rb + warp * kSlots);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < U / 4; ++i)
             dst[i] = make_float4(wm[4 * i], wm[4 * i + 1], wm[4 * i + 2], wm[4 * i + 3]);
         }
       }
       mbar_arrive(bar(C::bRed(buf)));
       if (!(ok = mbar_wait_warp(bar(C::bRed(buf)), par, ctl))) break;
-      float alpha[kSlots];
+      float alpha[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U / 4; ++i) {
         const float4 a0 = reinterpret_cast<const float4*>(rb)[i];
         const float4 a1 = reinterpret_cast<const float4*>(rb + kSlots)[i];
         const float4 a2 = reinterpret_cast<const float4*>(rb + 2 * kSlots)[i];
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // rounding matches): row q, key r, 128-byte swizzle
       uint8_t* pb = p_key + buf * kPBuf;
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q)
+      for (int q = 0; q < U; ++q)
         *reinterpret_cast<__nv_bfloat16*>(pb + (q >> 3) * 1024 + (q & 7) * 128 +
                                           ((chunk ^ (q & 7)) << 4)) = __float2bfloat16_rn(s[q]);
       if ((t_begin + j + 1) * kKeys > len) {
@@ -412,25 +451,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!(ok = mbar_wait_warp(bar(C::bO(pj & 1)), (pj >> 1) & 1, ctl))) break;
         tc_fence_after();
         if (o_rows) {
-          uint32_t orr[kSlots];
-          tmem_ld16_sync(tO + (pj & 1) * kSlots, orr);
+          uint32_t orr[U];
+          tmem_ld_slots<U>(tO + (pj & 1) * kSlots, orr);
 #pragma unroll
-          for (int q = 0; q < kSlots; ++q)
+          for (int q = 0; q < U; ++q)
             acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(orr[q]));
         }
       }
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) alpha_prev[q] = alpha[q];
+      for (int q = 0; q < U; ++q) alpha_prev[q] = alpha[q];
     }
     if (ok && T > 0) {
       const int pj = T - 1;
       if ((ok = mbar_wait_warp(bar(C::bO(pj & 1)), (pj >> 1) & 1, ctl))) {
         tc_fence_after();
         if (o_rows) {
-          uint32_t orr[kSlots];
-          tmem_ld16_sync(tO + (pj & 1) * kSlots, orr);
+          uint32_t orr[U];
+          tmem_ld_slots<U>(tO + (pj & 1) * kSlots, orr);
 #pragma unroll
-          for (int q = 0; q < kSlots; ++q)
+          for (int q = 0; q < U; ++q)
             acc[q] = fmaf(acc[q], alpha_prev[q], __uint_as_float(orr[q]));
         }
       }
@@ -438,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     // denominator: sum l over the 128 key lanes
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
+    for (int q = 0; q < U; ++q) {
 #pragma unroll
       for (int sh = 16; sh > 0; sh >>= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], sh);
     }
@@ -446,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       float4* dst = reinterpret_cast<float4*>(lsum + warp * kSlots);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < U / 4; ++i)
         dst[i] = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
     }
     softmax_bar();
@@ -454,13 +493,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (failed) *bad_page = 1;  // a failed split spoils the rows
     if (threadIdx.x < kSlots) {
       const int q = threadIdx.x;
-      xm[q] = failed ? -INFINITY : m[q];
-      xl[q] = failed ? 0.f
-                     : lsum[q] + lsum[kSlots + q] + lsum[2 * kSlots + q] + lsum[3 * kSlots + q];
+      const bool none = failed || q >= U;
+      float mq = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < U; ++k) mq = k == q ? m[k] : mq;
+      xm[q] = none ? -INFINITY : mq;
+      xl[q] = none ? 0.f
+                   : lsum[q] + lsum[kSlots + q] + lsum[2 * kSlots + q] + lsum[3 * kSlots + q];
     }
     if (o_rows && r < D) {
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) xo[q * D + r] = acc[q];
+      for (int q = 0; q < U; ++q) xo[q * D + r] = acc[q];
     }
   }
 
@@ -517,17 +560,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int D>
-cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
-  using C = FewCfg<D>;
+template <int D, int U, bool kAlone>
+cudaError_t launch_as(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
+  using C = FewCfg<D, kAlone>;
   CUtensorMap q, k, v;
   if (!paged_tensor_maps(a, D, kSlots / a.G, kKeys, &q, &k, &v)) return cudaErrorInvalidValue;
   const int64_t clusters = static_cast<int64_t>(a.pages.B) * a.pages.kv_heads;
-  if (a.splits == 0)
-    a.splits = paged_default_splits(
-        clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads, C::kSmemBytes);
   if (clusters * a.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  auto kern = sdpa_paged_few_kernel<D>;
+  auto kern = sdpa_paged_few_kernel<D, U, kAlone>;
   static std::atomic<uint64_t> attributes_set{0};
   cudaError_t e = paged_kernel_attributes(reinterpret_cast<const void*>(kern), C::kSmemBytes,
                                           &attributes_set);
@@ -546,6 +586,22 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, q, k, v, paged_params(a, ctl));
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
+  const int64_t clusters = static_cast<int64_t>(a.pages.B) * a.pages.kv_heads;
+  if (a.splits == 0)
+    a.splits = paged_default_splits(
+        clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads,
+        FewCfg<D, false>::kSmemBytes);
+  const bool alone =
+      clusters <= paged_resident_clusters(kThreads, FewCfg<D, true>::kSmemBytes, a.splits);
+  // the softmax's work per tile goes with the slots: 4, 8 or all 16 of them
+  const int64_t rows = static_cast<int64_t>(a.max_new) * a.G;
+  if (rows <= 4) return alone ? launch_as<D, 4, true>(a, ctl) : launch_as<D, 4, false>(a, ctl);
+  if (rows <= 8) return alone ? launch_as<D, 8, true>(a, ctl) : launch_as<D, 8, false>(a, ctl);
+  return alone ? launch_as<D, 16, true>(a, ctl) : launch_as<D, 16, false>(a, ctl);
 }
 
 }  // namespace
