@@ -205,13 +205,15 @@ def test_nan_queries_give_nan_and_stay_in_their_rows(new, splits):
     assert np.array_equal(got, want)
 
 
-@pytest.mark.parametrize("new,G", [(1, 2), (2, 16)])
-def test_more_sequences_than_are_ranked(new, G):
-    """300 sequences, one in seven of them idle, in both kernels."""
+@pytest.mark.parametrize("new,G,d", [(1, 2, 64), (1, 7, 64), (2, 16, 64), (2, 2, 128), (1, 8, 128),
+                                     (1, 16, 128), (3, 16, 128)])
+def test_more_sequences_than_are_ranked(new, G, d):
+    """300 sequences, one in seven of them idle: more than a CTA ranks and than
+    SMs, in both kernels and every number of query slots."""
     rng = np.random.default_rng(156)
     lens = rng.integers(new, 60, 300)
     news = np.where(np.arange(300) % 7, new, 0)
-    x = case(157, list(lens), list(news), G, 1, 16, 64)
+    x = case(157, list(lens), list(news), G, 1, 16, d)
     O, A = ref.sdpa_paged(*x)
     for splits in (1, 2):
         check(run(*x, num_splits=splits, max_new=new, out_dtype=F32), O, A, F32)
