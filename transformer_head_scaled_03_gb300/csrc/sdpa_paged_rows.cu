@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
 
   if (p.splits > 1) {
     // ---- merge the splits: every CTA of the cluster takes a share of the
-    // rows, its first threads one row's weights each, then all of its softmax
-    // threads four columns at a time.
+    // rows, fetches their m and l from all splits, works out the weights, and
+    // sums up the outputs four columns at a time.
     __syncwarp();
     cluster_sync();  // every split's m, l, O and bad-page flag are in its shared memory
     const int S = p.splits;
