@@ -212,3 +212,53 @@ def test_binding_checks_rows():
         mha.kv_pages_fork(K, V, table, lens, lens[:2], lens[:2], lens[:1])
     with pytest.raises(ValueError, match="CUDA"):
         mha.kv_pages_compact(K, V, table, lens, K.clone(), V.clone(), table.clone())
+
+
+def test_binding_refuses_broadcast_rows_and_pools():
+    """expand() gives a stride of 0, which the C ABI reads as "dense": rows
+    past the end of the storage.  Refused before any device is looked at."""
+    K, V, table, lens = cache()
+    bf = torch.bfloat16
+    offs, g, pe = torch.arange(4, dtype=torch.int32), torch.ones(64, dtype=bf), torch.zeros((5, 64))
+    q, kv = torch.zeros((3, 4, 64), dtype=bf), torch.zeros((3, 2, 64), dtype=bf)
+    flat = lambda x: x[:1].expand_as(x)
+    refused = lambda what: pytest.raises(ValueError, match=what)
+    with refused("Q.*evenly spaced"):
+        mha.sdpa_paged(flat(q), K, V, table, lens, offs)
+    append = lambda q=q, k=kv, v=kv, K=K, V=V: mha.qk_norm_rope_paged(
+        q, k, v, g, g, pe, K, V, table, lens, offs)
+    for name, kw in (("Q", dict(q=flat(q))), ("K", dict(k=flat(kv))), ("V", dict(v=flat(kv)))):
+        with refused(f"{name}.*evenly spaced"):
+            append(**kw)
+    # pools that are one page, or one layer, many times
+    layered = lambda x: x[None].expand(3, *x.shape)
+    two = lens[:2]
+    for pool in (flat, layered):
+        with refused("pages and layers"):
+            mha.sdpa_paged(q, pool(K), pool(V), table, lens, offs)
+        with refused("pages and layers"):
+            append(K=pool(K), V=pool(V))
+        with refused("pages and layers"):
+            mha.kv_pages_fork(pool(K), pool(V), table, lens, two, two, two)
+        with refused("pages and layers"):
+            mha.kv_pages_compact(pool(K), pool(V), table, lens, K, V, table)
+        with refused("pages and layers"):
+            mha.kv_pages_compact(K, V, table, lens, pool(K), pool(V), table)
+    # training rows: over the tokens of one item, over items of one token, over both
+    for B, L in ((1, 5), (5, 1), (2, 5)):
+        x = torch.zeros((1, 1, 4, 64)).expand(B, L, 4, 64)
+        dense, dy, g = torch.zeros((B, L, 4, 64)), torch.zeros((B, 4, L, 64)), torch.ones(64)
+        for pair in ((x, dense), (dense, x)):
+            with refused("evenly spaced"):
+                mha.qk_norm_rope(*pair, g, g, pe)
+            with refused("evenly spaced"):
+                mha.qk_norm_rope_backward(*pair, g, g, pe, dy, dy)
+
+
+def test_binding_refuses_broadcast_gradient_outputs(monkeypatch):
+    """The same for the given dQ and dK, which are looked at after the devices."""
+    monkeypatch.setattr(mha._binding, "_launch_on", lambda *a: 0)
+    x, dy, g = torch.zeros((1, 5, 4, 64)), torch.zeros((1, 4, 5, 64)), torch.ones(64)
+    for out in ((x[:, :1].expand_as(x), x.clone()), (x.clone(), x[:, :1].expand_as(x))):
+        with pytest.raises(ValueError, match="evenly spaced"):
+            mha.qk_norm_rope_backward(x, x, g, g, torch.zeros((5, 64)), dy, dy, out=out)

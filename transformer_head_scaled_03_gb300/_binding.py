@@ -392,6 +392,9 @@ def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
     P, Hkv, ps, d = shape[-4:]
     if strides[-3:] != (ps * d, d, 1) or V_pages.stride() != strides:
         raise ValueError("a page must be contiguous, and K_pages and V_pages laid out alike")
+    # the library reads a stride of 0 as "dense"
+    if P > 1 and strides[-4] == 0 or len(shape) == 5 and shape[0] > 1 and strides[0] == 0:
+        raise ValueError("pages and layers must not be broadcast")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
     B, cols = page_table.shape
@@ -412,7 +415,11 @@ def _packed(name, x, heads, d, dtype):
     st, sh, sc = x.stride()
     if sc != 1 or (heads > 1 and sh != d):
         raise ValueError(f"{name}'s heads must be contiguous")
-    return st if shape[0] > 1 else heads * d
+    if shape[0] <= 1:
+        return heads * d
+    if st == 0:     # a broadcast: the library reads 0 as "dense"
+        raise ValueError(f"{name}'s tokens must be evenly spaced, a row or more apart")
+    return st
 
 
 def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: int | None = None,
@@ -453,8 +460,9 @@ def _token_rows(name, x, B, L, d, dtype):
         raise ValueError(f"{name} must be [{B}, {L}, heads, {d}] {dtype}")
     heads, (sb, sl, sh, sc) = shape[2], x.stride()
     ts = sl if L > 1 else sb if B > 1 else heads * d
-    if (sc != 1 and d > 1 or heads > 1 and sh != d or B > 1 and L > 1 and sb != L * ts) \
-            and x.numel():
+    # a stride of 0 is a broadcast, which the library would read as "dense"
+    if (sc != 1 and d > 1 or heads > 1 and sh != d or B > 1 and L > 1 and sb != L * ts
+            or ts == 0) and x.numel():
         raise ValueError(f"{name}'s tokens must be evenly spaced and its heads contiguous")
     return heads, ts
 
