@@ -262,3 +262,17 @@ def test_binding_refuses_broadcast_gradient_outputs(monkeypatch):
     for out in ((x[:, :1].expand_as(x), x.clone()), (x.clone(), x[:, :1].expand_as(x))):
         with pytest.raises(ValueError, match="evenly spaced"):
             mha.qk_norm_rope_backward(x, x, g, g, torch.zeros((5, 64)), dy, dy, out=out)
+
+
+def test_binding_refuses_scattered_workspaces():
+    """A workspace's size is counted from its elements, so they must lie one
+    after the other: one byte expanded to a million would pass for a megabyte."""
+    x, dy, g = torch.zeros((1, 5, 4, 64)), torch.zeros((1, 4, 5, 64)), torch.ones(64)
+    K, V, table, lens = cache()
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 22),
+               torch.zeros(1 << 23, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            mha.qk_norm_rope_backward(x, x, g, g, torch.zeros((5, 64)), dy, dy, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            mha.kv_pages_compact(K, V, table, lens, K.clone(), V.clone(), table.clone(),
+                                 workspace=ws)

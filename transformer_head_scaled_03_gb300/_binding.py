@@ -382,6 +382,12 @@ def _new(stream, shape, dtype, device):
     return t
 
 
+def _check_workspace(workspace):
+    """A given workspace's size is counted from its elements."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
     """The mha_kv_pages of pools [P, Hkv, page, d] or [layers, P, Hkv, page, d]
     (pages and layers at any stride, a page itself contiguous)."""
@@ -524,6 +530,7 @@ def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int 
     if dQo.shape != (B, H, L, d) or dKo.shape != (B, Hkv, L, d) \
             or not dQo.is_contiguous() or not dKo.is_contiguous():
         raise ValueError("dQo and dKo must be contiguous [B, heads, L, d]")
+    _check_workspace(workspace)
     on = _launch_on(stream, Q, K, gamma_q, gamma_k, pe, dQo, dKo,
                     Q if positions is None else positions, Q if workspace is None else workspace,
                     *(() if out is None else out))
@@ -606,6 +613,7 @@ def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, tab
     in order; table_out is the renumbered page table.  Returns n (int32 [1])."""
     src = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
     dst = _kv_pages(K_out, V_out, table_out, kv_lengths)
+    _check_workspace(workspace)
     on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
                     K_pages if workspace is None else workspace)
     dev = _lib or lib()
