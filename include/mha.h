@@ -432,8 +432,10 @@ size_t qk_norm_rope_backward_workspace_bytes(int d);
  * 128, rope_dim a multiple of 16.
  * Checked on the device (MHA_ERR_DEVICE): kv_lengths[b] in [n_b,
  * table_cols*page_size], positions below pe_rows, page numbers -- such a
- * token's Qo rows are written as zeros and no page is touched for it.
- * Tokens that belong to no sequence are passed over.
+ * token's Qo rows are written as zeros and no page is touched for it; offsets
+ * ascending in [0, T], where a token meets them -- nothing is written for it.
+ * Tokens that belong to no sequence, ahead of the first or behind the last,
+ * are passed over.
  * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
  */
 mha_status qk_norm_rope_paged(const void *Q, int64_t q_token_stride,

@@ -327,3 +327,36 @@ def test_paged_empty():
     a = args(1, [0, 0])
     mha.qk_norm_rope_paged(*a)
     assert mha.mha_check() == mha.MHA_OK and torch.equal(a[6], dev(K, BF))
+
+
+@pytest.mark.parametrize("lead", [1, 9, 40])
+@pytest.mark.parametrize("new", [[1, 1, 1], [0, 5, 12]])
+def test_paged_tokens_ahead_of_the_first_sequence(lead, new):
+    """q_offsets[0] > 0 is allowed: the tokens ahead of it belong to no
+    sequence and are passed over, like those behind the last one."""
+    K, V, table, lens, offs, parts, gammas = paged_case(95, [40, 50, 30], new, 4, 2, 16, 64, 64,
+                                                        extra=lead + 3)
+    g, pe = [dev(x, BF) for x in gammas], mha.sinusoidal_pe(64, 64)
+    T = int(offs[-1])
+
+    def call(first):
+        kp, vp = dev(K, BF), dev(V, BF)
+        rows = [dev(np.roll(x, first, 0), BF) for x in parts]
+        out = torch.full(rows[0].shape, 7.0, dtype=BF, device="cuda")
+        mha.qk_norm_rope_paged(*rows, *g, pe, kp, vp, i32(table), i32(lens), i32(offs + first),
+                               out=out)
+        assert mha.mha_check() == mha.MHA_OK
+        assert torch.all(out[:first] == 7.0) and torch.all(out[first + T:] == 7.0)
+        return out[first:first + T], kp, vp
+
+    for a, b in zip(call(0), call(lead)):
+        assert torch.equal(a, b)
+
+
+def test_paged_offsets_that_do_not_ascend_are_reported():
+    K, V, table, lens, offs, parts, gammas = paged_case(96, [40, 50, 30], [4, 4, 4], 4, 2, 16, 64, 64)
+    g, pe = [dev(x, BF) for x in gammas], mha.sinusoidal_pe(64, 64)
+    for o in ([-1, 4, 8, 12], [6, 4, 8, 12], [0, 4, 8, 13], [0, 9, 12, 2], [0, 9, 1, 2]):
+        mha.qk_norm_rope_paged(*(dev(x, BF) for x in parts), *g, pe, dev(K, BF), dev(V, BF),
+                               i32(table), i32(lens), i32(o))
+        assert mha.mha_check() == mha.MHA_ERR_DEVICE, o

@@ -289,3 +289,17 @@ def test_rows_beyond_32_bit_offsets():
                              max_new=m, out_dtype=F32)
         assert mha.mha_check() == mha.MHA_OK
         check(to_np(got), O, A, F32)
+
+
+@pytest.mark.parametrize("lead", [1, 40])
+@pytest.mark.parametrize("new", [[1, 1, 1], [0, 5, 33]])
+def test_tokens_ahead_of_the_first_sequence_are_passed_over(lead, new):
+    """q_offsets[0] > 0: the same bits as without them, their rows untouched."""
+    Q, K, V, table, lens, offs = case(195, [90, 80, 70], new, 4, 2, 16, 64)
+    args = [dev(K, BF), dev(V, BF), i32(table), i32(lens)]
+    want = mha.sdpa_paged(dev(Q, BF), *args, i32(offs), max_new=max(new))
+    wide = dev(np.concatenate((np.full((lead, *Q.shape[1:]), np.nan, np.float32), Q)), BF)
+    out = torch.full(wide.shape, 7.0, dtype=BF, device="cuda")
+    mha.sdpa_paged(wide, *args, i32(offs + lead), max_new=max(new), out=out)
+    assert mha.mha_check() == mha.MHA_OK
+    assert torch.all(out[:lead] == 7.0) and torch.equal(out[lead:], want)

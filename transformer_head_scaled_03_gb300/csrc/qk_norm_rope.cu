@@ -676,9 +676,11 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (b < pg.B) {
       const int q0 = __ldg(p.q_offsets + b), q1 = __ldg(p.q_offsets + b + 1);
       const int len = __ldg(pg.kv_len + b);
-      if (q0 < 0 || t < q0 || t >= q1 || q1 > p.T) {
+      // ascending offsets put t into [q0, q1), or ahead of the first sequence,
+      // where it is nobody's
+      if (q0 < 0 || q1 < q0 || q1 > p.T || t >= q1 || (b > 0 && t < q0)) {
         if (lane == 0) atomicOr(p.err, kErrPages);
-      } else {
+      } else if (t >= q0) {
         const int n = q1 - q0;
         int page = -1;
         pos = len - n + (t - q0);
