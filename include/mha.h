@@ -293,6 +293,7 @@ mha_status embed_pe_forward(const int32_t *ids, const void *table, int vocab,
  *          row j % page_size of page page_table[b][j / page_size].  Entries
  *          behind a sequence's last held page are never read.
  *   kv_lengths : device int32 [B], tokens held by each sequence.
+ *   B : sequences; with none, page_table and kv_lengths may be NULL.
  * page_size is a power of two from 16 to 256; table_cols*page_size <= 2^30.
  */
 typedef struct {

@@ -276,3 +276,21 @@ def test_binding_refuses_scattered_workspaces():
         with pytest.raises(ValueError, match="workspace"):
             mha.kv_pages_compact(K, V, table, lens, K.clone(), V.clone(), table.clone(),
                                  workspace=ws)
+
+
+def test_no_sequences_need_no_table(lib):
+    """B = 0 as a binding passes it: an empty tensor's pointer is null."""
+    none = dict(B=0, page_table=None, kv_lengths=None)
+    assert paged(lib, pg=pages(**none), offs=None) == OK
+    assert lib.kv_pages_fork(pages(**none), None, None, None, 0, None) == OK
+    assert lib.qk_norm_rope_paged(P, 0, P, 0, P, 0, P, P, P, 9, 64, 0, P2, pages(**none), 0, P, 5, 4,
+                                  1e-6, None) == OK
+    # with sequences both are needed, the destination's table too
+    assert paged(lib, pg=pages(kv_lengths=None)) == INVALID
+    need = lib.kv_pages_compact_workspace_bytes(10)
+    to = dict(K=P3, V=0x40000, page_table=None)
+    assert lib.kv_pages_compact(pages(), pages(**to), P, P, need, None) == INVALID
+    # and what else is checked still is
+    assert paged(lib, pg=pages(**none, d=0)) == INVALID
+    assert paged(lib, pg=pages(**none), max_new=-1) == INVALID
+    assert lib.kv_pages_compact(pages(**none), pages(**{**none, **to}), None, P, need, None) == INVALID

@@ -303,3 +303,27 @@ def test_tokens_ahead_of_the_first_sequence_are_passed_over(lead, new):
     mha.sdpa_paged(wide, *args, i32(offs + lead), max_new=max(new), out=out)
     assert mha.mha_check() == mha.MHA_OK
     assert torch.all(out[:lead] == 7.0) and torch.equal(out[lead:], want)
+
+
+def test_a_batch_without_sequences():
+    """B = 0 through every paged call: the tokens are nobody's, no page is held."""
+    Hkv, ps, d = 2, 16, 64
+    kp = torch.randn((5, Hkv, ps, d), device="cuda").to(BF)
+    vp = torch.randn((5, Hkv, ps, d), device="cuda").to(BF)
+    keep = kp.clone(), vp.clone()
+    table = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    g, pe = torch.ones(d, dtype=BF, device="cuda"), mha.sinusoidal_pe(8, d)
+    for T in (0, 3):
+        q, k = (torch.randn((T, h, d), device="cuda").to(BF) for h in (4, Hkv))
+        for call in (lambda out: mha.qk_norm_rope_paged(q, k, k, g, g, pe, kp, vp, table, none,
+                                                        i32([0]), out=out),
+                     lambda out: mha.sdpa_paged(q, kp, vp, table, none, i32([0]), out=out)):
+            out = torch.full_like(q, 7.0)
+            assert call(out) is out and torch.all(out == 7.0)
+    mha.kv_pages_fork(kp, vp, table, none, none, none, none)
+    dst = torch.full_like(kp, 3.0), torch.full_like(vp, 5.0)
+    n = mha.kv_pages_compact(kp, vp, table, none, *dst, torch.empty_like(table))
+    assert mha.mha_check() == mha.MHA_OK and n.tolist() == [0]
+    assert torch.all(dst[0] == 3.0) and torch.all(dst[1] == 5.0)
+    assert torch.equal(kp, keep[0]) and torch.equal(vp, keep[1])

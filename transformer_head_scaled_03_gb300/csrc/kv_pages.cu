@@ -20,7 +20,9 @@
 namespace mha {
 
 mha_status validate_pages(const mha_kv_pages* p) {
-  if (!p || !p->K || !p->V || !p->page_table || !p->kv_lengths) return MHA_ERR_INVALID_ARG;
+  if (!p || !p->K || !p->V) return MHA_ERR_INVALID_ARG;
+  // without sequences there is no table to point to
+  if (p->B > 0 && (!p->page_table || !p->kv_lengths)) return MHA_ERR_INVALID_ARG;
   if (p->dtype != MHA_BF16 && p->dtype != MHA_F32) return MHA_ERR_INVALID_ARG;
   if (p->num_pages < 1 || p->page_size < 1 || p->kv_heads < 1 || p->d < 1 || p->layers < 1 ||
       p->B < 0 || p->table_cols < 1)
@@ -309,7 +311,7 @@ mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, in
       dst->B != src->B || dst->table_cols < src->table_cols)
     return MHA_ERR_INVALID_ARG;
   if (dst->K == src->K || dst->V == src->V || dst->K == src->V || dst->V == src->K ||
-      dst->page_table == src->page_table)
+      (dst->page_table && dst->page_table == src->page_table))
     return MHA_ERR_INVALID_ARG;
   if (!n_live || (reinterpret_cast<uintptr_t>(n_live) & 3u) || !workspace ||
       (reinterpret_cast<uintptr_t>(workspace) & 15u) ||
