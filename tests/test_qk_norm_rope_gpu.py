@@ -360,3 +360,47 @@ def test_paged_offsets_that_do_not_ascend_are_reported():
         mha.qk_norm_rope_paged(*(dev(x, BF) for x in parts), *g, pe, dev(K, BF), dev(V, BF),
                                i32(table), i32(lens), i32(o))
         assert mha.mha_check() == mha.MHA_ERR_DEVICE, o
+
+
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("dt,d,r", [(BF, 64, 64), (F32, 64, 32), (F32, 128, 128), (F32, 96, 32)])
+@pytest.mark.parametrize("pairing", [mha.ROPE_INTERLEAVED, mha.ROPE_HALF])
+def test_bad_positions_give_zeros_whatever_gamma_holds(value, dt, d, r, pairing):
+    rng = np.random.default_rng(55)
+    B, L, H, Hkv = 1, 7, 3, 2
+    q, k = (dev(draws(rng, (B, L, h, d), dt), dt) for h in (H, Hkv))
+    gammas = draws(rng, (d,), dt), draws(rng, (d,), dt)
+    for x in gammas:
+        x[[0, d // 2, d - 1]] = value
+    g = [dev(x, dt) for x in gammas]
+    pe = mha.sinusoidal_pe(10, r)
+    dys = [dev(draws(rng, (B, h, L, d), F32)) for h in (H, Hkv)]
+    pos, bad = i32([[0, 10, 9, -1, 3, 2 ** 31 - 1, 4]]), [1, 3, 5]
+    ys = mha.qk_norm_rope(q, k, *g, pe, positions=pos, pairing=pairing)
+    assert mha.mha_check() == mha.MHA_ERR_DEVICE
+    grads = mha.qk_norm_rope_backward(q, k, *g, pe, *dys, positions=pos, pairing=pairing)
+    assert mha.mha_check() == mha.MHA_ERR_DEVICE
+    for y, dx in zip(ys, grads):
+        assert torch.all(y[:, :, bad] == 0) and torch.all(dx[:, bad] == 0)
+        assert not torch.all(torch.isfinite(y)) and not torch.all(torch.isfinite(dx))
+    # dgamma takes no gamma: the other rows' sums, finite
+    assert all(torch.all(torch.isfinite(x)) for x in grads[2:])
+
+
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pairing", [mha.ROPE_INTERLEAVED, mha.ROPE_HALF])
+def test_paged_bad_entries_give_zeros_whatever_gamma_holds(value, d, pairing):
+    K, V, table, lens, offs, parts, gammas = paged_case(97, [40, 50, 30], [4, 4, 4], 4, 2, 16, d, d)
+    for x in gammas:
+        x[[0, d // 2, d - 1]] = value
+    lens[0], table[1] = 3, K.shape[0]           # a length below its new tokens, pages out of range
+    kp, vp = dev(K, BF), dev(V, BF)
+    out = torch.full(parts[0].shape, 7.0, dtype=BF, device="cuda")
+    mha.qk_norm_rope_paged(*(dev(x, BF) for x in parts), *(dev(x, BF) for x in gammas),
+                           mha.sinusoidal_pe(64, d), kp, vp, i32(table), i32(lens), i32(offs),
+                           pairing=pairing, out=out)
+    assert mha.mha_check() == mha.MHA_ERR_DEVICE
+    assert torch.all(out[:8] == 0) and not torch.all(torch.isfinite(out[8:]))
+    others = [p for p in range(K.shape[0]) if p not in table[2]]
+    assert torch.equal(kp[others], dev(K, BF)[others]) and torch.equal(vp[others], dev(V, BF)[others])

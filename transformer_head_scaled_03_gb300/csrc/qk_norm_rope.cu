@@ -564,7 +564,12 @@ __device__ __forceinline__ void norm_rope_vec_bwd_part(const TrainArgs& p, int w
     }
     const int h = h0 + c.round * V::kRows;
     if (c.here && h < heads) {
-      if (!c.pe) atomicOr(p.err, kErrPosition);
+      if (!c.pe) {
+        // zeros so far, unless gamma is not finite
+        atomicOr(p.err, kErrPosition);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
+      }
       T* dx = static_cast<T*>(p.dx[w]) + c.token * p.dts[w] + static_cast<int64_t>(h) * D;
       store8(dx + at.a, x);
       store8(dx + at.b, y);
@@ -738,8 +743,12 @@ __global__ void __launch_bounds__(32 * kWarps)
     turns.load(p.pe + static_cast<int64_t>(max(pos, 0)) * p.r, at.a, at.b, at.turns && pos >= 0,
                HALF);
     norm_rope_vec<D, HALF>(a, b, w == 0 ? p.gq : p.gk, at, turns, p.eps);
-    // a bad entry: the query row is zeros (a and b are), the page untouched
+    // a bad entry: the query row is zeros, the page untouched
     if (pos == -1 || (w == 1 && pos < 0)) continue;
+    if (pos < 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = b[i] = make_float2(0.f, 0.f);
+    }
     store8(y + at.a, a);
     store8(y + at.b, b);
   }
