@@ -404,3 +404,18 @@ def test_paged_bad_entries_give_zeros_whatever_gamma_holds(value, d, pairing):
     assert torch.all(out[:8] == 0) and not torch.all(torch.isfinite(out[8:]))
     others = [p for p in range(K.shape[0]) if p not in table[2]]
     assert torch.equal(kp[others], dev(K, BF)[others]) and torch.equal(vp[others], dev(V, BF)[others])
+
+
+@pytest.mark.parametrize("d", [64, 96])
+def test_no_heads_give_zero_gamma_gradients(d):
+    """H = Hkv = 0: dgamma is overwritten all the same, with a sum of nothing."""
+    x = torch.empty((2, 5, 0, d), dtype=BF, device="cuda")
+    dy = torch.empty((2, 0, 5, d), dtype=F32, device="cuda")
+    g, pe = torch.ones(d, dtype=BF, device="cuda"), mha.sinusoidal_pe(5, d)
+    for _ in range(3):
+        # the pieces that the allocator hands out next are not zeros
+        junk = [torch.full((n,), 7.0, device="cuda") for n in (2 * d,) * 8]
+        del junk
+        dq, dk, dgq, dgk = mha.qk_norm_rope_backward(x, x, g, g, pe, dy, dy)
+        assert dq.shape == dk.shape == (2, 5, 0, d)
+        assert torch.all(dgq == 0) and torch.all(dgk == 0) and mha.mha_check() == mha.MHA_OK

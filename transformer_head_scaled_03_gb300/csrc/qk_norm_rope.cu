@@ -915,6 +915,7 @@ mha_status qk_norm_rope_backward(const void* Q, int64_t q_token_stride, const vo
               {dq_token_stride, dk_token_stride}, static_cast<float*>(workspace)};
   float* dgamma[2] = {dgamma_q, dgamma_k};
   const bool rows_empty = B == 0 || L == 0;
+  if (H + Hkv == 0 && !dgamma_q && !dgamma_k) return MHA_OK;
   for (int w = 0; w < 2; ++w) {
     if (p.heads[w] == 0 && !dgamma[w]) continue;
     if (bad_ptr(dgamma[w], 16)) return MHA_ERR_INVALID_ARG;
@@ -925,7 +926,6 @@ mha_status qk_norm_rope_backward(const void* Q, int64_t q_token_stride, const vo
     if (bad_ptr(p.gamma[w], 16) || bad_ptr(p.dy[w], 16) || p.dx[w] == p.x[w] || p.dx[w] == p.dy[w])
       return MHA_ERR_INVALID_ARG;
   }
-  if (H + Hkv == 0) return MHA_OK;
   if (bad_ptr(workspace, 16) || workspace_bytes < qk_norm_rope_backward_workspace_bytes(d))
     return MHA_ERR_INVALID_ARG;
   DeviceCtl ctl;
@@ -934,7 +934,7 @@ mha_status qk_norm_rope_backward(const void* Q, int64_t q_token_stride, const vo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(B) * L * (H > Hkv ? H : Hkv);
   const VecShape v = vec_shape(static_cast<int64_t>(B) * L, H > Hkv ? H : Hkv, d);
-  unsigned blocks = vec ? grid_for(v.items, 2) : grid_for(rows, 4);
+  unsigned blocks = rows == 0 ? 0 : vec ? grid_for(v.items, 2) : grid_for(rows, 4);
   if (blocks > kMaxGradBlocks) blocks = kMaxGradBlocks;
   if (blocks) {
     if (vec)
