@@ -294,3 +294,26 @@ def test_no_sequences_need_no_table(lib):
     assert paged(lib, pg=pages(**none, d=0)) == INVALID
     assert paged(lib, pg=pages(**none), max_new=-1) == INVALID
     assert lib.kv_pages_compact(pages(**none), pages(**{**none, **to}), None, P, need, None) == INVALID
+
+
+def test_strides_of_size_one_do_not_count():
+    """Pages of one head, rows first; one page; one layer: contiguous pages
+    whatever torch says of the stride of a size of 1."""
+    K, V, table, lens = cache(Hkv=1)
+    Q, offs = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.arange(4, dtype=torch.int32)
+    rows_first = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)
+    one_page = lambda x: x[:1].as_strided((1, 1, 16, 64), (7, 5, 64, 1))
+    one_layer = lambda x: x.as_strided((1, *x.shape), (3, *x.stride()))
+    for a, b in ((rows_first(K), V), (K, rows_first(V)), (one_page(K), V[:1]),
+                 (one_layer(K), V[None]), (one_page(K), one_page(V))):
+        with pytest.raises(ValueError, match="CUDA"):
+            mha.sdpa_paged(Q, a, b, table, lens, offs)
+    got = mha._binding._kv_pages(one_page(K), V[:1], table, lens)
+    assert (got.num_pages, got.layers, got.page_stride, got.layer_stride) == (1, 1, 0, 0)
+    got = mha._binding._kv_pages(one_layer(rows_first(K)), V[None], table, lens)
+    assert (got.num_pages, got.layers, got.page_stride, got.layer_stride) == (6, 1, 16 * 64, 0)
+    # two heads' rows must follow each other, and K and V be alike, as before
+    K, V, table, lens = cache(Hkv=2)
+    for a, b in ((rows_first(K), rows_first(V)), (torch.cat((K, K))[::2], V)):
+        with pytest.raises(ValueError, match="laid out alike"):
+            mha.sdpa_paged(Q, a, b, table, lens, offs)

@@ -391,22 +391,28 @@ def _check_workspace(workspace):
 def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
     """The mha_kv_pages of pools [P, Hkv, page, d] or [layers, P, Hkv, page, d]
     (pages and layers at any stride, a page itself contiguous)."""
-    shape, strides = K_pages.shape, K_pages.stride()
+    shape = K_pages.shape
     if len(shape) not in (4, 5) or V_pages.shape != shape or V_pages.dtype != K_pages.dtype:
         raise ValueError("K_pages and V_pages must be alike, [P, Hkv, page, d] or "
                          "[layers, P, Hkv, page, d]")
     P, Hkv, ps, d = shape[-4:]
-    if strides[-3:] != (ps * d, d, 1) or V_pages.stride() != strides:
-        raise ValueError("a page must be contiguous, and K_pages and V_pages laid out alike")
+    layers = shape[0] if len(shape) == 5 else 1
+    strides = K_pages.stride()
+    if V_pages.stride() != strides or strides[-3:] != (ps * d, d, 1) or P == 1:
+        # a size of 1 has any stride: 0, as good as dense, stands for it
+        strides, other = (
+            (s[0] if layers > 1 else 0, s[-4] if P > 1 else 0, s[-3] if Hkv > 1 else ps * d, *s[-2:])
+            for s in (strides, V_pages.stride()))
+        if strides[-3:] != (ps * d, d, 1) or other != strides:
+            raise ValueError("a page must be contiguous, and K_pages and V_pages laid out alike")
     # the library reads a stride of 0 as "dense"
-    if P > 1 and strides[-4] == 0 or len(shape) == 5 and shape[0] > 1 and strides[0] == 0:
+    if P > 1 and strides[-4] == 0 or layers > 1 and strides[0] == 0:
         raise ValueError("pages and layers must not be broadcast")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
     B, cols = page_table.shape
     _int32("page_table", page_table, B, cols)
     _int32("kv_lengths", kv_lengths, B)
-    layers = shape[0] if len(shape) == 5 else 1
     return KvPages(K_pages.data_ptr(), V_pages.data_ptr(), _dtype_code(K_pages.dtype), P, ps, Hkv,
                    d, layers, strides[-4], strides[0] if layers > 1 else 0,
                    page_table.data_ptr(), kv_lengths.data_ptr(), B, cols)
