@@ -20,7 +20,7 @@ import transformer_head_scaled_03_gb300 as mha
 from transformer_head_scaled_03_gb300 import build as mha_build
 from transformer_head_scaled_03_gb300.inputs import round_to_bf16
 from tests.gpu_util import to_np
-from tests.paged_util import dev, i32
+from tests.paged_util import dev, i32, make_pages
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,71 @@ def test_training_step_through_the_attention():
         _, dg, _, mag = ref.qk_norm_rope_backward(to_np(x), to_np(g), rows,
                                                   to_np(dy).transpose(0, 2, 1, 3), 0, 1e-6)
         assert np.all(np.abs(to_np(got) - dg) <= (B * L * H + 32) * 2.0 ** -24 * mag + 1e-35)
+
+
+def side_stream_calls(rng):
+    """(name, call(stream), tensors that it updates in place) for every paged
+    and norm call on state of its own."""
+    H, Hkv, d, ps, lens = 4, 2, 64, 16, [70, 41, 0, 0]
+    K, V, table, offs, free = make_pages(rng, lens, [3, 2, 0, 0], Hkv, ps, d, bf16=True, spare=4)
+    state = lambda: [dev(K, BF), dev(V, BF), i32(table), i32(lens)]
+    T = int(offs[-1])
+    draw = lambda *shape, dt=BF: dev(rng.standard_normal(shape, dtype=np.float32), dt)
+    q, k, v = draw(T, H, d), draw(T, Hkv, d), draw(T, Hkv, d)
+    x, y = draw(2, 300, H, d), draw(2, 300, Hkv, d)
+    dx, dy = draw(2, H, 300, d, dt=torch.float32), draw(2, Hkv, 300, d)
+    g, pe = draw(d), mha.sinusoidal_pe(300, d)
+    o, pair = i32(offs), [i32([0, 1]), i32([2, 3]), i32(free[:2])]
+    a, f, c, p = state(), state(), state(), state()
+    dst = [torch.zeros_like(c[0]), torch.zeros_like(c[1]), torch.full_like(c[2], -1)]
+    return [
+        ("qk_norm_rope", lambda s: mha.qk_norm_rope(x, y, g, g, pe, stream=s), []),
+        ("qk_norm_rope_backward",
+         lambda s: mha.qk_norm_rope_backward(x, y, g, g, pe, dx, dy, stream=s), []),
+        ("qk_norm_rope_paged",
+         lambda s: [mha.qk_norm_rope_paged(q, k, v, g, g, pe, *a, o, stream=s)], a[:2]),
+        ("sdpa_paged", lambda s: [mha.sdpa_paged(q, *p, o, max_new=3, stream=s)], []),
+        ("kv_pages_fork", lambda s: mha.kv_pages_fork(*f, *pair, stream=s) or [], f),
+        ("kv_pages_compact", lambda s: [mha.kv_pages_compact(*c, *dst, stream=s)], dst),
+    ]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_calls_on_a_side_stream(which):
+    """The bits of the current stream's calls; and while a call still waits on
+    the side stream, what the current stream allocates and writes meanwhile
+    lies on none of the call's outputs or workspace."""
+    name, call, touched = side_stream_calls(np.random.default_rng(300))[which]
+    want = [t.clone() for t in (*call(None), *touched)]
+    torch.cuda.synchronize()
+    name, call, touched = side_stream_calls(np.random.default_rng(300))[which]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)       # about 10 ms
+    got = list(call(s))
+    over = [torch.full((n,), -7.0, device="cuda") for n in (4, 64, 1024, 1 << 16, 1 << 18, 1 << 19)
+            for _ in range(4)]
+    torch.cuda.synchronize()
+    assert mha.mha_check() == mha.MHA_OK, name
+    assert all(torch.equal(a, b) for a, b in zip(want, [*got, *touched])), name
+    assert all(torch.all(t == -7.0) for t in over)
+    # outputs given up while the call waits: their memory is not handed out before it has run
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    gone = call(s)
+    sizes = [(t.shape, t.dtype) for t in gone]
+    del gone
+    over = [torch.full(shape, -7, dtype=dt, device="cuda") for shape, dt in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.all(t == -7) for t in over), name
+    mha.mha_check()                         # a second fork of the same pairs is another's matter
+
+
+def test_paged_calls_refuse_streams_of_another_device():
+    """On the host, before anything is launched."""
+    for name, call, _ in side_stream_calls(np.random.default_rng(301)):
+        class Elsewhere:
+            device_index, cuda_stream = 1 + torch.cuda.current_device(), 0
+        with pytest.raises(ValueError, match="current device"):
+            call(Elsewhere())
