@@ -139,7 +139,6 @@ mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages*
     return MHA_ERR_INVALID_ARG;
   DeviceCtl ctl;
   if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
-  const float sc = scale == 0.f ? static_cast<float>(1.0 / sqrt(static_cast<double>(d))) : scale;
   PagedSdpaArgs a;
   a.Q = Q;
   a.q_stride = q_token_stride;
