@@ -322,13 +322,17 @@ typedef struct {
  *       H / kv_heads <= 128.
  *   max_new : the largest n_b, 1 <= max_new (0 will do for T = 0).  Up to 16
  *       rows (max_new times the query heads of a kv head) take a kernel of
- *       their own, so a tight bound matters while decoding.
+ *       their own, so a tight bound matters while decoding; one kernel serves
+ *       all sequences of a call.
  *   scale : as for sdpa_forward (0 selects 1/sqrt(d)).
  *   mask_kind : MHA_MASK_CAUSAL_BOTTOM_RIGHT (query i of n_b sees the tokens
  *       j <= kv_lengths[b] - n_b + i) or MHA_MASK_NONE (it sees all).
  *   num_splits : CTAs that share one block's keys, 1..16, merged exactly
  *       through one thread-block cluster; 0 picks a default.
  * The cache is pages->dtype BF16 with d in {64, 128}; `layer` picks the pool.
+ * Scores, exponentials and sums are fp32.  The weights are rounded to bf16
+ * before they meet V, as sdpa_forward's are, whatever out_dtype: an output
+ * moves by up to 2^-8 sum_j w_j |v_j|, beside its own rounding.
  * Rows of a page that lie behind the sequence's length may hold anything.
  * The keys and values that a sequence holds must be finite, those of new
  * tokens that a query does not see among them.  A NaN in a query reaches that
@@ -338,7 +342,8 @@ typedef struct {
  * page numbers in [0, num_pages) -- every row that would read through the bad
  * entry is written as zeros, and other rows of that sequence may be;
  * q_offsets ascending in [0, T] and n_b <= max_new -- nothing is written for
- * such a sequence.
+ * such a sequence.  Where offsets descend, ranges overlap: rows of the other
+ * sequences may be left unwritten too, or hold either one's result.
  * T or B may be 0.  The call allocates nothing and needs no workspace.
  * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
  */
@@ -372,7 +377,10 @@ enum {
  *   positions : device int32 [B, L], each in [0, pe_rows) (checked on the
  *        device: MHA_ERR_DEVICE, the token's rows written as zeros), or NULL:
  *        token l is at pos_offset + l, and pos_offset + L <= pe_rows.
- *   Qo [B, H, L, d], Ko [B, Hkv, L, d] : of dtype, as sdpa_forward takes them.
+ *   Qo [B, H, L, d], Ko [B, Hkv, L, d] : of dtype.  With Hkv = H that is what
+ *       sdpa_forward, sdpa_forward_lse and sdpa_backward take (the last two in
+ *       BF16 alone); they know no shared key heads, so for Hkv < H the caller
+ *       repeats Ko's heads, and sums dKo over the copies.
  *   eps : finite, > 0.
  * dtype BF16 or F32; the arithmetic is fp32, rounded once.  2 <= d <= 256,
  * rope_dim even in [2, d].  H or Hkv may be 0 (that part is skipped).
@@ -400,7 +408,8 @@ mha_status qk_norm_rope_forward(const void *Q, int64_t q_token_stride,
  *   dgamma_q, dgamma_k : fp32 [d], overwritten; 16-byte aligned.
  *   workspace : device, 16-byte aligned, at least
  *       qk_norm_rope_backward_workspace_bytes(d) bytes.
- * The sums run in a fixed order: equal calls give equal bits.  A token with a
+ * The sums run in a fixed order, in fp32 over a block's rows and fp64 over the
+ * blocks: equal calls give equal bits.  A token with a
  * bad position gets zero rows and adds nothing to dgamma.
  * Other arguments, support and errors as for qk_norm_rope_forward.
  */

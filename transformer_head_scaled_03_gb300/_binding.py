@@ -442,7 +442,8 @@ def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: 
     are q_offsets[b]..q_offsets[b+1], the newest of its kv_lengths[b] tokens)
     over a paged cache K_pages, V_pages [P, Hkv, page, d] (or with a leading
     layer dimension); bottom-right causal unless ``causal`` is False.
-    ``max_new`` bounds the new tokens of one sequence (default: T)."""
+    ``max_new`` bounds the new tokens of one sequence (default: T, which costs
+    a batch of single tokens a sixth to a third more than ``max_new=1``)."""
     pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
     if Q.dim() != 3 or K_pages.dtype != Q.dtype:
         raise ValueError("Q must be [T, H, d] of the cache's dtype")

@@ -8,8 +8,10 @@
 //   dgamma = sum over rows of dz * xh,  u = dz * gamma,
 //   dx = rstd * (u - xh * mean(u * xh))
 //
-// About ten flops per element moved: bound by HBM, or by the launch when
-// there are few rows.
+// About ten flops per element moved: HBM sets the floor, or the launch when
+// there are few rows.  What bounds the kernels is latency, by the counters:
+// DRAM at 45 (append) to 66 % of its nominal rate, 25 to 41 % of the warps
+// resident, half of the issue slots in use.
 //
 // Head sizes 64 and 128 (with rope_dim a multiple of 16) take the vector
 // kernels: a row's 16-byte vectors lie two to a lane, in 4 or 8 lanes, so a
@@ -18,11 +20,15 @@
 // exchange, and the sums of a row take 2 or 3 shuffles.  Other sizes take the
 // element-wise kernels, one warp per row.
 //
-// Measured, B16 L2048 H16 + 16 d64 bf16: forward 50 us (5.4 TB/s, 79 % of a
-// copy's rate; 33 % occupancy at 77 registers), gradient 102 us (4.6 TB/s; 25 %
-// at 128 registers, and two phases, queries and keys); B4 L4096 H32 + 8 d128:
-// 62 and 118 us (5.4 TB/s both).  The element-wise kernels took 1.4 ms for the
-// first.  Appending 10 K tokens of 32 + 8 + 8 heads: 47.6 us (5.2 TB/s); of
+// Measured with nothing in L2, bytes of the operator by time, B16 L2048
+// H16 + 16 d64 bf16: forward 51 us (5.2 TB/s; 33 % occupancy at 77 registers),
+// gradient with dQ in fp32 106 us (4.4 TB/s; 25 % at 128 registers, and two
+// phases, queries and keys); fp32 109 and 172 us (5.0 and 4.7 TB/s).
+// B4 L4096 H32 + 8 d128: 66 and 122 us, fp32 135 and 207.  The element-wise
+// kernels at the first shape with d = 96: 463 and 1,242 us, 8 to 12 times the
+// bytes' time: two bytes a lane, and x read twice; with d = 256 616 and 1,584
+// us, 4 to 6 times.  Appending 8,262 tokens of 32 + 8 + 8 heads: 48 us (203 MB,
+// 4.2 TB/s: a row is loaded, computed and stored before the next is requested);
 // four tokens: 3 us.
 #include <math.h>
 #include <stdint.h>

@@ -19,8 +19,8 @@
 // At 16 slots a byte of the cache meets at most 16 flops: bound by HBM, so
 // the pipeline is sized for bytes in flight (two CTAs of 96 KB per SM).
 // Measured: 16 sequences of 16 to 32 K tokens, 32 heads on 8 kv heads, d = 128:
-// 226 us, 7.1 TB/s of cache (DRAM at 87 % of its nominal rate); 64 sequences of
-// 200 to 1000 tokens: 49 us, where a CTA lives for five tiles and its start
+// 218 us, 7.1 TB/s of cache (DRAM at 89 % of its nominal rate); 64 sequences of
+// 200 to 1000 tokens: 45 us, where a CTA lives for five tiles and its start
 // and merge count (one CTA per SM with 64 KB stages: 70 us); one token over
 // 700 keys: 8 us on the device.
 #include <math.h>

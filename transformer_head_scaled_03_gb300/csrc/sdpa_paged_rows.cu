@@ -21,9 +21,9 @@
 // Bound by the chain softmax -> P V -> next S of a tile: with two tiles in
 // turn a 128-key step of 256 rows takes 2,950 clk where the tensor core needs
 // 2,048 (d = 128; 94 % of the measured burst rate of a large library product).
-// Measured: two sequences, 4,096 new of 8,192 tokens, 32 heads on 8: 580 us,
-// 1.42 PFLOP/s; a CTA's set-up and output are a tenth of it.  Six chunks of 90
-// to 444 tokens over 900 to 7,800 keys, 40 heads on 8: 152 us, 1.03 PFLOP/s:
+// Measured: two sequences, 4,096 new of 8,192 tokens, 32 heads on 8: 594 us,
+// 1.39 PFLOP/s; a CTA's set-up and output are a tenth of it.  Six chunks of 90
+// to 444 tokens over 900 to 7,800 keys, 40 heads on 8: 149 us, 1.06 PFLOP/s:
 // 256 blocks of 6 to 61 steps on 152 SMs; splitting their keys costs more than
 // it evens out (170 us).  16 new tokens each over 30 K keys, four sequences:
 // 101 us, 4.9 TB/s, HBM and the one-tile form's exposed chain together.
