@@ -317,3 +317,25 @@ def test_strides_of_size_one_do_not_count():
     for a, b in ((rows_first(K), rows_first(V)), (torch.cat((K, K))[::2], V)):
         with pytest.raises(ValueError, match="laid out alike"):
             mha.sdpa_paged(Q, a, b, table, lens, offs)
+
+
+@pytest.mark.parametrize("wide", [2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 31 - 1])
+def test_binding_refuses_integers_wider_than_c(wide):
+    """ctypes would pass their low 32 bits: layer 2^32 would be layer 0."""
+    K, V, table, lens = cache()
+    bf = torch.bfloat16
+    Q, offs = torch.zeros((3, 4, 64), dtype=bf), torch.arange(4, dtype=torch.int32)
+    kv, g, pe = torch.zeros((3, 2, 64), dtype=bf), torch.ones(64, dtype=bf), torch.zeros((5, 64))
+    x, dy = torch.zeros((1, 5, 4, 64), dtype=bf), torch.zeros((1, 4, 5, 64), dtype=bf)
+    paged_call = lambda **kw: mha.sdpa_paged(Q, K, V, table, lens, offs, **kw)
+    append = lambda **kw: mha.qk_norm_rope_paged(Q, kv, kv, g, g, pe, K, V, table, lens, offs, **kw)
+    norm = lambda **kw: mha.qk_norm_rope(x, x, g, g, pe, **kw)
+    grad = lambda **kw: mha.qk_norm_rope_backward(x, x, g, g, pe, dy, dy, **kw)
+    for call, names in ((paged_call, ("layer", "num_splits")), (append, ("layer", "pairing")),
+                        (norm, ("pos_offset", "pairing")), (grad, ("pos_offset", "pairing"))):
+        for name in names:
+            with pytest.raises(ValueError, match=f"{name} out of range"):
+                call(**{name: wide})
+    # a bound on new tokens may be as large as it likes, not as small
+    with pytest.raises(ValueError, match="CUDA" if wide > 0 else "max_new out of range"):
+        paged_call(max_new=wide)

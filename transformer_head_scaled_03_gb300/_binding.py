@@ -353,6 +353,14 @@ def _int32(name, t, *shape):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
+def _c_int(name, v):
+    """v as a C int (ctypes drops the bits above 32 without a word)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} out of range")
+    return v
+
+
 def _launch_on(stream, *tensors):
     """Check that every tensor is on the current device, where the library
     launches; the raw stream to launch on.  (The paged calls take tens of
@@ -451,16 +459,20 @@ def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: 
     q_ts = _packed("Q", Q, H, pages.d, Q.dtype)
     _int32("q_offsets", q_offsets, pages.B + 1)
     odt = out_dtype or Q.dtype
+    layer, num_splits = _c_int("layer", layer), _c_int("num_splits", num_splits)
+    # a bound above T says no more than T
+    max_new = max(1, T) if max_new is None else min(int(max_new), max(1, T))
+    max_new = _c_int("max_new", max_new)
     on = _launch_on(stream, Q, K_pages, V_pages, page_table, kv_lengths, q_offsets,
                     Q if out is None else out)
     if out is None:
         out = _new(stream, (T, H, d), odt, Q.device)
     elif out.shape != (T, H, d) or out.dtype != odt or not out.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
-    st = (_lib or lib()).sdpa_paged(Q.data_ptr(), q_ts, pages, int(layer), q_offsets.data_ptr(),
-                          out.data_ptr(), T, H, max(1, T) if max_new is None else int(max_new),
-                          float(scale or 0.0), MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE,
-                          _dtype_code(odt), int(num_splits), on)
+    st = (_lib or lib()).sdpa_paged(Q.data_ptr(), q_ts, pages, layer, q_offsets.data_ptr(),
+                          out.data_ptr(), T, H, max_new, float(scale or 0.0),
+                          MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE, _dtype_code(odt),
+                          num_splits, on)
     _check(st, "sdpa_paged")
     return out
 
@@ -507,6 +519,7 @@ def qk_norm_rope(Q, K, gamma_q, gamma_k, pe, pos_offset: int = 0, positions=None
     first pe.shape[1] columns rotated by the token's position (a row of pe, a
     ``sinusoidal_pe`` table): ``positions`` int32 [B, L], or pos_offset + l."""
     B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
+    pos_offset, pairing = _c_int("pos_offset", pos_offset), _c_int("pairing", pairing)
     on = _launch_on(stream, Q, K, gamma_q, gamma_k, pe, Q if positions is None else positions,
                     *(() if out is None else out))
     want = ((B, H, L, d), (B, Hkv, L, d))
@@ -519,8 +532,8 @@ def qk_norm_rope(Q, K, gamma_q, gamma_k, pe, pos_offset: int = 0, positions=None
     rows, r = pe.shape
     st = (_lib or lib()).qk_norm_rope_forward(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
-        pe.data_ptr(), rows, r, int(pairing), out[0].data_ptr(), out[1].data_ptr(), B, L, H, Hkv,
-        d, int(pos_offset), None if positions is None else positions.data_ptr(), float(eps),
+        pe.data_ptr(), rows, r, pairing, out[0].data_ptr(), out[1].data_ptr(), B, L, H, Hkv,
+        d, pos_offset, None if positions is None else positions.data_ptr(), float(eps),
         _dtype_code(Q.dtype), on)
     _check(st, "qk_norm_rope_forward")
     return out
@@ -534,6 +547,7 @@ def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int 
     fp32 each, as ``sdpa_backward`` returns them).  ``out``: (dQ, dK) to fill,
     laid out as Q and K may be."""
     B, L, H, Hkv, d, q_ts, k_ts = _rope_args(Q, K, gamma_q, gamma_k, pe, positions)
+    pos_offset, pairing = _c_int("pos_offset", pos_offset), _c_int("pairing", pairing)
     if dQo.shape != (B, H, L, d) or dKo.shape != (B, Hkv, L, d) \
             or not dQo.is_contiguous() or not dKo.is_contiguous():
         raise ValueError("dQo and dKo must be contiguous [B, heads, L, d]")
@@ -560,9 +574,9 @@ def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int 
     rows, r = pe.shape
     st = dev.qk_norm_rope_backward(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, gamma_q.data_ptr(), gamma_k.data_ptr(),
-        pe.data_ptr(), rows, r, int(pairing), dQo.data_ptr(), dKo.data_ptr(), out[0].data_ptr(),
+        pe.data_ptr(), rows, r, pairing, dQo.data_ptr(), dKo.data_ptr(), out[0].data_ptr(),
         dq_ts, out[1].data_ptr(), dk_ts, dgamma_q.data_ptr(), dgamma_k.data_ptr(), B, L, H, Hkv,
-        d, int(pos_offset), None if positions is None else positions.data_ptr(), float(eps),
+        d, pos_offset, None if positions is None else positions.data_ptr(), float(eps),
         _dtype_code(Q.dtype), _dtype_code(dQo.dtype), _dtype_code(dKo.dtype),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), on)
     _check(st, "qk_norm_rope_backward")
@@ -586,6 +600,7 @@ def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_tab
     if K.shape[0] != T or V.shape[0] != T:
         raise ValueError("Q, K and V must hold the same tokens")
     _gammas(gamma_q, gamma_k, pe, d, dt)
+    layer, pairing = _c_int("layer", layer), _c_int("pairing", pairing)
     _int32("q_offsets", q_offsets, pages.B + 1)
     on = _launch_on(stream, Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
                     q_offsets, Q if out is None else out)
@@ -595,8 +610,8 @@ def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_tab
         raise ValueError("out has the wrong shape, dtype or layout")
     st = (_lib or lib()).qk_norm_rope_paged(
         Q.data_ptr(), q_ts, K.data_ptr(), k_ts, V.data_ptr(), v_ts, gamma_q.data_ptr(),
-        gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], int(pairing), out.data_ptr(),
-        pages, int(layer), q_offsets.data_ptr(), T, H, float(eps), on)
+        gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], pairing, out.data_ptr(),
+        pages, layer, q_offsets.data_ptr(), T, H, float(eps), on)
     _check(st, "qk_norm_rope_paged")
     return out
 
