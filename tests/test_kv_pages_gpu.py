@@ -210,3 +210,37 @@ def test_captured_compaction_follows_the_lengths():
         for a, w in zip(dst, want):
             assert np.array_equal(to_np(a), w)
     assert mha.mha_check() == mha.MHA_OK
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Append, fork and compaction over 4.3 GB pools whose sequence lies past
+    2^31 elements: what a pool of the last pages alone gives."""
+    rng = np.random.default_rng(70)
+    Hkv, ps, d, last = 8, 128, 128, 6
+    P = (1 << 31) // (Hkv * ps * d) + 8
+    T, H = 9, 8
+    draw = lambda *shape: dev(rng.standard_normal(shape, dtype=np.float32), BF)
+    q, k, v, g = draw(T, H, d), draw(T, Hkv, d), draw(T, Hkv, d), draw(d)
+    K, V = draw(last, Hkv, ps, d), draw(last, Hkv, ps, d)
+    pe = mha.sinusoidal_pe(400, d)
+    table = np.array([[4, 1, 3, 2], [-1] * 4], np.int32)     # page 5 and page 0 are free
+
+    def steps(kp, vp, first):
+        t = i32(np.where(table < 0, -1, table + first))
+        lens, one = i32([300 + T, 0]), lambda x: i32([x])
+        out = mha.qk_norm_rope_paged(q, k, v, g, g, pe, kp, vp, t, lens, i32([0, T, T]))
+        mha.kv_pages_fork(kp, vp, t, lens, one(0), one(1), one(first + 5))
+        dst = [torch.zeros((5, Hkv, ps, d), dtype=BF, device="cuda") for _ in range(2)]
+        to = torch.full_like(t, -1)
+        n = mha.kv_pages_compact(kp, vp, t, lens, *dst, to)
+        assert mha.mha_check() == mha.MHA_OK
+        return [out, kp[first:first + last], vp[first:first + last], lens, *dst, to, n]
+
+    want = steps(K.clone(), V.clone(), 0)
+    assert want[-1].tolist() == [4]
+    first = P - last
+    big = [torch.zeros((P, Hkv, ps, d), dtype=BF, device="cuda") for _ in range(2)]
+    big[0][first:], big[1][first:] = K, V
+    for a, b in zip(want, steps(*big, first)):
+        assert torch.equal(a, b)
+    assert not torch.any(big[0][:first]) and not torch.any(big[1][:first])
