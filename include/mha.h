@@ -407,7 +407,8 @@ mha_status qk_norm_rope_forward(const void *Q, int64_t q_token_stride,
  *   dQ, dK : of dtype, laid out as Q and K with token strides of their own.
  *   dgamma_q, dgamma_k : fp32 [d], overwritten; 16-byte aligned.
  *   workspace : device, 16-byte aligned, at least
- *       qk_norm_rope_backward_workspace_bytes(d) bytes.
+ *       qk_norm_rope_backward_workspace_bytes(d) bytes; one call's at a time
+ *       (captured graphs that may run at once need one each).
  * The sums run in a fixed order, in fp32 over a block's rows and fp64 over the
  * blocks: equal calls give equal bits.  A token with a
  * bad position gets zero rows and adds nothing to dgamma.
@@ -490,7 +491,8 @@ mha_status kv_pages_fork(const mha_kv_pages *pages, const int32_t *parents,
  *       It must share no memory with src.
  *   n_live : device int32, the number of pages held.
  *   workspace : device, 16-byte aligned, at least
- *       kv_pages_compact_workspace_bytes(src->num_pages) bytes.
+ *       kv_pages_compact_workspace_bytes(src->num_pages) bytes; one call's at
+ *       a time, as above.
  * Entries of dst's table behind a sequence's last page, and pages from n_live
  * on, are left as they were.
  * Checked on the device (MHA_ERR_DEVICE): a length outside [0,
