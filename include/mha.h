@@ -59,7 +59,13 @@ typedef enum {
                                 length outside [1, Lk] (mha_check) */
 } mha_status;
 
-typedef enum { MHA_F32 = 0, MHA_BF16 = 1 } mha_dtype;
+typedef enum {
+    MHA_F32 = 0,
+    MHA_BF16 = 1,
+    MHA_E4M3 = 2 /* 8 bits, sign, 4 of exponent (bias 7), 3 of mantissa, largest
+                    448, no infinities; the paged cache's _e4m3 calls, the
+                    calls on selected pages and kv_pages_bounds only */
+} mha_dtype;
 
 enum {
     MHA_MASK_NONE = 0,
@@ -307,6 +313,19 @@ typedef struct {
 } mha_kv_pages;
 
 /*
+ * A paged cache in 8 bits: pools of MHA_E4M3 codes and, for every page and kv
+ * head, one scale for its keys and one for its values; row = code * scale.
+ *   K, V : device fp32 [layers, num_pages, kv_heads], dense, 4-byte aligned.
+ *          A scale is finite and >= 0; those of pages that no sequence holds
+ *          may be anything.
+ * The calls that take an mha_kv_scales expect pages->dtype MHA_E4M3; d is a
+ * multiple of 16.  Strides count elements, bytes here.
+ */
+typedef struct {
+    float *K, *V;
+} mha_kv_scales;
+
+/*
  * sdpa_paged -- attention of each sequence's newest tokens over its paged
  * cache: one token each while decoding, a few, or a long chunk of a prompt,
  * mixed in one call.  Query heads may share key/value heads.
@@ -352,6 +371,24 @@ mha_status sdpa_paged(const void *Q, int64_t q_token_stride,
                       const int32_t *q_offsets, void *O, int T, int H,
                       int max_new, float scale, int mask_kind,
                       mha_dtype out_dtype, int num_splits, mha_stream stream);
+
+/*
+ * sdpa_paged_e4m3 -- sdpa_paged over a cache in 8 bits.  Q is bf16; the rest is
+ * as for sdpa_paged, but for the products' operands: a query row meets the
+ * keys' codes as two e4m3 parts, which together are off by at most 2^-18 of
+ * the row's largest element, and the weights, times the values' scales over
+ * the largest of them that the CTA has met, meet the values' codes as two
+ * e4m3 parts (up to 16 rows, see max_new: off by 2^-8 of the weight or 2^-23 of
+ * the largest one) or in bf16 against values in bf16 (more rows: powers of two
+ * as scales are exact there, others round a value by 2^-8).
+ */
+mha_status sdpa_paged_e4m3(const void *Q, int64_t q_token_stride,
+                           const mha_kv_pages *pages,
+                           const mha_kv_scales *scales, int layer,
+                           const int32_t *q_offsets, void *O, int T, int H,
+                           int max_new, float scale, int mask_kind,
+                           mha_dtype out_dtype, int num_splits,
+                           mha_stream stream);
 
 /* How the rotation pairs a head's first rope_dim columns. */
 enum {
@@ -459,6 +496,28 @@ mha_status qk_norm_rope_paged(const void *Q, int64_t q_token_stride,
                               int H, float eps, mha_stream stream);
 
 /*
+ * qk_norm_rope_paged_e4m3 -- qk_norm_rope_paged into a cache in 8 bits.  A page
+ * keeps one scale per head, so the new rows of a page are stored together:
+ *   need = the smallest power of two s >= 2^-100 with max |x| <= 448 s over
+ *          the finite elements of the page's new rows; 0 where they are zeros
+ *   s    = max(need, the page's scale), of a page without older rows need
+ *   code = e4m3(x / s), to nearest, ties to even
+ * and where s has grown, the older rows' codes become e4m3(code * old / s):
+ * exact between powers of two, but for codes that leave the normal range
+ * (x / s below 2^-6).  "Older" are the sequence's rows of that page ahead of
+ * its new ones; what lies behind its length is not touched.  x is the normed,
+ * rotated key or the value in fp32; elements that are not finite are stored
+ * as NaN.
+ */
+mha_status qk_norm_rope_paged_e4m3(
+    const void *Q, int64_t q_token_stride, const void *K,
+    int64_t k_token_stride, const void *V, int64_t v_token_stride,
+    const void *gamma_q, const void *gamma_k, const float *pe, int pe_rows,
+    int rope_dim, int pairing, void *Qo, const mha_kv_pages *pages,
+    const mha_kv_scales *scales, int layer, const int32_t *q_offsets, int T,
+    int H, float eps, mha_stream stream);
+
+/*
  * kv_pages_fork -- n sequences continue n others (parallel samples, beams):
  * sequence children[i] takes parents[i]'s length and full pages (shared), and
  * the rows of its last, partly filled page are copied into page fresh[i], in
@@ -478,6 +537,13 @@ mha_status qk_norm_rope_paged(const void *Q, int64_t q_token_stride,
 mha_status kv_pages_fork(const mha_kv_pages *pages, const int32_t *parents,
                          const int32_t *children, const int32_t *fresh, int n,
                          mha_stream stream);
+
+/* kv_pages_fork_e4m3 -- kv_pages_fork of a cache in 8 bits: a fresh page takes
+ * the scales of the page that it copies, in every layer. */
+mha_status kv_pages_fork_e4m3(const mha_kv_pages *pages,
+                              const mha_kv_scales *scales,
+                              const int32_t *parents, const int32_t *children,
+                              const int32_t *fresh, int n, mha_stream stream);
 
 /*
  * kv_pages_compact -- the pages that some sequence holds, in increasing page
@@ -507,6 +573,112 @@ mha_status kv_pages_compact(const mha_kv_pages *src, const mha_kv_pages *dst,
 
 /* Workspace kv_pages_compact needs, in bytes (0 for a bad num_pages). */
 size_t kv_pages_compact_workspace_bytes(int num_pages);
+
+/* kv_pages_compact_e4m3 -- kv_pages_compact of a cache in 8 bits: the scales
+ * move with their pages.  dst_scales shares no memory with src_scales. */
+mha_status kv_pages_compact_e4m3(const mha_kv_pages *src,
+                                 const mha_kv_scales *src_scales,
+                                 const mha_kv_pages *dst,
+                                 const mha_kv_scales *dst_scales,
+                                 int32_t *n_live, void *workspace,
+                                 size_t workspace_bytes, mha_stream stream);
+
+/*
+ * Attention over a long cache can leave most pages out.  Every full page has
+ * bounds of its keys, column by column; a query's bounds of its scores with a
+ * page's keys then cost two rows in place of page_size; each query takes the
+ * pages with the largest ones.
+ *   bounds      : device int8 [layers, num_pages, kv_heads, 2, d], dense,
+ *                 16-byte aligned: lo, hi
+ *   bound_scale : device fp32 [layers, num_pages, kv_heads], dense
+ * with lo * bound_scale <= K <= hi * bound_scale over the page's rows.
+ *
+ * kv_pages_bounds -- the bounds of every page that the newest tokens
+ * [q_offsets[b], q_offsets[b+1]) have filled or lie in and that is full:
+ *   s = the smallest power of two >= 2^-100 with max |c| <= 127 s, 0 for zeros
+ *   lo = floor(min c / s), hi = ceil(max c / s) by columns;  bound_scale = s
+ * where c are the page's keys, or of a cache in 8 bits its codes, and
+ * bound_scale is s times the page's key scale.  Called after each append (of
+ * whole sequences at first: q_offsets from their lengths) it keeps the bounds
+ * of all full pages; pages that are shared keep theirs, and a page that a fork
+ * copies gets its own once it is full.
+ *   scales : of a cache in 8 bits (dtype MHA_E4M3); NULL for MHA_BF16.
+ *   T : the packed tokens, q_offsets as for sdpa_paged.
+ * d is 64 or 128.  Keys must be finite.
+ * Checked on the device (MHA_ERR_DEVICE): kv_lengths[b] in [n_b,
+ * table_cols*page_size], offsets ascending in [0, T], page numbers -- such a
+ * sequence's or page's bounds are left as they were.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status kv_pages_bounds(const mha_kv_pages *pages,
+                           const mha_kv_scales *scales, int layer,
+                           const int32_t *q_offsets, int T, int8_t *bounds,
+                           float *bound_scale, mha_stream stream);
+
+/*
+ * kv_pages_select -- for every new token and kv head, n_select of the pages
+ * that hold keys the token sees (causal, bottom-right, as in sdpa_paged): its
+ * newest page, and of the full ones before it those with the largest score,
+ * equal scores from the sequence's beginning on:
+ *   qi = q / s to the nearest whole number, ties to even, s the smallest power
+ *        of two >= 2^-100 with max |q| <= 127 s over the head's row
+ *   score = max over the kv head's query heads of
+ *           s * sum_c (max(qi_c, 0) hi_c + min(qi_c, 0) lo_c) * bound_scale
+ * (a sum of max(qi_c lo_c, qi_c hi_c), as lo <= hi).
+ * The sums are whole numbers, the products in fp32 in that order, so equal
+ * calls select equal pages on every device.  Elements of q that are not
+ * finite count as 0.
+ *   Q : bf16, T packed tokens as for sdpa_paged.
+ *   bounds, bound_scale : of all the layers; `layer` picks.
+ *   selected : device int32 [T, kv_heads, n_select], page numbers in the order
+ *       of their positions, -1 behind the last.
+ *   lengths : device int32 [T], the rows that the token sees in its selected
+ *       pages (all full but the newest); 0 for a token of no sequence, -1
+ *       where an entry is bad (selected then holds -1).
+ *   workspace : device, 16-byte aligned, at least
+ *       kv_pages_select_workspace_bytes(...) bytes; one call's at a time.
+ * The pools are not read: of *pages num_pages, page_size, kv_heads, d, layers
+ * and the tables count.  d is 64 or 128, H / kv_heads <= 128, 1 <= n_select <=
+ * 65536.
+ * Checked on the device (MHA_ERR_DEVICE): kv_lengths[b] in [n_b,
+ * table_cols*page_size], the page numbers a token sees, offsets ascending in
+ * [0, T].
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status kv_pages_select(const void *Q, int64_t q_token_stride,
+                           const mha_kv_pages *pages, int layer,
+                           const int32_t *q_offsets, const int8_t *bounds,
+                           const float *bound_scale, int T, int H,
+                           int n_select, int32_t *selected, int32_t *lengths,
+                           void *workspace, size_t workspace_bytes,
+                           mha_stream stream);
+
+/* Workspace kv_pages_select needs, in bytes (0 for bad sizes). */
+size_t kv_pages_select_workspace_bytes(int T, int kv_heads, int table_cols);
+
+/*
+ * sdpa_paged_selected -- attention of T tokens, each over its own pages per kv
+ * head: token t and kv head g see the first lengths[t] rows of the pages
+ * selected[t, g, :], which kv_pages_select has filled (any table of that
+ * layout will do).
+ *   Q, O, H, scale, layer, out_dtype, num_splits : as for sdpa_paged.
+ *   pages : the pools; its tables are not used.
+ *   scales : of a cache in 8 bits (dtype MHA_E4M3, whose operands are as in
+ *       sdpa_paged_e4m3); NULL for MHA_BF16.
+ *   selected : device int32 [T, kv_heads, n_select]; lengths : device int32
+ *       [T].  A token of length 0 is passed over: its row of O stays as it was.
+ * Checked on the device (MHA_ERR_DEVICE, the token's rows written as zeros):
+ * lengths in [0, n_select*page_size], page numbers.
+ * d is 64 or 128, H / kv_heads <= 128, n_select * page_size <= 2^30.
+ * Returns MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED or MHA_ERR_CUDA.
+ */
+mha_status sdpa_paged_selected(const void *Q, int64_t q_token_stride,
+                               const mha_kv_pages *pages,
+                               const mha_kv_scales *scales, int layer,
+                               const int32_t *selected, const int32_t *lengths,
+                               int n_select, void *O, int T, int H,
+                               float scale, mha_dtype out_dtype,
+                               int num_splits, mha_stream stream);
 
 /*
  * mha_create -- allocate a multi-head attention layer handle.

@@ -6,7 +6,9 @@ whose store layouts do the head split and the concat, and fp32 CUDA-core
 kernels.  This package is the thin Python binding over that ABI
 (``sdpa_forward``, ``mha_create``, ``mha_forward``, ``mha_check``,
 ``mha_destroy``; over a paged cache ``qk_norm_rope_paged``, ``sdpa_paged``,
-``kv_pages_fork``, ``kv_pages_compact``), the in-tree build (``build``) and the seeded input
+``kv_pages_fork``, ``kv_pages_compact``, which take pages in bf16 or in 8
+bits, and over the few of a long cache's pages that a query selects
+``kv_pages_bounds``, ``kv_pages_select``, ``sdpa_paged_selected``), the in-tree build (``build``) and the seeded input
 generators (``inputs``).  Attribute access loads the binding lazily, so
 importing the package (e.g. for ``inputs``) needs neither torch nor a GPU.
 """
@@ -15,13 +17,14 @@ _BINDING_NAMES = {
     "sdpa_forward_lse", "sdpa_backward",
     "embed_pe",
     "sdpa_paged", "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_paged", "kv_pages_fork",
-    "kv_pages_compact", "KvPages", "ROPE_INTERLEAVED", "ROPE_HALF",
+    "kv_pages_compact", "kv_pages_bounds", "kv_pages_select", "sdpa_paged_selected", "KvPages",
+    "KvScales", "ROPE_INTERLEAVED", "ROPE_HALF",
     "MASK_CAUSAL_BOTTOM_RIGHT", "mha_create", "mha_forward", "mha_check",
     "mha_destroy", "MhaHandle", "MhaError", "EncoderLayer", "EncoderParams",
     "ENCODER_PARAM_NAMES", "set_wait_limit_ms", "selftest_wait_timeout", "status_string", "lib",
     "MASK_NONE", "MASK_CAUSAL", "MASK_KEY_PADDING", "MHA_OK", "MHA_ERR_INVALID_ARG",
     "MHA_ERR_UNSUPPORTED", "MHA_ERR_CUDA", "MHA_ERR_OOM", "MHA_ERR_TIMEOUT",
-    "MHA_ERR_DEVICE", "MHA_F32", "MHA_BF16", "LIB_PATH",
+    "MHA_ERR_DEVICE", "MHA_F32", "MHA_BF16", "MHA_E4M3", "LIB_PATH",
 }
 
 

@@ -25,6 +25,7 @@ MHA_ERR_DEVICE = 6
 
 MHA_F32 = 0
 MHA_BF16 = 1
+MHA_E4M3 = 2
 
 MASK_NONE = 0
 MASK_CAUSAL = 1
@@ -57,6 +58,11 @@ class KvPages(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
                 ("page_table", ctypes.c_void_p), ("kv_lengths", ctypes.c_void_p),
                 ("B", ctypes.c_int), ("table_cols", ctypes.c_int)]
+
+
+class KvScales(ctypes.Structure):
+    """mha_kv_scales of include/mha.h."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p)]
 
 
 class MhaError(RuntimeError):
@@ -114,6 +120,26 @@ def _declare(lib):
     lib.kv_pages_compact_workspace_bytes.restype = ctypes.c_size_t
     lib.kv_pages_compact.argtypes = [kvp, kvp, vp, vp, ctypes.c_size_t, vp]
     lib.kv_pages_compact.restype = i32
+    scp, sz = ctypes.POINTER(KvScales), ctypes.c_size_t
+    lib.sdpa_paged_e4m3.argtypes = [vp, i64, kvp, scp, i32, vp, vp, i32, i32, i32, f32, i32, i32,
+                                    i32, vp]
+    lib.sdpa_paged_e4m3.restype = i32
+    lib.qk_norm_rope_paged_e4m3.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, vp,
+                                            kvp, scp, i32, vp, i32, i32, f32, vp]
+    lib.qk_norm_rope_paged_e4m3.restype = i32
+    lib.kv_pages_fork_e4m3.argtypes = [kvp, scp, vp, vp, vp, i32, vp]
+    lib.kv_pages_fork_e4m3.restype = i32
+    lib.kv_pages_compact_e4m3.argtypes = [kvp, scp, kvp, scp, vp, vp, sz, vp]
+    lib.kv_pages_compact_e4m3.restype = i32
+    lib.kv_pages_bounds.argtypes = [kvp, scp, i32, vp, i32, vp, vp, vp]
+    lib.kv_pages_bounds.restype = i32
+    lib.kv_pages_select_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.kv_pages_select_workspace_bytes.restype = sz
+    lib.kv_pages_select.argtypes = [vp, i64, kvp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.kv_pages_select.restype = i32
+    lib.sdpa_paged_selected.argtypes = [vp, i64, kvp, scp, i32, vp, vp, i32, vp, i32, i32, f32, i32,
+                                        i32, vp]
+    lib.sdpa_paged_selected.restype = i32
     lib.sdpa_forward_float_mask.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32,
                                             vp, vp, i64, i64, i32, i32, vp]
     lib.sdpa_forward_float_mask.restype = i32
@@ -378,6 +404,10 @@ def _launch_on(stream, *tensors):
     return stream.cuda_stream
 
 
+def _given(*tensors):
+    return [t for t in tensors if t is not None]
+
+
 def _new(stream, shape, dtype, device):
     """A tensor that `stream` (the current one when None) may use; the caching
     allocator keeps its memory until that stream is past it."""
@@ -396,9 +426,9 @@ def _check_workspace(workspace):
         raise ValueError("workspace must be contiguous")
 
 
-def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
-    """The mha_kv_pages of pools [P, Hkv, page, d] or [layers, P, Hkv, page, d]
-    (pages and layers at any stride, a page itself contiguous)."""
+def _kv_pools(K_pages, V_pages):
+    """What an mha_kv_pages says of pools [P, Hkv, page, d] or [layers, P, Hkv,
+    page, d] (pages and layers at any stride, a page itself contiguous)."""
     shape = K_pages.shape
     if len(shape) not in (4, 5) or V_pages.shape != shape or V_pages.dtype != K_pages.dtype:
         raise ValueError("K_pages and V_pages must be alike, [P, Hkv, page, d] or "
@@ -416,14 +446,38 @@ def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
     # the library reads a stride of 0 as "dense"
     if P > 1 and strides[-4] == 0 or layers > 1 and strides[0] == 0:
         raise ValueError("pages and layers must not be broadcast")
+    dtype = MHA_E4M3 if K_pages.dtype is _E4M3 else _dtype_code(K_pages.dtype)
+    return (K_pages.data_ptr(), V_pages.data_ptr(), dtype, P, ps, Hkv, d, layers, strides[-4],
+            strides[0] if layers > 1 else 0)
+
+
+def _kv_pages(K_pages, V_pages, page_table, kv_lengths):
+    """The mha_kv_pages of a cache."""
+    pools = _kv_pools(K_pages, V_pages)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
     B, cols = page_table.shape
     _int32("page_table", page_table, B, cols)
     _int32("kv_lengths", kv_lengths, B)
-    return KvPages(K_pages.data_ptr(), V_pages.data_ptr(), _dtype_code(K_pages.dtype), P, ps, Hkv,
-                   d, layers, strides[-4], strides[0] if layers > 1 else 0,
-                   page_table.data_ptr(), kv_lengths.data_ptr(), B, cols)
+    return KvPages(*pools, page_table.data_ptr(), kv_lengths.data_ptr(), B, cols)
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _kv_scales(K_pages, K_scale, V_scale):
+    """The mha_kv_scales of pools in 8 bits, None for others."""
+    if K_pages.dtype is not _E4M3:
+        if K_scale is not None or V_scale is not None:
+            raise ValueError("K_scale and V_scale are for pages in 8 bits (float8_e4m3fn)")
+        return None
+    if K_scale is None or V_scale is None:
+        raise ValueError("pages in 8 bits need K_scale and V_scale")
+    want = K_pages.shape[:-2]
+    for name, s in (("K_scale", K_scale), ("V_scale", V_scale)):
+        if s.dtype is not torch.float32 or s.shape != want or not s.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(want)}")
+    return KvScales(K_scale.data_ptr(), V_scale.data_ptr())
 
 
 def _packed(name, x, heads, d, dtype):
@@ -445,16 +499,19 @@ def _packed(name, x, heads, d, dtype):
 def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: int | None = None,
                causal: bool = True, scale: float | None = None,
                out_dtype: torch.dtype | None = None, layer: int = 0, num_splits: int = 0, out=None,
-               stream=None):
+               stream=None, K_scale=None, V_scale=None):
     """O [T, H, d] = attention of packed new tokens Q [T, H, d] (sequence b's
     are q_offsets[b]..q_offsets[b+1], the newest of its kv_lengths[b] tokens)
     over a paged cache K_pages, V_pages [P, Hkv, page, d] (or with a leading
     layer dimension); bottom-right causal unless ``causal`` is False.
     ``max_new`` bounds the new tokens of one sequence (default: T, which costs
-    a batch of single tokens a sixth to a third more than ``max_new=1``)."""
+    a batch of single tokens a sixth to a third more than ``max_new=1``).
+    Pages in 8 bits (float8_e4m3fn, Q in bf16) come with ``K_scale`` and
+    ``V_scale`` float32 [P, Hkv] (or [layers, P, Hkv])."""
     pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
-    if Q.dim() != 3 or K_pages.dtype != Q.dtype:
-        raise ValueError("Q must be [T, H, d] of the cache's dtype")
+    scales = _kv_scales(K_pages, K_scale, V_scale)
+    if Q.dim() != 3 or Q.dtype != (K_pages.dtype if scales is None else torch.bfloat16):
+        raise ValueError("Q must be [T, H, d] of the cache's dtype, or bf16 over pages in 8 bits")
     T, H, d = Q.shape
     q_ts = _packed("Q", Q, H, pages.d, Q.dtype)
     _int32("q_offsets", q_offsets, pages.B + 1)
@@ -464,16 +521,18 @@ def sdpa_paged(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, max_new: 
     max_new = max(1, T) if max_new is None else min(int(max_new), max(1, T))
     max_new = _c_int("max_new", max_new)
     on = _launch_on(stream, Q, K_pages, V_pages, page_table, kv_lengths, q_offsets,
-                    Q if out is None else out)
+                    Q if out is None else out, *_given(K_scale, V_scale))
     if out is None:
         out = _new(stream, (T, H, d), odt, Q.device)
     elif out.shape != (T, H, d) or out.dtype != odt or not out.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
-    st = (_lib or lib()).sdpa_paged(Q.data_ptr(), q_ts, pages, layer, q_offsets.data_ptr(),
-                          out.data_ptr(), T, H, max_new, float(scale or 0.0),
-                          MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE, _dtype_code(odt),
-                          num_splits, on)
-    _check(st, "sdpa_paged")
+    rest = (layer, q_offsets.data_ptr(), out.data_ptr(), T, H, max_new, float(scale or 0.0),
+            MASK_CAUSAL_BOTTOM_RIGHT if causal else MASK_NONE, _dtype_code(odt), num_splits, on)
+    dev = _lib or lib()
+    if scales is None:
+        _check(dev.sdpa_paged(Q.data_ptr(), q_ts, pages, *rest), "sdpa_paged")
+    else:
+        _check(dev.sdpa_paged_e4m3(Q.data_ptr(), q_ts, pages, scales, *rest), "sdpa_paged_e4m3")
     return out
 
 
@@ -585,15 +644,17 @@ def qk_norm_rope_backward(Q, K, gamma_q, gamma_k, pe, dQo, dKo, pos_offset: int 
 
 def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
                        q_offsets, pairing: int = ROPE_INTERLEAVED, eps: float = 1e-6,
-                       layer: int = 0, out=None, stream=None):
+                       layer: int = 0, out=None, stream=None, K_scale=None, V_scale=None):
     """Q' [T, H, d] for ``sdpa_paged``; the normed, rotated keys and the values
     of the T packed new tokens go into their pages (``kv_lengths`` already
-    counts them)."""
+    counts them).  Pages in 8 bits (float8_e4m3fn; the rows stay bf16) come
+    with ``K_scale`` and ``V_scale``, which are updated."""
     pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    scales = _kv_scales(K_pages, K_scale, V_scale)
     if Q.dim() != 3:
         raise ValueError("Q must be [T, H, d]")
     T, H, d = Q.shape
-    dt = K_pages.dtype
+    dt = K_pages.dtype if scales is None else torch.bfloat16
     q_ts = _packed("Q", Q, H, pages.d, dt)
     k_ts = _packed("K", K, pages.kv_heads, d, dt)
     v_ts = _packed("V", V, pages.kv_heads, d, dt)
@@ -603,41 +664,56 @@ def qk_norm_rope_paged(Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_tab
     layer, pairing = _c_int("layer", layer), _c_int("pairing", pairing)
     _int32("q_offsets", q_offsets, pages.B + 1)
     on = _launch_on(stream, Q, K, V, gamma_q, gamma_k, pe, K_pages, V_pages, page_table, kv_lengths,
-                    q_offsets, Q if out is None else out)
+                    q_offsets, Q if out is None else out, *_given(K_scale, V_scale))
     if out is None:
         out = _new(stream, (T, H, d), dt, Q.device)
     elif out.shape != (T, H, d) or out.dtype != dt or not out.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
-    st = (_lib or lib()).qk_norm_rope_paged(
-        Q.data_ptr(), q_ts, K.data_ptr(), k_ts, V.data_ptr(), v_ts, gamma_q.data_ptr(),
-        gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], pairing, out.data_ptr(),
-        pages, layer, q_offsets.data_ptr(), T, H, float(eps), on)
-    _check(st, "qk_norm_rope_paged")
+    rows = (Q.data_ptr(), q_ts, K.data_ptr(), k_ts, V.data_ptr(), v_ts, gamma_q.data_ptr(),
+            gamma_k.data_ptr(), pe.data_ptr(), pe.shape[0], pe.shape[1], pairing, out.data_ptr())
+    rest = (layer, q_offsets.data_ptr(), T, H, float(eps), on)
+    dev = _lib or lib()
+    if scales is None:
+        _check(dev.qk_norm_rope_paged(*rows, pages, *rest), "qk_norm_rope_paged")
+    else:
+        _check(dev.qk_norm_rope_paged_e4m3(*rows, pages, scales, *rest), "qk_norm_rope_paged_e4m3")
     return out
 
 
-def kv_pages_fork(K_pages, V_pages, page_table, kv_lengths, parents, children, fresh, stream=None):
+def kv_pages_fork(K_pages, V_pages, page_table, kv_lengths, parents, children, fresh, stream=None,
+                  K_scale=None, V_scale=None):
     """Sequences children[i] continue parents[i]: full pages shared, the last
-    partly filled one copied into page fresh[i] (every layer); page_table and
-    kv_lengths are updated in place."""
+    partly filled one copied into page fresh[i] (every layer; of pages in 8
+    bits with its ``K_scale`` and ``V_scale``); page_table and kv_lengths are
+    updated in place."""
     pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    scales = _kv_scales(K_pages, K_scale, V_scale)
     n = parents.numel()
     for name, t in (("parents", parents), ("children", children), ("fresh", fresh)):
         _int32(name, t, n)
-    on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, parents, children, fresh)
-    _check((_lib or lib()).kv_pages_fork(pages, parents.data_ptr(), children.data_ptr(),
-                                         fresh.data_ptr(), n, on), "kv_pages_fork")
+    on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, parents, children, fresh,
+                    *_given(K_scale, V_scale))
+    dev, pairs = _lib or lib(), (parents.data_ptr(), children.data_ptr(), fresh.data_ptr(), n, on)
+    if scales is None:
+        _check(dev.kv_pages_fork(pages, *pairs), "kv_pages_fork")
+    else:
+        _check(dev.kv_pages_fork_e4m3(pages, scales, *pairs), "kv_pages_fork_e4m3")
 
 
 def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
-                     workspace=None, stream=None):
+                     workspace=None, stream=None, K_scale=None, V_scale=None, K_scale_out=None,
+                     V_scale_out=None):
     """The pages that some sequence holds become pages 0..n-1 of K_out, V_out,
-    in order; table_out is the renumbered page table.  Returns n (int32 [1])."""
+    in order; table_out is the renumbered page table.  Returns n (int32 [1]).
+    Of pages in 8 bits the scales move to ``K_scale_out``, ``V_scale_out``."""
     src = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
     dst = _kv_pages(K_out, V_out, table_out, kv_lengths)
+    scales = _kv_scales(K_pages, K_scale, V_scale)
+    scales_out = _kv_scales(K_out, K_scale_out, V_scale_out)
     _check_workspace(workspace)
     on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, K_out, V_out, table_out,
-                    K_pages if workspace is None else workspace)
+                    K_pages if workspace is None else workspace,
+                    *_given(K_scale, V_scale, K_scale_out, V_scale_out))
     dev = _lib or lib()
     need = dev.kv_pages_compact_workspace_bytes(src.num_pages)
     # n, and the workspace 16 bytes behind it
@@ -647,8 +723,123 @@ def kv_pages_compact(K_pages, V_pages, page_table, kv_lengths, K_out, V_out, tab
         at, size = count.data_ptr() + 16, need
     else:
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(dev.kv_pages_compact(src, dst, count.data_ptr(), at, size, on), "kv_pages_compact")
+    if scales is None and scales_out is None:
+        _check(dev.kv_pages_compact(src, dst, count.data_ptr(), at, size, on), "kv_pages_compact")
+    else:
+        _check(dev.kv_pages_compact_e4m3(src, scales, dst, scales_out, count.data_ptr(), at, size, on),
+               "kv_pages_compact_e4m3")
     return count[:1]
+
+
+def _bounds_of(K_pages, bounds, bound_scale):
+    lead, d = K_pages.shape[:-2], K_pages.shape[-1]
+    if bounds.dtype is not torch.int8 or bounds.shape != (*lead, 2, d) or not bounds.is_contiguous():
+        raise ValueError(f"bounds must be a contiguous int8 tensor of shape {[*lead, 2, d]}")
+    if bound_scale.dtype is not torch.float32 or bound_scale.shape != lead \
+            or not bound_scale.is_contiguous():
+        raise ValueError(f"bound_scale must be a contiguous float32 tensor of shape {list(lead)}")
+
+
+def kv_pages_bounds(K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale, T: int,
+                    layer: int = 0, stream=None, K_scale=None, V_scale=None):
+    """Fill in, for every full page among those that hold one of the newest T
+    packed tokens, the bounds of its keys: ``bounds`` int8 [P, Hkv, 2, d] (lo,
+    hi by columns) and ``bound_scale`` float32 [P, Hkv] (both with a leading
+    layer dimension if the pools have one), lo * scale <= key <= hi * scale."""
+    pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    scales = _kv_scales(K_pages, K_scale, V_scale)
+    _int32("q_offsets", q_offsets, pages.B + 1)
+    _bounds_of(K_pages, bounds, bound_scale)
+    layer, T = _c_int("layer", layer), _c_int("T", T)
+    on = _launch_on(stream, K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale,
+                    *_given(K_scale, V_scale))
+    _check((_lib or lib()).kv_pages_bounds(pages, scales, layer, q_offsets.data_ptr(), T,
+                                           bounds.data_ptr(), bound_scale.data_ptr(), on),
+           "kv_pages_bounds")
+
+
+def kv_pages_select(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale,
+                    n_select: int, layer: int = 0, out=None, workspace=None, stream=None,
+                    K_scale=None, V_scale=None):
+    """(selected int32 [T, Hkv, n_select], lengths int32 [T]) for
+    ``sdpa_paged_selected``: for every packed new token Q [T, H, d] and kv head
+    its newest page and the full pages before it whose bounds (from
+    ``kv_pages_bounds``) admit the largest scores, in order of position, -1
+    behind the last; and the rows the token sees in them.  ``out``: the two to
+    fill."""
+    pages = _kv_pages(K_pages, V_pages, page_table, kv_lengths)
+    if _given(K_scale, V_scale):
+        _kv_scales(K_pages, K_scale, V_scale)    # the pages themselves are not read
+    if Q.dim() != 3 or Q.dtype is not torch.bfloat16:
+        raise ValueError("Q must be bf16 [T, H, d]")
+    T, H, d = Q.shape
+    q_ts = _packed("Q", Q, H, pages.d, Q.dtype)
+    _int32("q_offsets", q_offsets, pages.B + 1)
+    _bounds_of(K_pages, bounds, bound_scale)
+    layer, n_select = _c_int("layer", layer), _c_int("n_select", n_select)
+    if n_select < 1:
+        raise ValueError("n_select must be at least 1")
+    _check_workspace(workspace)
+    on = _launch_on(stream, Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale,
+                    *_given(K_scale, V_scale, workspace), *(() if out is None else out))
+    dev, Hkv = _lib or lib(), pages.kv_heads
+    if out is None:
+        # one allocation: the two tables, and the workspace 16 bytes on
+        n = T * Hkv * n_select
+        own = 0 if workspace is not None else dev.kv_pages_select_workspace_bytes(
+            T, Hkv, pages.table_cols) // 4
+        at = -(-(n + T) // 4) * 4
+        both = _new(stream, (at + own,), torch.int32, Q.device)
+        out = both[:n].view(T, Hkv, n_select), both[n:n + T]
+        if workspace is None:
+            workspace = both[at:]
+    else:
+        _int32("selected", out[0], T, Hkv, n_select)
+        _int32("lengths", out[1], T)
+        if workspace is None:
+            workspace = _new(stream, (dev.kv_pages_select_workspace_bytes(
+                T, Hkv, pages.table_cols) or 16,), torch.uint8, Q.device)
+    st = dev.kv_pages_select(Q.data_ptr(), q_ts, pages, layer, q_offsets.data_ptr(), bounds.data_ptr(),
+                             bound_scale.data_ptr(), T, H, n_select, out[0].data_ptr(),
+                             out[1].data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), on)
+    _check(st, "kv_pages_select")
+    return out
+
+
+def sdpa_paged_selected(Q, K_pages, V_pages, selected, lengths, scale: float | None = None,
+                        out_dtype: torch.dtype | None = None, layer: int = 0, num_splits: int = 0,
+                        out=None, stream=None, K_scale=None, V_scale=None):
+    """O [T, H, d] = attention of each token Q [T, H, d] over the first
+    lengths[t] rows of its own pages selected[t, g, :] (int32 [T, Hkv, n]) per
+    kv head, as ``kv_pages_select`` gives them.  A token of length 0 is passed
+    over."""
+    pools = _kv_pools(K_pages, V_pages)
+    scales = _kv_scales(K_pages, K_scale, V_scale)
+    Hkv, pd = pools[5], pools[6]
+    if Q.dim() != 3 or Q.dtype != (K_pages.dtype if scales is None else torch.bfloat16):
+        raise ValueError("Q must be [T, H, d] of the cache's dtype, or bf16 over pages in 8 bits")
+    T, H, d = Q.shape
+    q_ts = _packed("Q", Q, H, pd, Q.dtype)
+    if selected.dim() != 3:
+        raise ValueError("selected must be [T, Hkv, pages]")
+    n = selected.shape[2]
+    _int32("selected", selected, T, Hkv, n)
+    _int32("lengths", lengths, T)
+    odt = out_dtype or Q.dtype
+    layer, num_splits = _c_int("layer", layer), _c_int("num_splits", num_splits)
+    on = _launch_on(stream, Q, K_pages, V_pages, selected, lengths, Q if out is None else out,
+                    *_given(K_scale, V_scale))
+    if out is None:
+        out = _new(stream, (T, H, d), odt, Q.device)
+    elif out.shape != (T, H, d) or out.dtype != odt or not out.is_contiguous():
+        raise ValueError("out has the wrong shape, dtype or layout")
+    st = (_lib or lib()).sdpa_paged_selected(
+        Q.data_ptr(), q_ts, KvPages(*pools, None, None, 0, 1), scales, layer, selected.data_ptr(),
+        lengths.data_ptr(), n, out.data_ptr(), T, H, float(scale or 0.0), _dtype_code(odt), num_splits,
+        on)
+    _check(st, "sdpa_paged_selected")
+    return out
 
 
 class MhaHandle:

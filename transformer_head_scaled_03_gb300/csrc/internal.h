@@ -139,6 +139,12 @@ namespace mha {
 
 // The checks of an mha_kv_pages, for every entry point that takes one.
 mha_status validate_pages(const mha_kv_pages* p);
+// Those of a cache in 8 bits, and of calls that take either (scales NULL for
+// one that is not in 8 bits).
+mha_status validate_pages_e4m3(const mha_kv_pages* p, const mha_kv_scales* s);
+mha_status validate_pages_any(const mha_kv_pages* p, const mha_kv_scales* s);
+// And of calls that read no rows.
+mha_status validate_pages_shape(const mha_kv_pages* p);
 
 // The current device's error word and wait limit (false if CUDA fails).
 bool device_ctl(DeviceCtl* ctl);

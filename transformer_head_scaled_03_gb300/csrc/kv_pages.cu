@@ -19,11 +19,12 @@
 
 namespace mha {
 
-mha_status validate_pages(const mha_kv_pages* p) {
+namespace {
+
+mha_status check_pages(const mha_kv_pages* p) {
   if (!p || !p->K || !p->V) return MHA_ERR_INVALID_ARG;
   // without sequences there is no table to point to
   if (p->B > 0 && (!p->page_table || !p->kv_lengths)) return MHA_ERR_INVALID_ARG;
-  if (p->dtype != MHA_BF16 && p->dtype != MHA_F32) return MHA_ERR_INVALID_ARG;
   if (p->num_pages < 1 || p->page_size < 1 || p->kv_heads < 1 || p->d < 1 || p->layers < 1 ||
       p->B < 0 || p->table_cols < 1)
     return MHA_ERR_INVALID_ARG;
@@ -35,13 +36,37 @@ mha_status validate_pages(const mha_kv_pages* p) {
     return MHA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p->table_cols) * p->page_size > (int64_t{1} << 30))
     return MHA_ERR_UNSUPPORTED;
-  const int es = p->dtype == MHA_BF16 ? 2 : 4;
-  if ((static_cast<int64_t>(p->d) * es) % 16) return MHA_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(p->d) * bytes_of(p->dtype)) % 16) return MHA_ERR_UNSUPPORTED;
   const int64_t page = static_cast<int64_t>(p->kv_heads) * p->page_size * p->d;
   if (page > (int64_t{1} << 31)) return MHA_ERR_UNSUPPORTED;
   for (int64_t s : {p->page_stride, p->layer_stride})
     if (s < 0 || (s > 0 && s < page) || s % p->d) return MHA_ERR_INVALID_ARG;
   return MHA_OK;
+}
+
+}  // namespace
+
+mha_status validate_pages(const mha_kv_pages* p) {
+  if (p && p->dtype != MHA_BF16 && p->dtype != MHA_F32) return MHA_ERR_INVALID_ARG;
+  return check_pages(p);
+}
+
+mha_status validate_pages_e4m3(const mha_kv_pages* p, const mha_kv_scales* s) {
+  if (!p || p->dtype != MHA_E4M3 || !s || !s->K || !s->V) return MHA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(s->K) | reinterpret_cast<uintptr_t>(s->V)) & 3u)
+    return MHA_ERR_INVALID_ARG;
+  return check_pages(p);
+}
+
+mha_status validate_pages_shape(const mha_kv_pages* p) {
+  if (p && p->dtype != MHA_BF16 && p->dtype != MHA_F32 && p->dtype != MHA_E4M3)
+    return MHA_ERR_INVALID_ARG;
+  return check_pages(p);
+}
+
+mha_status validate_pages_any(const mha_kv_pages* p, const mha_kv_scales* s) {
+  if (p && p->dtype == MHA_E4M3) return validate_pages_e4m3(p, s);
+  return s ? MHA_ERR_INVALID_ARG : validate_pages(p);
 }
 
 namespace {
@@ -54,15 +79,18 @@ struct Pools {
   uint4* V;
   int64_t page_stride, layer_stride;
   int num_pages;
+  // of a cache in 8 bits, [layers, num_pages, kv_heads]; else nullptr
+  float* k_scale;
+  float* v_scale;
 };
 
-Pools pools_of(const mha_kv_pages& p) {
-  const int es = p.dtype == MHA_BF16 ? 2 : 4;
+Pools pools_of(const mha_kv_pages& p, const mha_kv_scales* s) {
+  const int es = bytes_of(p.dtype);
   const int64_t ps = p.page_stride ? p.page_stride
                                    : static_cast<int64_t>(p.kv_heads) * p.page_size * p.d;
   const int64_t ls = p.layer_stride ? p.layer_stride : ps * p.num_pages;
   return Pools{static_cast<uint4*>(p.K), static_cast<uint4*>(p.V), ps * es / 16, ls * es / 16,
-               p.num_pages};
+               p.num_pages, s ? s->K : nullptr, s ? s->V : nullptr};
 }
 
 // Copy n 16-byte vectors with a block, four loads of a thread under way at a
@@ -129,6 +157,11 @@ __global__ void __launch_bounds__(kThreads)
     const int g = s % kv_heads, kv = (s / kv_heads) & 1, y = s / (2 * kv_heads);
     uint4* base = (kv ? pool.V : pool.K) + y * pool.layer_stride + static_cast<int64_t>(g) * slab_stride;
     block_copy(base + fr * pool.page_stride, base + src * pool.page_stride, vecs);
+    if (pool.k_scale && rem && threadIdx.x == 0) {
+      float* scale = (kv ? pool.v_scale : pool.k_scale) +
+                     static_cast<int64_t>(y) * pool.num_pages * kv_heads + g;
+      scale[static_cast<int64_t>(fr) * kv_heads] = scale[static_cast<int64_t>(src) * kv_heads];
+    }
   }
 }
 
@@ -221,7 +254,8 @@ struct Renumber {
 // blockIdx.y renumbers the page tables, a sequence per block at a time.
 __global__ void __launch_bounds__(kThreads)
     kv_move_kernel(const Pools src, const Pools dst, const unsigned* __restrict__ bits,
-                   const int32_t* __restrict__ rank, int page_vecs, const Renumber tables) {
+                   const int32_t* __restrict__ rank, int page_vecs, int kv_heads,
+                   const Renumber tables) {
   pdl_wait();
   if (blockIdx.y == gridDim.y - 1) {
     for (int b = blockIdx.x; b < tables.B; b += gridDim.x) {
@@ -246,6 +280,13 @@ __global__ void __launch_bounds__(kThreads)
     const int r = rank_of(bits, rank, page);
     if (r >= dst.num_pages) continue;
     block_copy(to0 + r * dst.page_stride, from0 + page * src.page_stride, page_vecs);
+    if (src.k_scale) {
+      const float* from = (kv ? src.v_scale : src.k_scale) +
+                          (static_cast<int64_t>(y) * src.num_pages + page) * kv_heads;
+      float* to = (kv ? dst.v_scale : dst.k_scale) +
+                  (static_cast<int64_t>(y) * dst.num_pages + r) * kv_heads;
+      for (int g = threadIdx.x; g < kv_heads; g += kThreads) to[g] = from[g];
+    }
   }
 }
 
@@ -261,50 +302,47 @@ int num_sms() {
 
 int words_of(int num_pages) { return (num_pages + 31) / 32; }
 
-}  // namespace
-}  // namespace mha
-
-using namespace mha;
-
-extern "C" {
-
-mha_status kv_pages_fork(const mha_kv_pages* pages, const int32_t* parents,
-                         const int32_t* children, const int32_t* fresh, int n, mha_stream stream) {
-  const mha_status st = validate_pages(pages);
-  if (st != MHA_OK) return st;
+// The entry points' common part, after the checks of the pages and scales.
+mha_status fork_pages(const mha_kv_pages* pages, const mha_kv_scales* scales,
+                      const int32_t* parents, const int32_t* children, const int32_t* fresh, int n,
+                      mha_stream stream) {
   if (n < 0 || n > pages->B) return MHA_ERR_INVALID_ARG;
   if (n == 0) return MHA_OK;
   for (const int32_t* p : {parents, children, fresh})
     if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return MHA_ERR_INVALID_ARG;
   DeviceCtl ctl;
   if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
-  const int es = pages->dtype == MHA_BF16 ? 2 : 4;
+  const int es = bytes_of(pages->dtype);
   const int64_t slabs = static_cast<int64_t>(pages->layers) * 2 * pages->kv_heads;
   // every block checks its pair against all others first: no more blocks than
   // keep the SMs full (about sixteen each)
   const int64_t want = (16 * static_cast<int64_t>(num_sms()) + n - 1) / n;
   const dim3 grid(n, static_cast<unsigned>(slabs < want ? slabs : want));
   kv_fork_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      pools_of(*pages), pages->page_table, pages->kv_lengths, parents, children, fresh, n,
+      pools_of(*pages, scales), pages->page_table, pages->kv_lengths, parents, children, fresh, n,
       pages->B, pages->table_cols, page_shift_of(pages->page_size), pages->kv_heads,
       pages->d * es / 16, pages->layers, ctl.err);
   return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 
-size_t kv_pages_compact_workspace_bytes(int num_pages) {
+size_t compact_workspace_bytes(int num_pages) {
   if (num_pages < 1 || num_pages > kMaxPages) return 0;
   return static_cast<size_t>(words_of(num_pages)) * 8;  // bits, ranks
 }
 
-mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, int32_t* n_live,
-                            void* workspace, size_t workspace_bytes, mha_stream stream) {
-  mha_status st = validate_pages(src);
+mha_status compact_pages(const mha_kv_pages* src, const mha_kv_scales* src_scales,
+                         const mha_kv_pages* dst, const mha_kv_scales* dst_scales, int32_t* n_live,
+                         void* workspace, size_t workspace_bytes, mha_stream stream) {
+  mha_status st = validate_pages_any(src, src_scales);
   if (st != MHA_OK) return st;
   if (!dst) return MHA_ERR_INVALID_ARG;
   mha_kv_pages to = *dst;
   to.kv_lengths = src->kv_lengths;  // dst's own are not used
-  st = validate_pages(&to);
+  st = validate_pages_any(&to, dst_scales);
   if (st != MHA_OK) return st;
+  if (src_scales && (src_scales->K == dst_scales->K || src_scales->V == dst_scales->V ||
+                     src_scales->K == dst_scales->V || src_scales->V == dst_scales->K))
+    return MHA_ERR_INVALID_ARG;
   if (src->num_pages > kMaxPages) return MHA_ERR_UNSUPPORTED;
   if (dst->dtype != src->dtype || dst->page_size != src->page_size ||
       dst->kv_heads != src->kv_heads || dst->d != src->d || dst->layers != src->layers ||
@@ -315,7 +353,7 @@ mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, in
     return MHA_ERR_INVALID_ARG;
   if (!n_live || (reinterpret_cast<uintptr_t>(n_live) & 3u) || !workspace ||
       (reinterpret_cast<uintptr_t>(workspace) & 15u) ||
-      workspace_bytes < kv_pages_compact_workspace_bytes(src->num_pages))
+      workspace_bytes < compact_workspace_bytes(src->num_pages))
     return MHA_ERR_INVALID_ARG;
   if (src->layers > 32767) return MHA_ERR_UNSUPPORTED;
   DeviceCtl ctl;
@@ -325,7 +363,7 @@ mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, in
   unsigned* bits = static_cast<unsigned*>(workspace);
   int32_t* rank = reinterpret_cast<int32_t*>(bits + words);
   const int shift = page_shift_of(src->page_size);
-  const int es = src->dtype == MHA_BF16 ? 2 : 4;
+  const int es = bytes_of(src->dtype);
   const int page_vecs = src->kv_heads * src->page_size * (src->d * es / 16);
   cudaError_t e = cudaFuncSetAttribute(kv_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxPages / 8);
@@ -345,11 +383,49 @@ mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, in
   cfg.numAttrs = 1;
   const Renumber tables{src->page_table, src->kv_lengths, src->B, src->table_cols, shift,
                         dst->page_table, dst->table_cols};
-  e = cudaLaunchKernelEx(&cfg, kv_move_kernel, pools_of(*src), pools_of(*dst),
+  e = cudaLaunchKernelEx(&cfg, kv_move_kernel, pools_of(*src, src_scales), pools_of(*dst, dst_scales),
                          static_cast<const unsigned*>(bits), static_cast<const int32_t*>(rank),
-                         page_vecs, tables);
+                         page_vecs, src->kv_heads, tables);
   if (e != cudaSuccess) return MHA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mha
+
+using namespace mha;
+
+extern "C" {
+
+mha_status kv_pages_fork(const mha_kv_pages* pages, const int32_t* parents,
+                         const int32_t* children, const int32_t* fresh, int n, mha_stream stream) {
+  const mha_status st = validate_pages(pages);
+  return st != MHA_OK ? st : fork_pages(pages, nullptr, parents, children, fresh, n, stream);
+}
+
+mha_status kv_pages_fork_e4m3(const mha_kv_pages* pages, const mha_kv_scales* scales,
+                              const int32_t* parents, const int32_t* children,
+                              const int32_t* fresh, int n, mha_stream stream) {
+  const mha_status st = validate_pages_e4m3(pages, scales);
+  return st != MHA_OK ? st : fork_pages(pages, scales, parents, children, fresh, n, stream);
+}
+
+size_t kv_pages_compact_workspace_bytes(int num_pages) {
+  return compact_workspace_bytes(num_pages);
+}
+
+mha_status kv_pages_compact(const mha_kv_pages* src, const mha_kv_pages* dst, int32_t* n_live,
+                            void* workspace, size_t workspace_bytes, mha_stream stream) {
+  return compact_pages(src, nullptr, dst, nullptr, n_live, workspace, workspace_bytes, stream);
+}
+
+mha_status kv_pages_compact_e4m3(const mha_kv_pages* src, const mha_kv_scales* src_scales,
+                                 const mha_kv_pages* dst, const mha_kv_scales* dst_scales,
+                                 int32_t* n_live, void* workspace, size_t workspace_bytes,
+                                 mha_stream stream) {
+  if (!src_scales || !dst_scales) return MHA_ERR_INVALID_ARG;
+  return compact_pages(src, src_scales, dst, dst_scales, n_live, workspace, workspace_bytes,
+                       stream);
 }
 
 }  // extern "C"

@@ -18,7 +18,12 @@ struct PagesView {
   const int32_t* table;
   const int32_t* kv_len;
   int B, cols;
+  // of a cache in 8 bits, [num_pages, kv_heads]; else nullptr
+  float* k_scale;
+  float* v_scale;
 };
+
+inline int bytes_of(mha_dtype t) { return t == MHA_E4M3 ? 1 : t == MHA_BF16 ? 2 : 4; }
 
 // log2 of a page size that pages_view has accepted.
 inline int page_shift_of(int page_size) {
@@ -28,14 +33,16 @@ inline int page_shift_of(int page_size) {
 }
 
 // The layer's view of checked pages.
-inline PagesView pages_view(const mha_kv_pages& p, int layer) {
+inline PagesView pages_view(const mha_kv_pages& p, int layer, const mha_kv_scales* s = nullptr) {
   const int64_t ps = p.page_stride ? p.page_stride
                                    : static_cast<int64_t>(p.kv_heads) * p.page_size * p.d;
   const int64_t ls = p.layer_stride ? p.layer_stride : ps * p.num_pages;
-  const int64_t off = ls * layer * (p.dtype == MHA_BF16 ? 2 : 4);
+  const int64_t off = ls * layer * bytes_of(p.dtype);
+  const int64_t scale_off = static_cast<int64_t>(p.num_pages) * p.kv_heads * layer;
   return PagesView{static_cast<char*>(p.K) + off, static_cast<char*>(p.V) + off, p.num_pages,
                    page_shift_of(p.page_size), p.kv_heads, p.d, ps, p.page_table, p.kv_lengths,
-                   p.B, p.table_cols};
+                   p.B, p.table_cols, s ? s->K + scale_off : nullptr,
+                   s ? s->V + scale_off : nullptr};
 }
 
 // Which packed token belongs to which sequence: the number of sequences that

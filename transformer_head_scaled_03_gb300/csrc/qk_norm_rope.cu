@@ -34,6 +34,8 @@
 #include <stdint.h>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "internal.h"
 #include "kv_pages.cuh"
@@ -664,20 +666,20 @@ struct PagedArgs {
 
 constexpr int kMaxBlockTokens = 8;  // one warp looks one token up
 
-// A block takes block_tokens tokens (gridDim.y blocks share them when there
+// A block takes block_tokens tokens (`parts` blocks share them when there
 // are few): their sequences, positions and page rows are looked up once, a
 // warp per token, then all warps take their rows, queries, keys and values,
-// kRows at a time.
-template <int D, int HALF>
-__global__ void __launch_bounds__(32 * kWarps)
-    norm_rope_paged_kernel(const PagedArgs p, int block_tokens) {
+// kRows at a time (without KV the queries alone).
+template <int D, int HALF, bool KV>
+__device__ __forceinline__ void norm_rope_paged_rows(const PagedArgs& p, int block, int part,
+                                                     int parts, int block_tokens) {
   using V = VecLane<D>;
   __shared__ int64_t row_at[kMaxBlockTokens];  // the token's pool row of head 0, in elements
   __shared__ int pos_of[kMaxBlockTokens];      // -1: no sequence's, -2: a bad entry
   const PagesView& pg = p.pages;
   const V at(p.r);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * block_tokens;
+  const int t0 = block * block_tokens;
   const int tokens = min(block_tokens, p.T - t0);
   if (warp < tokens) {
     const int t = t0 + warp;
@@ -713,9 +715,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   __syncthreads();
   const int head_rows = D << pg.page_shift;  // elements from kv head to kv head of a page
   const int q_items = (tokens * p.H + V::kRows - 1) / V::kRows;
-  const int kv_items = (tokens * pg.kv_heads + V::kRows - 1) / V::kRows;
-  for (int it = blockIdx.y * kWarps + warp; it < q_items + 2 * kv_items;
-       it += gridDim.y * kWarps) {
+  const int kv_items = KV ? (tokens * pg.kv_heads + V::kRows - 1) / V::kRows : 0;
+  for (int it = part * kWarps + warp; it < q_items + 2 * kv_items; it += parts * kWarps) {
     // queries, keys, values: uniform in a warp
     const int w = it < q_items ? 0 : it < q_items + kv_items ? 1 : 2;
     const int heads = w ? pg.kv_heads : p.H;
@@ -757,6 +758,228 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     store8(y + at.a, a);
     store8(y + at.b, b);
+  }
+}
+
+template <int D, int HALF>
+__global__ void __launch_bounds__(32 * kWarps)
+    norm_rope_paged_kernel(const PagedArgs p, int block_tokens) {
+  norm_rope_paged_rows<D, HALF, true>(p, blockIdx.x, blockIdx.y, gridDim.y, block_tokens);
+}
+
+// ---------------------------------------------------------- pages in 8 bits
+
+// The smallest power of two s >= 2^-100 with x <= 448 s; 0 for x = 0.  448 is
+// 1.75 * 2^8.
+__device__ __forceinline__ float e4m3_scale_of(float x) {
+  if (x == 0.f) return 0.f;
+  const unsigned u = __float_as_uint(x);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, -100);
+  return __uint_as_float(static_cast<unsigned>(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float finite_or_nan(float x) {
+  return isfinite(x) ? x : __uint_as_float(0x7fffffffu);
+}
+
+__device__ __forceinline__ void store8_e4m3(uint8_t* y, const float2 (&v)[4], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = e4m3x2(finite_or_nan(v[2 * i].x) * inv, finite_or_nan(v[2 * i].y) * inv) |
+           e4m3x2(finite_or_nan(v[2 * i + 1].x) * inv, finite_or_nan(v[2 * i + 1].y) * inv) << 16;
+  *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float finite_max(const float2 (&v)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = fabsf(v[i].x), b = fabsf(v[i].y);
+    m = fmaxf(m, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+  }
+  return m;
+}
+
+// Sixteen codes times r.
+__device__ __forceinline__ uint4 rescale16(uint4 u, float r) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o = 0u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+          static_cast<__nv_fp8x2_storage_t>(w[i] >> (16 * k) & 0xffffu), __NV_E4M3)));
+      o |= e4m3x2(f.x * r, f.y * r) << (16 * k);
+    }
+    w[i] = o;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The page that unit `rest` of the touched ones is, sequence by sequence, 32
+// of them at a time: its sequence's place and new tokens.
+struct TouchedPage {
+  int q0, first, len, page;  // first: position of the sequence's first new token
+  int col;
+};
+
+__device__ __forceinline__ bool touched_page(const PagedArgs& p, int64_t rest, TouchedPage* out) {
+  const PagesView& pg = p.pages;
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < pg.B; b0 += 32) {
+    const int b = b0 + lane;
+    int q0 = 0, first = 0, len = 0, count = 0;
+    if (b < pg.B) {
+      q0 = __ldg(p.q_offsets + b);
+      const int q1 = __ldg(p.q_offsets + b + 1);
+      len = __ldg(pg.kv_len + b);
+      const int n = q1 - q0;
+      first = len - n;
+      // what is wrong is reported with the queries
+      if (q0 >= 0 && n > 0 && q1 <= p.T && first >= 0 &&
+          len <= (static_cast<int64_t>(pg.cols) << pg.page_shift))
+        count = ((len - 1) >> pg.page_shift) - (first >> pg.page_shift) + 1;
+    }
+    int64_t incl = count;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += up;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, rest < incl);
+    if (in) {
+      const int src = __ffs(in) - 1;
+      const int64_t off = __shfl_sync(0xffffffffu, rest - (incl - count), src);
+      out->q0 = __shfl_sync(0xffffffffu, q0, src);
+      out->first = __shfl_sync(0xffffffffu, first, src);
+      out->len = __shfl_sync(0xffffffffu, len, src);
+      out->col = (out->first >> pg.page_shift) + static_cast<int>(off);
+      out->page = __ldg(pg.table + static_cast<int64_t>(b0 + src) * pg.cols + out->col);
+      return out->page >= 0 && out->page < pg.num_pages;
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// One unit, (touched page, keys or values, kv head), by NW warps: the largest
+// new element, the scale, the older rows where it has grown, the new rows.
+// Rows beyond kKept rounds are computed twice rather than kept.
+template <int D, int HALF, int NW>
+__device__ __forceinline__ void append_e4m3_unit(const PagedArgs& p, int64_t unit, float* tops) {
+  using V = VecLane<D>;
+  constexpr int kKept = 2;
+  constexpr int kGroups = NW * V::kRows;  // rows at a time
+  const PagesView& pg = p.pages;
+  const V at(p.r);
+  const int lane = threadIdx.x & 31;
+  const int warp = NW == 1 ? 0 : threadIdx.x >> 5;
+  const int g = static_cast<int>(unit % pg.kv_heads);
+  const int w = static_cast<int>(unit / pg.kv_heads) & 1;  // 0: keys
+  TouchedPage tp;
+  if (!touched_page(p, unit / (2 * pg.kv_heads), &tp)) return;  // the same for all its warps
+  const int start = tp.col << pg.page_shift;
+  const int r0 = max(tp.first - start, 0);  // older rows
+  int r1 = min(tp.len - start, 1 << pg.page_shift);
+  r1 = min(r1, max(p.pe_rows - start, r0));  // a token behind the table is left out
+  if (r1 <= r0) return;
+  const int64_t scale_at = static_cast<int64_t>(tp.page) * pg.kv_heads + g;
+  float* scale = (w ? pg.v_scale : pg.k_scale) + scale_at;
+  const float old = r0 > 0 ? *scale : 0.f;
+  uint8_t* to = static_cast<uint8_t*>(w ? pg.V : pg.K) + tp.page * pg.page_stride +
+                ((static_cast<int64_t>(g) * D) << pg.page_shift);
+  const __nv_bfloat16* x = (w ? p.v : p.k) + static_cast<int64_t>(g) * D;
+  const int64_t ts = w ? p.vs : p.ks;
+  const int64_t t0 = tp.q0 + start - tp.first;  // token of page row 0
+  auto row_values = [&](int row, float2 (&a)[4], float2 (&b)[4]) {
+    Raw8<__nv_bfloat16> ra, rb;
+    ra.zero();
+    rb.zero();
+    if (row < r1) {
+      ra.load(x + (t0 + row) * ts + at.a);
+      rb.load(x + (t0 + row) * ts + at.b);
+    }
+    ra.get(a);
+    rb.get(b);
+    if (w == 0) {
+      Turns turns;
+      turns.load(p.pe + static_cast<int64_t>(start + min(row, r1 - 1)) * p.r, at.a, at.b, at.turns,
+                 HALF);
+      norm_rope_vec<D, HALF>(a, b, p.gk, at, turns, p.eps);
+      if (row >= r1) {  // gamma may be infinite
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = b[i] = make_float2(0.f, 0.f);
+      }
+    }
+  };
+  const int row0 = r0 + warp * V::kRows + lane / V::kLanes;
+  float2 a[kKept][4], b[kKept][4];
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) {
+    if (k == 0 || r0 + k * kGroups < r1) {
+      row_values(row0 + k * kGroups, a[k], b[k]);
+      top = fmaxf(top, fmaxf(finite_max(a[k]), finite_max(b[k])));
+    }
+  }
+  for (int r = kKept * kGroups; r0 + r < r1; r += kGroups) {
+    float2 c[4], d[4];
+    row_values(row0 + r, c, d);
+    top = fmaxf(top, fmaxf(finite_max(c), finite_max(d)));
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  if constexpr (NW > 1) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();  // every warp has read the old scale, too
+#pragma unroll
+    for (int k = 0; k < NW; ++k) top = fmaxf(top, tops[k]);
+  }
+  const float s = fmaxf(old, e4m3_scale_of(top));
+  const float inv = s > 0.f ? 1.f / s : 0.f;
+  if (old > 0.f && s > old) {
+    const int vecs = r0 * D / 16;
+    for (int v = warp * 32 + lane; v < vecs; v += 32 * NW) {
+      uint4* c = reinterpret_cast<uint4*>(to) + v;
+      *c = rescale16(*c, old * inv);
+    }
+  }
+  auto put = [&](int row, const float2 (&a)[4], const float2 (&b)[4]) {
+    if (row >= r1) return;
+    store8_e4m3(to + row * D + at.a, a, inv);
+    store8_e4m3(to + row * D + at.b, b, inv);
+  };
+#pragma unroll
+  for (int k = 0; k < kKept; ++k)
+    if (k == 0 || r0 + k * kGroups < r1) put(row0 + k * kGroups, a[k], b[k]);
+  for (int r = kKept * kGroups; r0 + r < r1; r += kGroups) {
+    float2 c[4], d[4];
+    row_values(row0 + r, c, d);
+    put(row0 + r, c, d);
+  }
+  if (warp == 0 && lane == 0) *scale = s;
+}
+
+// The first `page_blocks` blocks take the touched pages, a unit each (NW = 8)
+// or one to a warp (NW = 1: few rows to a page); the others the queries.
+template <int D, int HALF, int NW>
+__global__ void __launch_bounds__(32 * kWarps)
+    norm_rope_paged_e4m3_kernel(const PagedArgs p, int page_blocks, int block_tokens, int parts) {
+  __shared__ float tops[kWarps];
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < page_blocks) {
+    append_e4m3_unit<D, HALF, NW>(
+        p, NW == 1 ? static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5) : block, tops);
+  } else {
+    const int q = block - page_blocks;
+    norm_rope_paged_rows<D, HALF, false>(p, q / parts, q % parts, parts, block_tokens);
   }
 }
 
@@ -838,6 +1061,92 @@ mha_status check_rows(const void* x, int64_t* ts, int heads, int d, int dtype, b
   if (bad_ptr(x, 16)) return MHA_ERR_INVALID_ARG;
   if (vec && (*ts * (dtype == MHA_BF16 ? 2 : 4)) % 16) return MHA_ERR_INVALID_ARG;
   return MHA_OK;
+}
+
+// Units of the 8-bit pages and blocks of the queries in one launch.
+cudaError_t launch_append_e4m3(const PagedArgs& p, int d, int block_tokens, cudaStream_t s) {
+  const PagesView& pg = p.pages;
+  // pages that T tokens can touch: two for every sequence, and one for every
+  // page_size tokens
+  const int64_t seqs = p.T < pg.B ? p.T : pg.B;
+  const int64_t touched = (p.T >> pg.page_shift) + 2 * seqs;
+  const int64_t units = (touched < p.T ? touched : p.T) * 2 * pg.kv_heads;
+  // a warp to a unit while its rows are at most four on average
+  const bool few = p.T <= 4 * seqs;
+  const int64_t page_blocks = few ? (units + kWarps - 1) / kWarps : units;
+  const int token_blocks = (p.T + block_tokens - 1) / block_tokens;
+  const int rounds = (block_tokens * p.H + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
+  const int room = 2 * num_sms() / token_blocks;
+  const int parts = room < 1 ? 1 : room < rounds ? room : rounds;
+  const int64_t blocks = page_blocks + static_cast<int64_t>(token_blocks) * parts;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  auto go = [&](auto kern) {
+    kern<<<grid, 32 * kWarps, 0, s>>>(p, static_cast<int>(page_blocks), block_tokens, parts);
+  };
+  const bool half = p.half == MHA_ROPE_HALF;
+  if (d == 64 && few)
+    half ? go(norm_rope_paged_e4m3_kernel<64, 1, 1>) : go(norm_rope_paged_e4m3_kernel<64, 0, 1>);
+  else if (d == 64)
+    half ? go(norm_rope_paged_e4m3_kernel<64, 1, 8>) : go(norm_rope_paged_e4m3_kernel<64, 0, 8>);
+  else if (few)
+    half ? go(norm_rope_paged_e4m3_kernel<128, 1, 1>) : go(norm_rope_paged_e4m3_kernel<128, 0, 1>);
+  else
+    half ? go(norm_rope_paged_e4m3_kernel<128, 1, 8>) : go(norm_rope_paged_e4m3_kernel<128, 0, 8>);
+  return cudaGetLastError();
+}
+
+// The entry points' common part, after the checks of the pages and scales.
+mha_status append_paged(const void* Q, int64_t q_token_stride, const void* K,
+                        int64_t k_token_stride, const void* V, int64_t v_token_stride,
+                        const void* gamma_q, const void* gamma_k, const float* pe, int pe_rows,
+                        int rope_dim, int pairing, void* Qo, const mha_kv_pages* pages,
+                        const mha_kv_scales* scales, int layer, const int32_t* q_offsets, int T,
+                        int H, float eps, mha_stream stream) {
+  if (T < 0 || H < 1 || layer < 0 || layer >= pages->layers) return MHA_ERR_INVALID_ARG;
+  if (pages->dtype == MHA_F32) return MHA_ERR_UNSUPPORTED;
+  const int d = pages->d, Hkv = pages->kv_heads;
+  mha_status st = check_rope(pe, pe_rows, rope_dim, pairing, d, eps, MHA_BF16);
+  if (st != MHA_OK) return st;
+  if (!vector_rows(d, rope_dim)) return MHA_ERR_UNSUPPORTED;
+  if (T == 0 || pages->B == 0) return MHA_OK;
+  st = check_rows(Q, &q_token_stride, H, d, MHA_BF16, true);
+  if (st == MHA_OK) st = check_rows(K, &k_token_stride, Hkv, d, MHA_BF16, true);
+  if (st == MHA_OK) st = check_rows(V, &v_token_stride, Hkv, d, MHA_BF16, true);
+  if (st != MHA_OK) return st;
+  if (bad_ptr(gamma_q, 16) || bad_ptr(gamma_k, 16) || bad_ptr(Qo, 16) || Qo == Q ||
+      bad_ptr(q_offsets, 4))
+    return MHA_ERR_INVALID_ARG;
+  DeviceCtl ctl;
+  if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
+  auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
+  const PagedArgs p{bf(Q), bf(K), bf(V), q_token_stride, k_token_stride, v_token_stride,
+                    bf(gamma_q), bf(gamma_k), pe, pe_rows, rope_dim, pairing,
+                    static_cast<__nv_bfloat16*>(Qo), pages_view(*pages, layer, scales), q_offsets, T, H,
+                    eps, ctl.err};
+  // a block per token until the SMs have four each, then up to eight tokens
+  const int64_t per_block = T / (4 * static_cast<int64_t>(num_sms()));
+  const int block_tokens = per_block < 1 ? 1 : per_block < kMaxBlockTokens
+                                                   ? static_cast<int>(per_block)
+                                                   : kMaxBlockTokens;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (scales)
+    return launch_append_e4m3(p, d, block_tokens, s) == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+  // a round of rows for every warp, as long as the SMs have room
+  const int token_blocks = (T + block_tokens - 1) / block_tokens;
+  const int rounds = (H + 2 * Hkv + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
+  const int room = 2 * num_sms() / token_blocks;
+  const dim3 grid(static_cast<unsigned>(token_blocks),
+                  static_cast<unsigned>(room < 1 ? 1 : room < rounds ? room : rounds));
+  if (d == 64 && pairing == MHA_ROPE_HALF)
+    norm_rope_paged_kernel<64, 1><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
+  else if (d == 64)
+    norm_rope_paged_kernel<64, 0><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
+  else if (pairing == MHA_ROPE_HALF)
+    norm_rope_paged_kernel<128, 1><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
+  else
+    norm_rope_paged_kernel<128, 0><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
+  return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 
 }  // namespace
@@ -972,50 +1281,25 @@ mha_status qk_norm_rope_paged(const void* Q, int64_t q_token_stride, const void*
                               int pe_rows, int rope_dim, int pairing, void* Qo,
                               const mha_kv_pages* pages, int layer, const int32_t* q_offsets,
                               int T, int H, float eps, mha_stream stream) {
-  mha_status st = validate_pages(pages);
+  const mha_status st = validate_pages(pages);
   if (st != MHA_OK) return st;
-  if (T < 0 || H < 1 || layer < 0 || layer >= pages->layers) return MHA_ERR_INVALID_ARG;
-  if (pages->dtype != MHA_BF16) return MHA_ERR_UNSUPPORTED;
-  const int d = pages->d, Hkv = pages->kv_heads;
-  st = check_rope(pe, pe_rows, rope_dim, pairing, d, eps, MHA_BF16);
+  return append_paged(Q, q_token_stride, K, k_token_stride, V, v_token_stride, gamma_q, gamma_k, pe,
+                      pe_rows, rope_dim, pairing, Qo, pages, nullptr, layer, q_offsets, T, H, eps,
+                      stream);
+}
+
+mha_status qk_norm_rope_paged_e4m3(const void* Q, int64_t q_token_stride, const void* K,
+                                   int64_t k_token_stride, const void* V, int64_t v_token_stride,
+                                   const void* gamma_q, const void* gamma_k, const float* pe,
+                                   int pe_rows, int rope_dim, int pairing, void* Qo,
+                                   const mha_kv_pages* pages, const mha_kv_scales* scales,
+                                   int layer, const int32_t* q_offsets, int T, int H, float eps,
+                                   mha_stream stream) {
+  const mha_status st = validate_pages_e4m3(pages, scales);
   if (st != MHA_OK) return st;
-  if (!vector_rows(d, rope_dim)) return MHA_ERR_UNSUPPORTED;
-  if (T == 0 || pages->B == 0) return MHA_OK;
-  st = check_rows(Q, &q_token_stride, H, d, MHA_BF16, true);
-  if (st == MHA_OK) st = check_rows(K, &k_token_stride, Hkv, d, MHA_BF16, true);
-  if (st == MHA_OK) st = check_rows(V, &v_token_stride, Hkv, d, MHA_BF16, true);
-  if (st != MHA_OK) return st;
-  if (bad_ptr(gamma_q, 16) || bad_ptr(gamma_k, 16) || bad_ptr(Qo, 16) || Qo == Q ||
-      bad_ptr(q_offsets, 4))
-    return MHA_ERR_INVALID_ARG;
-  DeviceCtl ctl;
-  if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
-  auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
-  const PagedArgs p{bf(Q), bf(K), bf(V), q_token_stride, k_token_stride, v_token_stride,
-                    bf(gamma_q), bf(gamma_k), pe, pe_rows, rope_dim, pairing,
-                    static_cast<__nv_bfloat16*>(Qo), pages_view(*pages, layer), q_offsets, T, H,
-                    eps, ctl.err};
-  // a block per token until the SMs have four each, then up to eight tokens
-  const int64_t per_block = T / (4 * static_cast<int64_t>(num_sms()));
-  const int block_tokens = per_block < 1 ? 1 : per_block < kMaxBlockTokens
-                                                   ? static_cast<int>(per_block)
-                                                   : kMaxBlockTokens;
-  // a round of rows for every warp, as long as the SMs have room
-  const int token_blocks = (T + block_tokens - 1) / block_tokens;
-  const int rounds = (H + 2 * Hkv + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
-  const int room = 2 * num_sms() / token_blocks;
-  const dim3 grid(static_cast<unsigned>(token_blocks),
-                  static_cast<unsigned>(room < 1 ? 1 : room < rounds ? room : rounds));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (d == 64 && pairing == MHA_ROPE_HALF)
-    norm_rope_paged_kernel<64, 1><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
-  else if (d == 64)
-    norm_rope_paged_kernel<64, 0><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
-  else if (pairing == MHA_ROPE_HALF)
-    norm_rope_paged_kernel<128, 1><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
-  else
-    norm_rope_paged_kernel<128, 0><<<grid, 32 * kWarps, 0, s>>>(p, block_tokens);
-  return cudaGetLastError() == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+  return append_paged(Q, q_token_stride, K, k_token_stride, V, v_token_stride, gamma_q, gamma_k, pe,
+                      pe_rows, rope_dim, pairing, Qo, pages, scales, layer, q_offsets, T, H, eps,
+                      stream);
 }
 
 }  // extern "C"

@@ -112,17 +112,16 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
   return best;
 }
 
-}  // namespace mha
+namespace {
 
-using namespace mha;
-
-extern "C" {
-
-mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages* pages, int layer,
-                      const int32_t* q_offsets, void* O, int T, int H, int max_new, float scale,
-                      int mask_kind, mha_dtype out_dtype, int num_splits, mha_stream stream) {
-  const mha_status st = validate_pages(pages);
-  if (st != MHA_OK) return st;
+// The entry points' common part: the checks that follow those of the pages,
+// and the choice of the kernel.  `selected`: a page table per token and kv
+// head, [T, kv_heads, cols], with the tokens' lengths; else nullptr.
+mha_status attend(const void* Q, int64_t q_token_stride, const mha_kv_pages* pages,
+                  const mha_kv_scales* scales, int layer, const int32_t* q_offsets,
+                  const int32_t* selected, const int32_t* lengths, int cols, void* O, int T, int H,
+                  int max_new, float scale, int mask_kind, mha_dtype out_dtype, int num_splits,
+                  mha_stream stream) {
   if (T < 0 || H < 1 || max_new < (T > 0 ? 1 : 0) || layer < 0 || layer >= pages->layers ||
       H % pages->kv_heads != 0)
     return MHA_ERR_INVALID_ARG;
@@ -135,18 +134,32 @@ mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages*
   if (q_token_stride == 0) q_token_stride = static_cast<int64_t>(H) * d;
   if (q_token_stride < static_cast<int64_t>(H) * d || q_token_stride % d)
     return MHA_ERR_INVALID_ARG;
-  if (pages->dtype != MHA_BF16 || (d != 64 && d != 128) || G > 128) return MHA_ERR_UNSUPPORTED;
-  if (T == 0 || pages->B == 0) return MHA_OK;
+  if (pages->dtype == MHA_F32 || (d != 64 && d != 128) || G > 128) return MHA_ERR_UNSUPPORTED;
+  const bool by_token = !q_offsets && lengths;
+  if (T == 0 || (!by_token && pages->B == 0)) return MHA_OK;
   for (const void* p : {Q, static_cast<const void*>(O)})
     if (!p || (reinterpret_cast<uintptr_t>(p) & 15u)) return MHA_ERR_INVALID_ARG;
-  if (O == Q || !q_offsets || (reinterpret_cast<uintptr_t>(q_offsets) & 3u))
+  if (O == Q) return MHA_ERR_INVALID_ARG;
+  if (by_token) {
+    if (!selected || ((reinterpret_cast<uintptr_t>(selected) |
+                       reinterpret_cast<uintptr_t>(lengths)) & 3u))
+      return MHA_ERR_INVALID_ARG;
+  } else if (!q_offsets || (reinterpret_cast<uintptr_t>(q_offsets) & 3u)) {
     return MHA_ERR_INVALID_ARG;
+  }
   DeviceCtl ctl;
   if (!device_ctl(&ctl)) return MHA_ERR_CUDA;
   PagedSdpaArgs a;
   a.Q = Q;
   a.q_stride = q_token_stride;
-  a.pages = pages_view(*pages, layer);
+  a.pages = pages_view(*pages, layer, scales);
+  a.head_tables = by_token;
+  if (by_token) {
+    a.pages.table = selected;
+    a.pages.kv_len = lengths;
+    a.pages.B = T;
+    a.pages.cols = cols;
+  }
   a.q_offsets = q_offsets;
   a.O = O;
   a.T = T;
@@ -164,10 +177,52 @@ mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages*
   // 856 us, where the single tokens alone take 667 and the chunk alone 229.
   // Single tokens with a loose max_new pay for it: 64 sequences of 200 to 1000
   // keys 59 us instead of 45, 16 of 16 to 32 K 279 instead of 240.
+  if (scales) return launch_sdpa_paged_simple(a, ctl) == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
   const cudaError_t e = static_cast<int64_t>(a.max_new) * G <= kPagedFewRows
                             ? launch_sdpa_paged_few(a, ctl)
                             : launch_sdpa_paged_rows(a, ctl);
   return e == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mha
+
+using namespace mha;
+
+extern "C" {
+
+mha_status sdpa_paged(const void* Q, int64_t q_token_stride, const mha_kv_pages* pages, int layer,
+                      const int32_t* q_offsets, void* O, int T, int H, int max_new, float scale,
+                      int mask_kind, mha_dtype out_dtype, int num_splits, mha_stream stream) {
+  const mha_status st = validate_pages(pages);
+  if (st != MHA_OK) return st;
+  return attend(Q, q_token_stride, pages, nullptr, layer, q_offsets, nullptr, nullptr, 0, O, T, H,
+                max_new, scale, mask_kind, out_dtype, num_splits, stream);
+}
+
+mha_status sdpa_paged_e4m3(const void* Q, int64_t q_token_stride, const mha_kv_pages* pages,
+                           const mha_kv_scales* scales, int layer, const int32_t* q_offsets,
+                           void* O, int T, int H, int max_new, float scale, int mask_kind,
+                           mha_dtype out_dtype, int num_splits, mha_stream stream) {
+  const mha_status st = validate_pages_e4m3(pages, scales);
+  if (st != MHA_OK) return st;
+  return attend(Q, q_token_stride, pages, scales, layer, q_offsets, nullptr, nullptr, 0, O, T, H,
+                max_new, scale, mask_kind, out_dtype, num_splits, stream);
+}
+
+mha_status sdpa_paged_selected(const void* Q, int64_t q_token_stride, const mha_kv_pages* pages,
+                               const mha_kv_scales* scales, int layer, const int32_t* selected,
+                               const int32_t* lengths, int n_select, void* O, int T, int H,
+                               float scale, mha_dtype out_dtype, int num_splits,
+                               mha_stream stream) {
+  const mha_status st = validate_pages_any(pages, scales);
+  if (st != MHA_OK) return st;
+  if (n_select < 1) return MHA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_select) * pages->page_size > (int64_t{1} << 30))
+    return MHA_ERR_UNSUPPORTED;
+  if (T > 0 && (!selected || !lengths)) return MHA_ERR_INVALID_ARG;
+  return attend(Q, q_token_stride, pages, scales, layer, nullptr, selected, lengths, n_select, O, T,
+                H, 1, scale, MHA_MASK_CAUSAL_BOTTOM_RIGHT, out_dtype, num_splits, stream);
 }
 
 }  // extern "C"

@@ -14,8 +14,9 @@ namespace mha {
 struct PagedSdpaArgs {
   const void* Q;
   int64_t q_stride;  // elements from token to token
-  PagesView pages;
-  const int32_t* q_offsets;
+  PagesView pages;   // with a table per token and kv head: B = T, kv_len a token's
+  const int32_t* q_offsets;  // nullptr: "sequence" t is token t alone
+  bool head_tables;  // the page table is [B, kv_heads, cols]
   void* O;  // [T, H, d]
   int T, H, G, max_new;
   bool causal, out_f32;
@@ -27,6 +28,7 @@ struct PagedSdpaArgs {
 constexpr int kPagedMaxSplits = 16;
 constexpr int kPagedFewRows = 16;  // query slots of the few-rows form
 
+cudaError_t launch_sdpa_paged_simple(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_few(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 
@@ -36,7 +38,9 @@ struct PagedParams {
   const int32_t* kv_len;
   const int32_t* q_offsets;
   void* O;
-  int B, cols, num_pages, page_shift, kv_heads;
+  const float* k_scale;  // of a cache in 8 bits, [num_pages, kv_heads]
+  const float* v_scale;
+  int B, cols, num_pages, page_shift, kv_heads, head_tables;
   int T, H, G, max_new, causal, out_f32, splits;
   float scale_log2;  // scale * log2(e)
   float inv_G;       // 1 / G
@@ -52,8 +56,9 @@ __device__ __forceinline__ int div_by_group(const PagedParams& p, int x) {
 }
 
 inline PagedParams paged_params(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
-  return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.B, a.pages.cols,
-                     a.pages.num_pages, a.pages.page_shift, a.pages.kv_heads, a.T, a.H, a.G,
+  return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.k_scale,
+                     a.pages.v_scale, a.pages.B, a.pages.cols, a.pages.num_pages,
+                     a.pages.page_shift, a.pages.kv_heads, a.head_tables, a.T, a.H, a.G,
                      a.max_new, a.causal, a.out_f32, a.splits,
                      static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634),
                      1.f / static_cast<float>(a.G), ctl.err, ctl.limit_ns};
@@ -83,8 +88,14 @@ inline bool paged_tensor_maps(const PagedSdpaArgs& a, int d, int tokens, int til
                            CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The row of the page table that sequence b's kv head g reads.
+__device__ __forceinline__ const int32_t* table_row(const PagedParams& p, int b, int g) {
+  return p.table + (p.head_tables ? static_cast<int64_t>(b) * p.kv_heads + g : b) * p.cols;
+}
+
 // Sequence b's new tokens [q0, q0 + n) and length; bad: its length, its
-// offsets (then n = 0).
+// offsets (then n = 0).  Without offsets a sequence is one token, passed over
+// when its length is 0.
 struct PagedSeq {
   int q0, n, len;
   bool bad_len, bad_offsets;
@@ -95,14 +106,21 @@ __device__ __forceinline__ PagedSeq paged_seq_of(const PagedParams& p, int q0, i
   s.len = len;
   s.bad_offsets = q0 < 0 || q1 < q0 || q1 > p.T || q1 - q0 > p.max_new;
   s.q0 = q0;
-  s.n = s.bad_offsets ? 0 : q1 - q0;
+  s.n = s.bad_offsets || (!p.q_offsets && len == 0) ? 0 : q1 - q0;
   const int64_t cap = static_cast<int64_t>(p.cols) << p.page_shift;
   s.bad_len = s.n > 0 && (s.len < 1 || s.len > cap || (p.causal && s.len < s.n));
   return s;
 }
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
-  return paged_seq_of(p, __ldg(p.q_offsets + b), __ldg(p.q_offsets + b + 1), __ldg(p.kv_len + b));
+  const int len = __ldg(p.kv_len + b);
+  return p.q_offsets ? paged_seq_of(p, __ldg(p.q_offsets + b), __ldg(p.q_offsets + b + 1), len)
+                     : paged_seq_of(p, b, b + 1, len);
+}
+
+// Where sequence i's tokens start.
+__device__ __forceinline__ int paged_offset(const PagedParams& p, int i) {
+  return p.q_offsets ? __ldg(p.q_offsets + i) : i;
 }
 
 // The page boxes of one tile of ROWS keys, one per lane of the producer warp:
@@ -112,15 +130,17 @@ struct PageBoxes {
   int page;   // this lane's page number
   bool mine;  // this lane has a box of the tile
 
-  // Request the page number of the tile that starts at key `key0`.
-  __device__ __forceinline__ void fetch(const PagedParams& p, int b, int key0, int len, int lane) {
+  // Request the page number of the tile that starts at key `key0`, from the
+  // sequence's row of the page table.
+  __device__ __forceinline__ void fetch(const PagedParams& p, const int32_t* row, int key0, int len,
+                                        int lane) {
     const int slot = lane / KB;
     const int in_tile = ROWS >> p.page_shift;  // 0: the tile is part of a page
     const int entry = (key0 >> p.page_shift) + slot;
     mine = slot < (in_tile > 0 ? in_tile : 1) &&
            (static_cast<int64_t>(entry) << p.page_shift) < len;
     page = 0;
-    if (mine) page = __ldg(p.table + static_cast<int64_t>(b) * p.cols + entry);
+    if (mine) page = __ldg(row + entry);
   }
   __device__ __forceinline__ bool in_range(const PagedParams& p) const {
     return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);

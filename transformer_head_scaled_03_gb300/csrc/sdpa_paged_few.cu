@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
   PagedSeq seq{};
   if (sorted) {
     for (int i = threadIdx.x; i <= p.B; i += kThreads) {
-      off_s[i] = __ldg(p.q_offsets + i);
+      off_s[i] = paged_offset(p, i);
       if (i < p.B) lens_s[i] = __ldg(p.kv_len + i);
     }
   } else {
@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
         for (int kb = 0; kb < C::KB; ++kb)
           tma_load_3d(base + C::kOffQ + kb * kQBox, &tmQ, bar(C::bQ), kb * 64, g * p.G, seq.q0);
       }
+      const int32_t* row = table_row(p, b, g);
       PageBoxes<kKeys, C::KB> cur, nxt;
-      cur.fetch(p, b, t_begin * kKeys, len, lane);
+      cur.fetch(p, row, t_begin * kKeys, len, lane);
       int issued = 0;
       // the box of every lane into the ring's next slot; false: gave up
       auto load = [&](const PageBoxes<kKeys, C::KB>& boxes, const CUtensorMap* map, int key0) {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
         // the next tile's keys go before this tile's values
         const int key0 = first + j * kKeys;
         if (j + 1 < T) {
-          nxt.fetch(p, b, key0 + kKeys, len, lane);
+          nxt.fetch(p, row, key0 + kKeys, len, lane);
           if (!(ok = load(nxt, &tmK, key0 + kKeys))) break;
         }
         ok = load(cur, &tmV, key0);

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
   const bool sorted = p.B > 1 && p.B <= kMaxSorted;
   if (sorted) {
     for (int i = threadIdx.x; i <= p.B; i += C::kThreads) {
-      off_s[i] = __ldg(p.q_offsets + i);
+      off_s[i] = paged_offset(p, i);
       if (i < p.B) lens_s[i] = __ldg(p.kv_len + i);
     }
     __syncthreads();
@@ -260,8 +260,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
             tma_load_3d(base + C::kOffQ + (t * C::KB + kb) * kSub, &tmQ, bar(C::bQ), kb * 64,
                         g * p.G, seq.q0 + i0 + t * tile_tokens);
       }
+      const int32_t* row = table_row(p, b, g);
       PageBoxes<BN, C::KB> cur, nxt;
-      cur.fetch(p, b, j0 * BN, len, lane);
+      cur.fetch(p, row, j0 * BN, len, lane);
       int k_issued = 0, v_issued = 0;
       for (int j = 0; j < n_kv; ++j) {
         const int st = j % NST;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NQT, NST, BN>::kThreads,
         __syncwarp();
         cur.load(p, &tmK, base + C::kOffK + st * C::kKVTileBytes, bar(C::bKF(st)), key0, g, lane);
         k_issued = j + 1;
-        if (j + 1 < n_kv) nxt.fetch(p, b, key0 + BN, len, lane);
+        if (j + 1 < n_kv) nxt.fetch(p, row, key0 + BN, len, lane);
         if (!mbar_wait_warp(bar(C::bVE(st)), ph ^ 1u, ctl)) break;
         if (lane == 0) mbar_expect_tx(bar(C::bVF(st)), bytes);
         __syncwarp();
