@@ -177,10 +177,11 @@ mha_status attend(const void* Q, int64_t q_token_stride, const mha_kv_pages* pag
   // 856 us, where the single tokens alone take 667 and the chunk alone 229.
   // Single tokens with a loose max_new pay for it: 64 sequences of 200 to 1000
   // keys 59 us instead of 45, 16 of 16 to 32 K 279 instead of 240.
-  if (scales) return launch_sdpa_paged_simple(a, ctl) == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
-  const cudaError_t e = static_cast<int64_t>(a.max_new) * G <= kPagedFewRows
-                            ? launch_sdpa_paged_few(a, ctl)
-                            : launch_sdpa_paged_rows(a, ctl);
+  const bool few = static_cast<int64_t>(a.max_new) * G <= kPagedFewRows;
+  const cudaError_t e =
+      few ? scales ? launch_sdpa_paged_few_e4m3(a, ctl) : launch_sdpa_paged_few(a, ctl)
+      : scales ? launch_sdpa_paged_simple(a, ctl)
+               : launch_sdpa_paged_rows(a, ctl);
   return e == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 

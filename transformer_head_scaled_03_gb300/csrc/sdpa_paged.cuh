@@ -30,6 +30,7 @@ constexpr int kPagedFewRows = 16;  // query slots of the few-rows form
 
 cudaError_t launch_sdpa_paged_simple(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_few(const PagedSdpaArgs& a, const DeviceCtl& ctl);
+cudaError_t launch_sdpa_paged_few_e4m3(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 
 // Kernel arguments.
@@ -93,6 +94,23 @@ __device__ __forceinline__ const int32_t* table_row(const PagedParams& p, int b,
   return p.table + (p.head_tables ? static_cast<int64_t>(b) * p.kv_heads + g : b) * p.cols;
 }
 
+// The tensor maps of one layer's pools in 8 bits [P, Hkv * page, d], boxes of
+// `rows` whole rows that stay inside a page.
+inline bool paged_tensor_maps_e4m3(const PagedSdpaArgs& a, int d, int tile_rows, CUtensorMap* k,
+                                   CUtensorMap* v) {
+  const int page = 1 << a.pages.page_shift;
+  const uint64_t pd[3] = {static_cast<uint64_t>(d),
+                          static_cast<uint64_t>(a.pages.kv_heads) << a.pages.page_shift,
+                          static_cast<uint64_t>(a.pages.num_pages)};
+  const uint64_t pst[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(a.pages.page_stride)};
+  const uint32_t pb[3] = {static_cast<uint32_t>(d),
+                          static_cast<uint32_t>(page < tile_rows ? page : tile_rows), 1};
+  const CUtensorMapSwizzle swizzle =
+      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return encode_tensor_map(k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.K, pd, pst, pb, swizzle) &&
+         encode_tensor_map(v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages.V, pd, pst, pb, swizzle);
+}
+
 // Sequence b's new tokens [q0, q0 + n) and length; bad: its length, its
 // offsets (then n = 0).  Without offsets a sequence is one token, passed over
 // when its length is 0.
@@ -124,8 +142,9 @@ __device__ __forceinline__ int paged_offset(const PagedParams& p, int i) {
 }
 
 // The page boxes of one tile of ROWS keys, one per lane of the producer warp:
-// lane = page of the tile * KB + 64-column block.
-template <int ROWS, int KB>
+// lane = page of the tile * KB + column block of kRowBytes (64 columns in
+// bf16; in 8 bits the whole row).
+template <int ROWS, int KB, int kRowBytes = 128>
 struct PageBoxes {
   int page;   // this lane's page number
   bool mine;  // this lane has a box of the tile
@@ -151,7 +170,8 @@ struct PageBoxes {
   // Bytes that the warp's boxes bring (warp-collective).
   __device__ __forceinline__ uint32_t bytes(const PagedParams& p) const {
     const uint32_t rows = min(ROWS, 1 << p.page_shift);
-    return __popc(__ballot_sync(0xffffffffu, good(p))) * rows * 128u;
+    return __popc(__ballot_sync(0xffffffffu, good(p))) * rows *
+           static_cast<uint32_t>(kRowBytes);
   }
   // Load this lane's box of head g into the tile at `dst` ([KB][ROWS][128 B]).
   __device__ __forceinline__ void load(const PagedParams& p, const CUtensorMap* map, uint32_t dst,
@@ -159,8 +179,8 @@ struct PageBoxes {
     if (!good(p)) return;
     const int slot = lane / KB, kb = lane % KB;
     const int row = (key0 & ((1 << p.page_shift) - 1)) + (g << p.page_shift);
-    tma_load_3d(dst + kb * (ROWS * 128) + (slot << p.page_shift) * 128, map, bar, kb * 64, row,
-                page);
+    tma_load_3d(dst + kb * (ROWS * kRowBytes) + (slot << p.page_shift) * kRowBytes, map, bar,
+                kb * 64, row, page);
   }
 };
 
@@ -242,6 +262,70 @@ __device__ __forceinline__ void sum_sharers(float4& o, int sharers) {
     o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
     o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
     o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
+  }
+}
+
+// The four softmax warps of the few-rows kernels.
+__device__ __forceinline__ void softmax_bar() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// What the merge of the few-rows kernels keeps in shared memory, fp32: this
+// CTA's m and l of the 16 slots and its partial outputs [16][d], then every
+// split's m and l and the weights, [16 splits][16] each.
+constexpr int few_merge_bytes(int d) {
+  return (2 * kPagedFewRows + kPagedFewRows * d + 3 * kPagedMaxSplits * kPagedFewRows) * 4;
+}
+
+// Merge the splits through distributed shared memory (warps 0-3, after a
+// cluster barrier): every split's m and l are fetched, each thread works out
+// weights, 2^(m_s - M) / sum, then the outputs, four columns a place, each
+// another remote load.
+template <int D>
+__device__ __forceinline__ void few_merge(const PagedParams& p, const PagedSeq& seq, int g,
+                                          int split, float* xm, volatile int* bad_page) {
+  constexpr int kSlots = kPagedFewRows;
+  float* xl = xm + kSlots;
+  float* xo = xl + kSlots;
+  float* xw = xo + kSlots * D;
+  const int rows = seq.n * p.G;
+  const int S = p.splits;
+  float* lm = xw + kPagedMaxSplits * kSlots;
+  float* ll = lm + kPagedMaxSplits * kSlots;
+  const uint32_t xm_s = smem_u32(xm), xl_s = smem_u32(xl), xo_s = smem_u32(xo);
+  const bool bad = any_bad(smem_u32(const_cast<int*>(bad_page)), S);
+#pragma unroll 1
+  for (int x = threadIdx.x; x < S * kSlots; x += 128) {
+    const uint32_t q = x % kSlots, s = x / kSlots;
+    lm[x] = ld_cluster_f32(cluster_map(xm_s + 4u * q, s));
+    ll[x] = ld_cluster_f32(cluster_map(xl_s + 4u * q, s));
+  }
+  softmax_bar();
+#pragma unroll 1
+  for (int x = threadIdx.x; x < S * kSlots; x += 128)
+    xw[x] = bad ? 0.f : split_weight(lm + x % kSlots, ll + x % kSlots, kSlots, S, x / kSlots);
+  softmax_bar();
+  const int total = rows * (D / 4);
+  const int per = (total + S - 1) / S;
+  const int e0 = split * per;
+  const int e1 = min(total, e0 + per);
+  const int sharers = merge_sharers(per, S, 128);
+#pragma unroll 1
+  for (int f0 = e0; f0 < e1; f0 += 128 / sharers) {
+    const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
+    const int q = e / (D / 4);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e < e1) {
+#pragma unroll 2
+      for (int s = threadIdx.x % sharers; s < S; s += sharers)
+        add_split(o, xo_s + 16u * e, s, xw[s * kSlots + q]);
+    }
+    sum_sharers(o, sharers);
+    if (e < e1 && threadIdx.x % sharers == 0) {
+      const int i = div_by_group(p, q);
+      const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
+      store_out4(p, row * D + (e - q * (D / 4)) * 4, o);
+    }
   }
 }
 

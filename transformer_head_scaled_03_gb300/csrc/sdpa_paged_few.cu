@@ -65,7 +65,7 @@ struct FewCfg {
   // the merge's m[16], l[16], o[16][D], then every split's m and l and the
   // weights, [16 splits][16] each, in the first slot: written once every product has completed
   static constexpr int kOffX = kOffRing;
-  static constexpr int kXBytes = (2 * kSlots + kSlots * D + 3 * kPagedMaxSplits * kSlots) * 4;
+  static constexpr int kXBytes = few_merge_bytes(D);
   static_assert(kXBytes <= kTile, "the merge fits a stage");
   static constexpr int kOffBar = kOffRed + 3 * 4 * kSlots * 4;
   static constexpr int bQ = 0;
@@ -93,10 +93,6 @@ struct FewCfg {
 // Places of K(j) and V(j) in the ring's order, for T tiles.
 __device__ __forceinline__ int place_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int place_of_v(int j, int T) { return j + 1 < T ? 2 * j + 2 : 2 * j + 1; }
-
-__device__ __forceinline__ void softmax_bar() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-}
 
 // N query slots (of the products' 16) of this thread's lane in tensor memory.
 template <int N>
@@ -176,7 +172,6 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
   float* xm = reinterpret_cast<float*>(gbase + C::kOffX);
   float* xl = xm + kSlots;
   float* xo = xl + kSlots;
-  float* xw = xo + kSlots * D;
 
   // ---- this CTA's (sequence, kv head) and key tiles; the cluster spans the
   // splits.  CTAs start roughly in grid order, so sequences are taken
@@ -508,51 +503,9 @@ __global__ void __launch_bounds__(kThreads, FewCfg<D, kAlone>::kCtas)
     }
   }
 
-  // ---- merge the splits through distributed shared memory: every split's m
-  // and l are fetched, each thread works out weights, 2^(m_s - M) / sum, then
-  // the outputs, four columns a place, each another remote load
   __syncwarp();
   cluster_sync();  // every split's m, l, O and bad-page flag are in its shared memory
-  if (warp < 4) {
-    const int S = p.splits;
-    float* lm = xw + kPagedMaxSplits * kSlots;
-    float* ll = lm + kPagedMaxSplits * kSlots;
-    const uint32_t xm_s = smem_u32(xm), xl_s = smem_u32(xl), xo_s = smem_u32(xo);
-    const bool bad = any_bad(smem_u32(const_cast<int*>(bad_page)), S);
-#pragma unroll 1
-    for (int x = threadIdx.x; x < S * kSlots; x += 128) {
-      const uint32_t q = x % kSlots, s = x / kSlots;
-      lm[x] = ld_cluster_f32(cluster_map(xm_s + 4u * q, s));
-      ll[x] = ld_cluster_f32(cluster_map(xl_s + 4u * q, s));
-    }
-    softmax_bar();
-#pragma unroll 1
-    for (int x = threadIdx.x; x < S * kSlots; x += 128)
-      xw[x] = bad ? 0.f : split_weight(lm + x % kSlots, ll + x % kSlots, kSlots, S, x / kSlots);
-    softmax_bar();
-    const int total = rows * (D / 4);
-    const int per = (total + S - 1) / S;
-    const int e0 = split * per;
-    const int e1 = min(total, e0 + per);
-    const int sharers = merge_sharers(per, S, 128);
-#pragma unroll 1
-    for (int f0 = e0; f0 < e1; f0 += 128 / sharers) {
-      const int e = f0 + static_cast<int>(threadIdx.x) / sharers;
-      const int q = e / (D / 4);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e < e1) {
-#pragma unroll 2
-        for (int s = threadIdx.x % sharers; s < S; s += sharers)
-          add_split(o, xo_s + 16u * e, s, xw[s * kSlots + q]);
-      }
-      sum_sharers(o, sharers);
-      if (e < e1 && threadIdx.x % sharers == 0) {
-        const int i = div_by_group(p, q);
-        const int64_t row = static_cast<int64_t>(seq.q0 + i) * p.H + g * p.G + (q - i * p.G);
-        store_out4(p, row * D + (e - q * (D / 4)) * 4, o);
-      }
-    }
-  }
+  if (warp < 4) few_merge<D>(p, seq, g, split, xm, bad_page);
   __syncwarp();
   cluster_sync();  // no CTA leaves while another still reads its shared memory
   if (warp == kMmaWarp) {
