@@ -23,7 +23,7 @@ SOURCES = ["mha_api.cu", "sdpa_bf16.cu", "gemm_bf16.cu", "gemm_ln_bf16.cu", "fp3
            "layernorm.cu", "encoder_api.cu", "sdpa_decode.cu",
            "embed_pe.cu", "sdpa_backward.cu", "host_pipeline.cu",
            "sdpa_paged.cu", "sdpa_paged_few.cu", "sdpa_paged_rows.cu",
-           "sdpa_paged_few_e4m3.cu", "sdpa_paged_simple.cu", "qk_norm_rope.cu", "kv_pages.cu", "kv_select.cu"]
+           "sdpa_paged_few_e4m3.cu", "sdpa_paged_rows_e4m3.cu", "qk_norm_rope.cu", "kv_pages.cu", "kv_select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

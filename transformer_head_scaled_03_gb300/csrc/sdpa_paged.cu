@@ -180,7 +180,7 @@ mha_status attend(const void* Q, int64_t q_token_stride, const mha_kv_pages* pag
   const bool few = static_cast<int64_t>(a.max_new) * G <= kPagedFewRows;
   const cudaError_t e =
       few ? scales ? launch_sdpa_paged_few_e4m3(a, ctl) : launch_sdpa_paged_few(a, ctl)
-      : scales ? launch_sdpa_paged_simple(a, ctl)
+      : scales ? launch_sdpa_paged_rows_e4m3(a, ctl)
                : launch_sdpa_paged_rows(a, ctl);
   return e == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }

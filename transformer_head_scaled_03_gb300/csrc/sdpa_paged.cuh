@@ -28,9 +28,9 @@ struct PagedSdpaArgs {
 constexpr int kPagedMaxSplits = 16;
 constexpr int kPagedFewRows = 16;  // query slots of the few-rows form
 
-cudaError_t launch_sdpa_paged_simple(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_few(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_few_e4m3(const PagedSdpaArgs& a, const DeviceCtl& ctl);
+cudaError_t launch_sdpa_paged_rows_e4m3(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 cudaError_t launch_sdpa_paged_rows(const PagedSdpaArgs& a, const DeviceCtl& ctl);
 
 // Kernel arguments.
