@@ -91,13 +91,7 @@ __device__ __forceinline__ int place_of_v(int j, int T) { return j + 1 < T ? 2 *
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 8) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(taddr)
-        : "memory");
+    tmem_ld8_sync(taddr, r);
   } else if constexpr (N == 16) {
     tmem_ld16_sync(taddr, r);
   } else {

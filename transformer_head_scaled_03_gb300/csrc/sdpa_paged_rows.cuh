@@ -181,7 +181,8 @@ __device__ __forceinline__ void rows_store(const PagedParams& p, uint32_t tO, bo
 // their m and l from all splits, works out the weights, and sums up the outputs
 // four columns at a time.  Between cluster barriers; xo_s, xm_s: shared
 // addresses of the partial outputs [NQT * 128][D + 4] and of m and l of every
-// row; w_at: three times kShare floats.
+// row; w_at: three times kShare floats.  The block's first kThreads threads
+// (whole warps) call this.
 template <int D, int NQT, int kThreads>
 __device__ __forceinline__ void rows_merge(const PagedParams& p, const PagedSeq& seq, int g, int i0,
                                            int split, int tile_tokens, uint32_t xo_s,
@@ -206,13 +207,13 @@ __device__ __forceinline__ void rows_merge(const PagedParams& p, const PagedSeq&
     lm[x] = ld_cluster_f32(cluster_map(xm_s + 4u * row, s));
     ll[x] = ld_cluster_f32(cluster_map(xm_s + 4u * (NQT * kRowsM + row), s));
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 #pragma unroll 1
   for (int x = threadIdx.x; x < mine * S; x += kThreads) {
     const int k = x / S;
     weights[x] = bad ? 0.f : split_weight(lm + k * S, ll + k * S, 1, S, x - k * S);
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   const int total = mine * (D / 4);
   // place e of this CTA's share: its shared address, its output element
   auto place_from = [&](int row, int c) {
