@@ -967,16 +967,88 @@ __device__ __forceinline__ void append_e4m3_unit(const PagedArgs& p, int64_t uni
   if (warp == 0 && lane == 0) *scale = s;
 }
 
+// Where packed token t lies: its position; -1: no sequence's, or offsets that
+// are bad; -2: another bad entry (both reported).  Warp-collective.
+__device__ __forceinline__ int position_of_token(const PagedArgs& p, int t) {
+  const PagesView& pg = p.pages;
+  const int b = sequence_of_token(p.q_offsets, pg.B, t);
+  if (b >= pg.B) return -1;
+  const int q0 = __ldg(p.q_offsets + b), q1 = __ldg(p.q_offsets + b + 1);
+  const int len = __ldg(pg.kv_len + b);
+  if (q0 < 0 || q1 < q0 || q1 > p.T || t >= q1 || (b > 0 && t < q0)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrPages);
+    return -1;
+  }
+  if (t < q0) return -1;
+  const int n = q1 - q0, pos = len - n + (t - q0);
+  int page = -1;
+  if (len >= n && len <= (static_cast<int64_t>(pg.cols) << pg.page_shift))
+    page = __ldg(pg.table + static_cast<int64_t>(b) * pg.cols + (pos >> pg.page_shift));
+  if (page >= 0 && page < pg.num_pages && pos < p.pe_rows) return pos;
+  if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrPages);
+  return -2;
+}
+
+// The queries of many tokens: a warp takes one token's heads, so its position,
+// sines and cosines are looked up once, and has kAhead rounds of rows under way.
+template <int D, int HALF>
+__device__ __forceinline__ void norm_rope_queries(const PagedArgs& p, int t) {
+  using V = VecLane<D>;
+  constexpr int kAhead = 2;
+  if (t >= p.T) return;
+  const int pos = position_of_token(p, t);
+  if (pos == -1) return;
+  const V at(p.r);
+  const int h0 = (threadIdx.x & 31) / V::kLanes;
+  const __nv_bfloat16* x = p.q + t * p.qs;
+  __nv_bfloat16* y = p.qo + static_cast<int64_t>(t) * p.H * D;
+  Turns turns;
+  turns.load(p.pe + static_cast<int64_t>(max(pos, 0)) * p.r, at.a, at.b, at.turns && pos >= 0,
+             HALF);
+  for (int h1 = 0; h1 < p.H; h1 += kAhead * V::kRows) {
+    Raw8<__nv_bfloat16> ra[kAhead], rb[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = h1 + k * V::kRows + h0;
+      ra[k].zero();
+      rb[k].zero();
+      if (h < p.H && pos >= 0) {
+        ra[k].load(x + static_cast<int64_t>(h) * D + at.a);
+        rb[k].load(x + static_cast<int64_t>(h) * D + at.b);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = h1 + k * V::kRows + h0;
+      if (h1 + k * V::kRows >= p.H) break;
+      float2 a[4], b[4];
+      ra[k].get(a);
+      rb[k].get(b);
+      norm_rope_vec<D, HALF>(a, b, p.gq, at, turns, p.eps);
+      if (h >= p.H) continue;
+      if (pos < 0) {  // gamma may be infinite
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = b[i] = make_float2(0.f, 0.f);
+      }
+      store8(y + static_cast<int64_t>(h) * D + at.a, a);
+      store8(y + static_cast<int64_t>(h) * D + at.b, b);
+    }
+  }
+}
+
 // The first `page_blocks` blocks take the touched pages, a unit each (NW = 8)
-// or one to a warp (NW = 1: few rows to a page); the others the queries.
+// or one to a warp (NW = 1: few rows to a page); the others the queries, a
+// token to a warp (parts = 0) or as norm_rope_paged_rows does.
 template <int D, int HALF, int NW>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, NW == 1 ? 2 : 3)
     norm_rope_paged_e4m3_kernel(const PagedArgs p, int page_blocks, int block_tokens, int parts) {
   __shared__ float tops[kWarps];
   const int block = static_cast<int>(blockIdx.x);
   if (block < page_blocks) {
     append_e4m3_unit<D, HALF, NW>(
         p, NW == 1 ? static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5) : block, tops);
+  } else if (parts == 0) {
+    norm_rope_queries<D, HALF>(p, (block - page_blocks) * kWarps + (threadIdx.x >> 5));
   } else {
     const int q = block - page_blocks;
     norm_rope_paged_rows<D, HALF, false>(p, q / parts, q % parts, parts, block_tokens);
@@ -1074,11 +1146,15 @@ cudaError_t launch_append_e4m3(const PagedArgs& p, int d, int block_tokens, cuda
   // a warp to a unit while its rows are at most four on average
   const bool few = p.T <= 4 * seqs;
   const int64_t page_blocks = few ? (units + kWarps - 1) / kWarps : units;
-  const int token_blocks = (p.T + block_tokens - 1) / block_tokens;
-  const int rounds = (block_tokens * p.H + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
-  const int room = 2 * num_sms() / token_blocks;
-  const int parts = room < 1 ? 1 : room < rounds ? room : rounds;
-  const int64_t blocks = page_blocks + static_cast<int64_t>(token_blocks) * parts;
+  // queries: a warp to a token as soon as that is eight warps to an SM
+  int token_blocks = (p.T + kWarps - 1) / kWarps, parts = 0;
+  if (p.T < 8 * num_sms()) {
+    token_blocks = (p.T + block_tokens - 1) / block_tokens;
+    const int rounds = (block_tokens * p.H + kWarps * (512 / d) - 1) / (kWarps * (512 / d));
+    const int room = 2 * num_sms() / token_blocks;
+    parts = room < 1 ? 1 : room < rounds ? room : rounds;
+  }
+  const int64_t blocks = page_blocks + static_cast<int64_t>(token_blocks) * (parts ? parts : 1);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
   auto go = [&](auto kern) {
