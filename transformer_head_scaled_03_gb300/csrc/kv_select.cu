@@ -117,12 +117,15 @@ struct Extremes<false> {
   }
 };
 
+// Codes as the high bytes of bf16 numbers, whose order is theirs (no code's bits
+// there are an infinity or a NaN): two to an instruction, where decoding them
+// first would wait for the conversion unit.
 template <>
 struct Extremes<true> {
-  __half2 lo[8], hi[8];
-  static __device__ __forceinline__ __half2 two(unsigned u, int i) {
-    return __half2(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>(i ? u >> 16 : u & 0xffffu), __NV_E4M3));
+  __nv_bfloat162 lo[8], hi[8];
+  static __device__ __forceinline__ __nv_bfloat162 two(unsigned w, int odd) {
+    const unsigned x = odd ? w & 0xff00ff00u : w << 8 & 0xff00ff00u;
+    return *reinterpret_cast<const __nv_bfloat162*>(&x);
   }
   __device__ __forceinline__ void set(uint4 u) {
     const unsigned w[4] = {u.x, u.y, u.z, u.w};
@@ -133,7 +136,7 @@ struct Extremes<true> {
     const unsigned w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const __half2 v = two(w[i / 2], i & 1);
+      const __nv_bfloat162 v = two(w[i / 2], i & 1);
       lo[i] = __hmin2(lo[i], v), hi[i] = __hmax2(hi[i], v);
     }
   }
@@ -145,12 +148,20 @@ struct Extremes<true> {
     }
   }
   static constexpr int kCols = 16;
+  // (even columns' codes lie in element 2 k of a word, odd ones' in 2 k + 1)
   __device__ __forceinline__ void get(float (&l)[16], float (&h)[16]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 a = __half22float2(lo[i]), b = __half22float2(hi[i]);
-      l[2 * i] = a.x, l[2 * i + 1] = a.y, h[2 * i] = b.x, h[2 * i + 1] = b.y;
+      const int c = 4 * (i / 2) + (i & 1);
+      decode(lo[i], l[c], l[c + 2]);
+      decode(hi[i], h[c], h[c + 2]);
     }
+  }
+  static __device__ __forceinline__ void decode(__nv_bfloat162 v, float& a, float& b) {
+    const unsigned x = *reinterpret_cast<const unsigned*>(&v);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((x >> 8 & 0xffu) | (x >> 16 & 0xff00u)), __NV_E4M3)));
+    a = f.x, b = f.y;
   }
 };
 
@@ -252,8 +263,9 @@ __device__ __forceinline__ TokenPlace place_of(const SelectArgs& a, int t) {
   return w;
 }
 
-constexpr int kScoreWarps = 8;
-constexpr int kHeadsAtOnce = 8;  // query heads in shared memory at a time
+constexpr int kScoreWarps = 4;
+constexpr int kRun = 32;          // pages of a warp: one look-up of their numbers
+constexpr int kHeadsAtOnce = 16;  // query heads in shared memory at a time
 // the score that marks a bad page number (a NaN no product gives)
 constexpr unsigned kBadScore = 0x7fffffffu;
 
@@ -264,30 +276,43 @@ __device__ __forceinline__ int dot16(uint4 q, uint4 x, int s) {
   return __dp4a(static_cast<int>(q.w), static_cast<int>(x.w), s);
 }
 
-// The scores of a stretch of one (token, kv head)'s pages: D / 16 lanes to a
-// page, 16 columns of lo and hi to a lane.
+// The scores of one (token, kv head)'s pages, a run of kRun neighbouring ones to
+// a warp: D / 16 lanes to a page, 16 columns of lo and hi to a lane, kAhead
+// rounds of pages under way.  Four heads' sums are spread over the lanes while
+// they are summed up, half as many exchanges as one by one.
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps)
-    kv_score_kernel(const SelectArgs a, int pages_per_block) {
+    kv_score_kernel(const SelectArgs a, int chunks) {
   constexpr int L = D / 16;       // lanes per page
-  constexpr int kPages = 32 / L;  // pages per warp
+  constexpr int kPages = 32 / L;  // pages per warp and round
+  constexpr int kAhead = 4;
+  static_assert(kRun % (kPages * kAhead) == 0, "whole rounds");
   __shared__ uint4 q_pos[kHeadsAtOnce][L], q_neg[kHeadsAtOnce][L];
   __shared__ float q_step[kHeadsAtOnce];
   const PagesView& pg = a.pages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunks = (pg.cols + pages_per_block - 1) / pages_per_block;
   const int item = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
   const int chunk = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks));
   const int t = item / pg.kv_heads, g = item % pg.kv_heads;
   pdl_launch_dependents();
   const TokenPlace w = place_of(a, t);
   const int newest = w.pos >> pg.page_shift;  // full pages that the token sees
-  const int c0 = chunk * pages_per_block;
+  const int b0 = chunk * kScoreWarps * kRun;
   // without a choice to make, or pages of this stretch, there is nothing to score
-  if (w.state < 1 || newest < a.n_select || c0 >= newest) return;
-  const int c1 = min(newest, c0 + pages_per_block);
-  const int32_t* row = pg.table + static_cast<int64_t>(w.b) * pg.cols;
-  float* scores = a.scores + (static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols;
+  if (w.state < 1 || newest < a.n_select || b0 >= newest) return;
+  const int c0 = b0 + warp * kRun;
+  int pages = -1;
+  if (c0 + lane < newest) pages = __ldg(pg.table + static_cast<int64_t>(w.b) * pg.cols + c0 + lane);
+  const bool good = pages >= 0 && pages < pg.num_pages;
+  const int64_t at0 = static_cast<int64_t>(good ? pages : 0) * pg.kv_heads + g;
+  float scale = 0.f;
+  if (good) scale = __ldg(a.bound_scale + at0);
+  const int part = lane % L;
+  // this lane's heads of four, after the sums
+  const int mine = (lane & L / 2 ? 2 : 0) + (lane & L / 4 ? 1 : 0);
+  float best[kRun / kPages];
+#pragma unroll
+  for (int i = 0; i < kRun / kPages; ++i) best[i] = -INFINITY;
   for (int h0 = 0; h0 < a.G; h0 += kHeadsAtOnce) {
     const int heads = min(kHeadsAtOnce, a.G - h0);
     if (h0) __syncthreads();
@@ -317,40 +342,65 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
       if (lane == 0) q_step[h] = step;
     }
     __syncthreads();
-    const int part = lane % L;
-    for (int c = c0 + warp * kPages; c < c1; c += kScoreWarps * kPages) {
-      const int mine = c + lane / L;
-      int page = -1;
-      if (mine < c1) page = __ldg(row + mine);
-      const bool good = page >= 0 && page < pg.num_pages;
-      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-      float scale = 0.f;
-      if (good) {
-        const int64_t at = static_cast<int64_t>(page) * pg.kv_heads + g;
-        const uint4* from = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + part;
-        lo = __ldg(from);
-        hi = __ldg(from + L);
-        scale = __ldg(a.bound_scale + at);
-      }
-      float best = -INFINITY;
-      for (int h = 0; h < heads; ++h) {
-        int s = dot16(q_neg[h][part], lo, dot16(q_pos[h][part], hi, 0));
 #pragma unroll
-        for (int k = 1; k < L; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        best = fmaxf(best, static_cast<float>(s) * q_step[h]);
+    for (int i0 = 0; i0 < kRun / kPages; i0 += kAhead) {
+      if (c0 + i0 * kPages >= newest) break;
+      uint4 lo[kAhead], hi[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        // a page behind the last, or a bad one, reads page 0's: nothing comes of it
+        const int64_t at = __shfl_sync(0xffffffffu, at0, (i0 + i) * kPages + lane / L);
+        const uint4* from = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + part;
+        lo[i] = __ldg(from);
+        hi[i] = __ldg(from + L);
       }
-      // + 0: a product that underflows has no sign
-      float score = best * scale + 0.f;
-      if (h0 && mine < c1 && part == 0) score = fmaxf(score, scores[mine]);
-      if (mine < c1 && part == 0) scores[mine] = good ? score : __uint_as_float(kBadScore);
+      for (int h = 0; h < heads; h += 4) {
+        int s[kAhead][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // heads behind the last are the last once more
+          const int hk = min(h + k, heads - 1);
+          const uint4 qp = q_pos[hk][part], qn = q_neg[hk][part];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) s[i][k] = dot16(qn, lo[i], dot16(qp, hi[i], 0));
+        }
+        const float step = q_step[min(h + mine, heads - 1)];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const bool upper = lane & L / 2, second = lane & L / 4;
+          int a0 = upper ? s[i][2] : s[i][0], a1 = upper ? s[i][3] : s[i][1];
+          a0 += __shfl_xor_sync(0xffffffffu, upper ? s[i][0] : s[i][2], L / 2);
+          a1 += __shfl_xor_sync(0xffffffffu, upper ? s[i][1] : s[i][3], L / 2);
+          int sum = (second ? a1 : a0) + __shfl_xor_sync(0xffffffffu, second ? a0 : a1, L / 4);
+#pragma unroll
+          for (int k = L / 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+          best[i0 + i] = fmaxf(best[i0 + i], static_cast<float>(sum) * step);
+        }
+      }
     }
   }
+  // page l of the run to lane l, coalesced
+  float score = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRun / kPages; ++i) {
+    float x = best[i];
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, L / 2));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, L / 4));
+    const float v = __shfl_sync(0xffffffffu, x, lane % kPages * L);
+    if (lane / kPages == i) score = v;
+  }
+  // + 0: a product that underflows has no sign
+  score = score * scale + 0.f;
+  if (c0 + lane < newest)
+    a.scores[(static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols + c0 + lane] =
+        good ? score : __uint_as_float(kBadScore);
 }
 
 // --------------------------------------------------------------------- choice
 
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickKeys = 8192;  // that stay in shared memory; those behind are read again
 
 // fp32 in the order of unsigned whole numbers; a NaN, which finite bounds and
 // scales never give, below all others.
@@ -361,10 +411,14 @@ __device__ __forceinline__ unsigned rank_key(float x) {
 }
 
 // One block per (token, kv head): the n_select - 1 largest scores by a search
-// for the smallest of them, eight bits at a time, then the pages in order.
+// for the smallest of them, eight bits at a time from the highest one in which
+// any two differ (scores share their exponent's first bits, and one bin's
+// counter would serialise them), then the pages in order.
 __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs a) {
+  __shared__ unsigned keys[kPickKeys];
   __shared__ int bins[256];
-  __shared__ int counts[2][kPickWarps + 1];
+  __shared__ int counts[2][kPickWarps];
+  __shared__ unsigned least[kPickWarps], most[kPickWarps];
   __shared__ int found[2];
   const PagesView& pg = a.pages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -376,6 +430,7 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
   const float* scores = a.scores + (static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols;
   int picked = 0;
   bool bad = w.state < 0;
+  for (int i = threadIdx.x; i < 256; i += kPickThreads) bins[i] = 0;
   pdl_wait();
   if (w.state == 1 && newest < a.n_select) {
     // every page there is
@@ -390,30 +445,53 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
   } else if (w.state == 1) {
     const int want = a.n_select - 1;
     bool wrong = false;
-    for (int c = threadIdx.x; c < newest; c += kPickThreads)
-      wrong = wrong || __float_as_uint(scores[c]) == kBadScore;
+    unsigned lo = 0xffffffffu, hi = 0u;
+    for (int c = threadIdx.x; c < newest; c += kPickThreads) {
+      const float x = scores[c];
+      const unsigned key = rank_key(x);
+      wrong = wrong || __float_as_uint(x) == kBadScore;
+      if (c < kPickKeys) keys[c] = key;
+      lo = min(lo, key);
+      hi = max(hi, key);
+    }
+    auto key_of = [&](int c) { return c < kPickKeys ? keys[c] : rank_key(scores[c]); };
     if (threadIdx.x == 0) {
       const int page = __ldg(row + newest);
       wrong = wrong || page < 0 || page >= pg.num_pages;
     }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      least[warp] = lo;
+      most[warp] = hi;
+    }
     bad = __syncthreads_or(wrong);
-    // the want-th largest key, and how many of the equal ones are in
-    unsigned prefix = 0;
+#pragma unroll
+    for (int i = 0; i < kPickWarps; ++i) {
+      lo = min(lo, least[i]);
+      hi = max(hi, most[i]);
+    }
+    // the want-th largest key, and how many of the equal ones are in.  Above
+    // bit `top` all keys agree.
+    int top = lo == hi ? 0 : 32 - __clz(lo ^ hi);
+    unsigned prefix = top == 32 ? 0u : hi >> top << top;
     int left = want;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kPickThreads) bins[i] = 0;
-      __syncthreads();
+    while (top > 0 && want > 0) {
+      const int shift = max(top - 8, 0);
       for (int c = threadIdx.x; c < newest; c += kPickThreads) {
-        const unsigned key = rank_key(scores[c]);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&bins[(key >> shift) & 255], 1);
+        const unsigned key = key_of(c);
+        if (top == 32 || key >> top == prefix >> top)
+          atomicAdd(&bins[(key >> shift) & (0xffu >> (8 - (top - shift)))], 1);
       }
       __syncthreads();
       if (warp == 0) {
         // lane l: bins 255 - 8 l and the seven below
         int mine[8], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += mine[i] = bins[255 - 8 * lane - i];
+        for (int i = 0; i < 8; ++i) {
+          sum += mine[i] = bins[255 - 8 * lane - i];
+          bins[255 - 8 * lane - i] = 0;
+        }
         int incl = sum;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
@@ -435,6 +513,7 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
       __syncthreads();
       prefix |= static_cast<unsigned>(found[0]) << shift;
       left = found[1];
+      top = shift;
     }
     // a warp takes a stretch of neighbouring columns: first its number of
     // larger and of equal keys, then the places
@@ -442,7 +521,7 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
     const int s0 = warp * stretch, s1 = min(newest, s0 + stretch);
     int above = 0, equal = 0;
     for (int c = s0 + lane; c - lane < s1; c += 32) {
-      const unsigned key = c < s1 ? rank_key(scores[c]) : 0u;
+      const unsigned key = c < s1 ? key_of(c) : 0u;
       above += __popc(__ballot_sync(0xffffffffu, c < s1 && want > 0 && key > prefix));
       equal += __popc(__ballot_sync(0xffffffffu, c < s1 && want > 0 && key == prefix));
     }
@@ -457,7 +536,7 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
       e0 += counts[1][i];
     }
     for (int c = s0 + lane; c - lane < s1; c += 32) {
-      const unsigned key = c < s1 ? rank_key(scores[c]) : 0u;
+      const unsigned key = c < s1 ? key_of(c) : 0u;
       const bool is_above = c < s1 && want > 0 && key > prefix;
       const bool is_equal = c < s1 && want > 0 && key == prefix;
       const unsigned ma = __ballot_sync(0xffffffffu, is_above);
@@ -566,14 +645,14 @@ mha_status kv_pages_select(const void* Q, int64_t q_token_stride, const mha_kv_p
                      q_offsets, bounds + at * 2 * d, bound_scale + at, T, H, G, n_select, selected,
                      lengths, static_cast<float*>(workspace), ctl.err};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int step = 256;
-  const int64_t blocks = items * ((pages->table_cols + step - 1) / step);
+  const int chunks = (pages->table_cols + kScoreWarps * kRun - 1) / (kScoreWarps * kRun);
+  const int64_t blocks = items * chunks;
   if (blocks > 0x7fffffffLL) return MHA_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>(blocks);
   if (d == 64)
-    kv_score_kernel<64><<<grid, 32 * kScoreWarps, 0, s>>>(a, step);
+    kv_score_kernel<64><<<grid, 32 * kScoreWarps, 0, s>>>(a, chunks);
   else
-    kv_score_kernel<128><<<grid, 32 * kScoreWarps, 0, s>>>(a, step);
+    kv_score_kernel<128><<<grid, 32 * kScoreWarps, 0, s>>>(a, chunks);
   if (cudaGetLastError() != cudaSuccess) return MHA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items));

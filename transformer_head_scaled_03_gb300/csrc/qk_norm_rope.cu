@@ -1036,14 +1036,21 @@ __device__ __forceinline__ void norm_rope_queries(const PagedArgs& p, int t) {
   }
 }
 
-// The first `page_blocks` blocks take the touched pages, a unit each (NW = 8)
-// or one to a warp (NW = 1: few rows to a page); the others the queries, a
-// token to a warp (parts = 0) or as norm_rope_paged_rows does.
+// page_blocks blocks take the touched pages, a unit each (NW = 8) or one to a
+// warp (NW = 1: few rows to a page); the others the queries, a token to a warp
+// (parts = 0) or as norm_rope_paged_rows does.  The two alternate while there
+// are both: a unit waits for its look-ups and its maximum under the queries'
+// stream (44 us instead of 50 with the pages first).
 template <int D, int HALF, int NW>
 __global__ void __launch_bounds__(32 * kWarps, NW == 1 ? 2 : 3)
     norm_rope_paged_e4m3_kernel(const PagedArgs p, int page_blocks, int block_tokens, int parts) {
   __shared__ float tops[kWarps];
-  const int block = static_cast<int>(blockIdx.x);
+  int block = static_cast<int>(blockIdx.x);
+  const int pairs = min(page_blocks, static_cast<int>(gridDim.x) - page_blocks);
+  if (block < 2 * pairs)
+    block = block / 2 + (block & 1 ? page_blocks : 0);
+  else if (block - pairs < page_blocks)
+    block -= pairs;
   if (block < page_blocks) {
     append_e4m3_unit<D, HALF, NW>(
         p, NW == 1 ? static_cast<int64_t>(block) * kWarps + (threadIdx.x >> 5) : block, tops);
