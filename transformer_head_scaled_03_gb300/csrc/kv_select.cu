@@ -44,13 +44,12 @@ struct BoundsArgs {
 
 constexpr int kBoundWarps = 8;
 
-// Which full page unit u is: pages are numbered sequence by sequence, a warp
-// summing up 32 sequences at a time.  False behind the last.
-__device__ __forceinline__ bool full_page_of(const BoundsArgs& a, int64_t u, bool report, int* b_out,
+// Which full page `rest` of them is: pages are numbered sequence by sequence, a
+// warp summing up 32 sequences at a time.  False behind the last.
+__device__ __forceinline__ bool full_page_of(const BoundsArgs& a, int rest, bool report, int* b_out,
                                              int* col) {
   const int lane = threadIdx.x & 31;
   const PagesView& pg = a.pages;
-  int64_t rest = u;
   for (int b0 = 0; b0 < pg.B; b0 += 32) {
     const int b = b0 + lane;
     int first = 0, count = 0;
@@ -65,117 +64,83 @@ __device__ __forceinline__ bool full_page_of(const BoundsArgs& a, int64_t u, boo
         count = (len >> pg.page_shift) - first;
       }
     }
-    int64_t incl = count;
+    // at most 32 sequences of 2^26 pages
+    unsigned incl = static_cast<unsigned>(count);
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, incl, s);
+      const unsigned up = __shfl_up_sync(0xffffffffu, incl, s);
       if (lane >= s) incl += up;
     }
-    const unsigned in = __ballot_sync(0xffffffffu, rest < incl);
-    if (in) {
+    const unsigned in = __ballot_sync(0xffffffffu, static_cast<unsigned>(rest) < incl);
+    if (in && !report) {
       const int src = __ffs(in) - 1;
       *b_out = b0 + src;
-      *col = static_cast<int>(__shfl_sync(0xffffffffu, rest - (incl - count) + first, src));
+      *col = __shfl_sync(0xffffffffu, rest - static_cast<int>(incl) + count + first, src);
       return true;
     }
-    rest -= __shfl_sync(0xffffffffu, incl, 31);
+    rest -= static_cast<int>(__shfl_sync(0xffffffffu, incl, 31));
+    if (rest < 0) rest = 0;  // of a report
   }
   return false;
 }
 
-// 16 bytes of keys as minima and maxima.
+// 16 bytes of keys as numbers in bf16, two to a register: bf16 as it is; codes as
+// the high bytes of bf16 numbers, whose order is theirs (no code's bits there
+// are an infinity or a NaN), where decoding them first would wait for the
+// conversion unit.
 template <bool E8>
-struct Extremes;
-
-template <>
-struct Extremes<false> {
-  __nv_bfloat162 lo[4], hi[4];
-  __device__ __forceinline__ void set(uint4 u) {
-    const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = hi[i] = v[i];
-  }
-  __device__ __forceinline__ void add(uint4 u) {
-    const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = __hmin2(lo[i], v[i]), hi[i] = __hmax2(hi[i], v[i]);
-  }
-  __device__ __forceinline__ void exchange(int mask) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo[i] = __hmin2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], mask));
-      hi[i] = __hmax2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], mask));
-    }
-  }
-  static constexpr int kCols = 8;
-  __device__ __forceinline__ void get(float (&l)[8], float (&h)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = __bfloat1622float2(lo[i]), b = __bfloat1622float2(hi[i]);
-      l[2 * i] = a.x, l[2 * i + 1] = a.y, h[2 * i] = b.x, h[2 * i + 1] = b.y;
-    }
-  }
-};
-
-// Codes as the high bytes of bf16 numbers, whose order is theirs (no code's bits
-// there are an infinity or a NaN): two to an instruction, where decoding them
-// first would wait for the conversion unit.
-template <>
-struct Extremes<true> {
-  __nv_bfloat162 lo[8], hi[8];
-  static __device__ __forceinline__ __nv_bfloat162 two(unsigned w, int odd) {
-    const unsigned x = odd ? w & 0xff00ff00u : w << 8 & 0xff00ff00u;
+struct Keys16 {
+  static constexpr int kRegs = E8 ? 8 : 4;
+  static __device__ __forceinline__ __nv_bfloat162 at(const uint4& u, int i) {
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+    const unsigned x = !E8 ? w[i & 3] : i & 1 ? w[i / 2] & 0xff00ff00u : w[i / 2] << 8 & 0xff00ff00u;
     return *reinterpret_cast<const __nv_bfloat162*>(&x);
   }
-  __device__ __forceinline__ void set(uint4 u) {
-    const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = hi[i] = two(w[i / 2], i & 1);
-  }
-  __device__ __forceinline__ void add(uint4 u) {
-    const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 v = two(w[i / 2], i & 1);
-      lo[i] = __hmin2(lo[i], v), hi[i] = __hmax2(hi[i], v);
-    }
-  }
-  __device__ __forceinline__ void exchange(int mask) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = __hmin2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], mask));
-      hi[i] = __hmax2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], mask));
-    }
-  }
-  static constexpr int kCols = 16;
-  // (even columns' codes lie in element 2 k of a word, odd ones' in 2 k + 1)
-  __device__ __forceinline__ void get(float (&l)[16], float (&h)[16]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = 4 * (i / 2) + (i & 1);
-      decode(lo[i], l[c], l[c + 2]);
-      decode(hi[i], h[c], h[c + 2]);
-    }
-  }
-  static __device__ __forceinline__ void decode(__nv_bfloat162 v, float& a, float& b) {
+  // The first column of register i; the other is the next, of codes the one
+  // after that.
+  static __device__ __forceinline__ int column(int i) { return E8 ? 4 * (i / 2) + (i & 1) : 2 * i; }
+  static __device__ __forceinline__ float2 values(__nv_bfloat162 v) {
+    if constexpr (!E8) return __bfloat1622float2(v);
     const unsigned x = *reinterpret_cast<const unsigned*>(&v);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>((x >> 8 & 0xffu) | (x >> 16 & 0xff00u)), __NV_E4M3)));
-    a = f.x, b = f.y;
   }
 };
 
-// A warp per (full page, kv head): the page's rows of a head lie one behind
-// the other, so a lane's 16 bytes keep their columns from load to load.
+// N registers of minima and maxima down to `R`, over the lanes that hold other
+// rows of the same columns: each exchange halves the registers of a lane.  at0
+// becomes the place of those that are left.
+template <int N, int R>
+__device__ __forceinline__ void reduce_rows(__nv_bfloat162 (&lo)[N], __nv_bfloat162 (&hi)[N],
+                                            int& at0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = N / 2, mask = 16; n >= R; n /= 2, mask /= 2) {
+    const bool upper = lane & mask;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (i >= n) break;
+      const __nv_bfloat162 gl = upper ? lo[i] : lo[n + i], gh = upper ? hi[i] : hi[n + i];
+      const __nv_bfloat162 kl = upper ? lo[n + i] : lo[i], kh = upper ? hi[n + i] : hi[i];
+      lo[i] = __hmin2(kl, __shfl_xor_sync(0xffffffffu, gl, mask));
+      hi[i] = __hmax2(kh, __shfl_xor_sync(0xffffffffu, gh, mask));
+    }
+    at0 += upper ? n : 0;
+  }
+}
+
+// A warp per (full page, kv head): the page's rows of a head lie one behind the
+// other, so a lane's 16 bytes keep their columns from load to load.
 template <int D, bool E8>
 __global__ void __launch_bounds__(32 * kBoundWarps) kv_bounds_kernel(const BoundsArgs a) {
+  using K = Keys16<E8>;
   const PagesView& pg = a.pages;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kBoundWarps + (threadIdx.x >> 5);
+  const unsigned unit = blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
   int b = 0, col = 0;
   // the first warp of all looks at every sequence for its report
-  if (unit == 0) full_page_of(a, int64_t{1} << 40, true, &b, &col);
-  if (!full_page_of(a, unit / pg.kv_heads, false, &b, &col)) return;
+  if (unit == 0) full_page_of(a, 0, true, &b, &col);
+  if (!full_page_of(a, static_cast<int>(unit / pg.kv_heads), false, &b, &col)) return;
   const int g = static_cast<int>(unit % pg.kv_heads);
   const int page = __ldg(pg.table + static_cast<int64_t>(b) * pg.cols + col);
   if (page < 0 || page >= pg.num_pages) {
@@ -183,47 +148,57 @@ __global__ void __launch_bounds__(32 * kBoundWarps) kv_bounds_kernel(const Bound
     return;
   }
   constexpr int kEs = E8 ? 1 : 2;
-  constexpr int kRowVecs = D * kEs / 16;  // lanes to a row
+  constexpr int kRowVecs = D * kEs / 16;        // lanes to a row
+  constexpr int kRegs = K::kRegs;
+  constexpr int kLeft = kRegs * kRowVecs / 32;  // registers of a lane in the end
+  static_assert(kLeft == 1 || kLeft == 2, "a lane's columns");
   const uint4* from = reinterpret_cast<const uint4*>(
       static_cast<const char*>(pg.K) +
-      (page * pg.page_stride + ((static_cast<int64_t>(g) * D) << pg.page_shift)) * kEs);
+      (page * pg.page_stride + ((static_cast<int64_t>(g) * D) << pg.page_shift)) * kEs) + lane;
   const int vecs = kRowVecs << pg.page_shift;  // a multiple of 32
-  Extremes<E8> x;
-  x.set(__ldg(from + lane));
-#pragma unroll 4
-  for (int v = 32 + lane; v < vecs; v += 32) x.add(__ldg(from + v));
+  const int64_t at = static_cast<int64_t>(page) * pg.kv_heads + g;
+  const float page_scale = E8 ? __ldg(pg.k_scale + at) : 1.f;
+  __nv_bfloat162 lo[kRegs], hi[kRegs];
+  constexpr int kAtOnce = 4;
+  for (int v = 0; v < vecs; v += 32 * kAtOnce) {
+    uint4 u[kAtOnce];
 #pragma unroll
-  for (int s = kRowVecs; s < 32; s <<= 1) x.exchange(s);
-  constexpr int N = Extremes<E8>::kCols;
-  float lo[N], hi[N];
-  x.get(lo, hi);
+    for (int k = 0; k < kAtOnce; ++k)
+      if (v + 32 * k < vecs) u[k] = __ldg(from + v + 32 * k);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (v + 32 * k >= vecs) break;
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i) {
+        const __nv_bfloat162 x = K::at(u[k], i);
+        lo[i] = v + k == 0 ? x : __hmin2(lo[i], x);
+        hi[i] = v + k == 0 ? x : __hmax2(hi[i], x);
+      }
+    }
+  }
+  int at0 = 0;
+  reduce_rows<kRegs, kLeft>(lo, hi, at0);
+  float2 l[kLeft], h[kLeft];
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) top = fmaxf(top, fmaxf(-lo[i], hi[i]));
+  for (int i = 0; i < kLeft; ++i) {
+    l[i] = K::values(lo[i]);
+    h[i] = K::values(hi[i]);
+    top = fmaxf(top, fmaxf(fmaxf(-l[i].x, -l[i].y), fmaxf(h[i].x, h[i].y)));
+  }
   const float step = step_of(warp_max_f32(top));
   // a power of two: the products are exact
   const float inv = step > 0.f ? __uint_as_float(0x7f000000u - __float_as_uint(step)) : 0.f;
-  if (lane < kRowVecs) {
-    uint32_t l4[N / 4], h4[N / 4];
+  int8_t* out = a.bounds + at * 2 * D + lane % kRowVecs * (16 / kEs);
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      l4[i] = h4[i] = 0u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int il = __float2int_rd(lo[4 * i + k] * inv), ih = __float2int_ru(hi[4 * i + k] * inv);
-        l4[i] |= (static_cast<unsigned>(il) & 0xffu) << (8 * k);
-        h4[i] |= (static_cast<unsigned>(ih) & 0xffu) << (8 * k);
-      }
-    }
-    const int64_t at = static_cast<int64_t>(page) * pg.kv_heads + g;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.bounds + at * 2 * D + lane * N);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      out[i] = l4[i];
-      out[D / 4 + i] = h4[i];
-    }
-    if (lane == 0) a.bound_scale[at] = E8 ? step * pg.k_scale[at] : step;
+  for (int i = 0; i < kLeft; ++i) {
+    const int c = K::column(at0 + i), next = E8 ? 2 : 1;
+    out[c] = static_cast<int8_t>(__float2int_rd(l[i].x * inv));
+    out[c + next] = static_cast<int8_t>(__float2int_rd(l[i].y * inv));
+    out[D + c] = static_cast<int8_t>(__float2int_ru(h[i].x * inv));
+    out[D + c + next] = static_cast<int8_t>(__float2int_ru(h[i].y * inv));
   }
+  if (lane == 0) a.bound_scale[at] = E8 ? step * page_scale : step;
 }
 
 // ---------------------------------------------------------------------- scores
@@ -240,6 +215,7 @@ struct SelectArgs {
   int32_t* lengths;
   float* scores;  // [T, kv_heads, cols]
   unsigned* err;
+  uint64_t limit_ns;
 };
 
 // A token's sequence and position; state 0: no sequence's, -1: a bad entry.
@@ -247,27 +223,54 @@ struct TokenPlace {
   int b, pos, state;
 };
 
+// The sequence is the first whose tokens end behind t; 32 of them are looked at
+// with one round of loads.  Warp-collective.
 __device__ __forceinline__ TokenPlace place_of(const SelectArgs& a, int t) {
   const PagesView& pg = a.pages;
-  TokenPlace w{sequence_of_token(a.q_offsets, pg.B, t), 0, 0};
-  if (w.b >= pg.B) return w;
-  const int q0 = __ldg(a.q_offsets + w.b), q1 = __ldg(a.q_offsets + w.b + 1);
-  const int len = __ldg(pg.kv_len + w.b);
-  if (q0 < 0 || q1 < q0 || q1 > a.T || t >= q1 || (w.b > 0 && t < q0)) {
-    w.state = -1;
-  } else if (t >= q0) {
-    const int n = q1 - q0;
-    w.pos = len - n + (t - q0);
-    w.state = len >= n && len <= (static_cast<int64_t>(pg.cols) << pg.page_shift) ? 1 : -1;
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < pg.B; b0 += 32) {
+    const int b = b0 + lane;
+    int q0 = 0, q1 = 0, len = 0;
+    if (b < pg.B) {
+      q0 = __ldg(a.q_offsets + b);
+      q1 = __ldg(a.q_offsets + b + 1);
+      len = __ldg(pg.kv_len + b);
+    }
+    const unsigned behind = __ballot_sync(0xffffffffu, b < pg.B && q1 > t);
+    if (!behind) continue;
+    const int src = __ffs(behind) - 1;
+    q0 = __shfl_sync(0xffffffffu, q0, src);
+    q1 = __shfl_sync(0xffffffffu, q1, src);
+    len = __shfl_sync(0xffffffffu, len, src);
+    TokenPlace w{b0 + src, 0, 0};
+    if (q0 < 0 || q1 < q0 || q1 > a.T || (w.b > 0 && t < q0)) {
+      w.state = -1;
+    } else if (t >= q0) {
+      const int n = q1 - q0;
+      w.pos = len - n + (t - q0);
+      w.state = len >= n && len <= (static_cast<int64_t>(pg.cols) << pg.page_shift) ? 1 : -1;
+    }
+    if (w.state < 1) w.pos = 0;
+    return w;
   }
-  return w;
+  return TokenPlace{0, 0, 0};
 }
 
 constexpr int kScoreWarps = 4;
-constexpr int kRun = 32;          // pages of a warp: one look-up of their numbers
 constexpr int kHeadsAtOnce = 16;  // query heads in shared memory at a time
 // the score that marks a bad page number (a NaN no product gives)
 constexpr unsigned kBadScore = 0x7fffffffu;
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned;
+// completion is signalled on `bar` as transaction bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ int dot16(uint4 q, uint4 x, int s) {
   s = __dp4a(static_cast<int>(q.x), static_cast<int>(x.x), s);
@@ -276,43 +279,71 @@ __device__ __forceinline__ int dot16(uint4 q, uint4 x, int s) {
   return __dp4a(static_cast<int>(q.w), static_cast<int>(x.w), s);
 }
 
-// The scores of one (token, kv head)'s pages, a run of kRun neighbouring ones to
-// a warp: D / 16 lanes to a page, 16 columns of lo and hi to a lane, kAhead
-// rounds of pages under way.  Four heads' sums are spread over the lanes while
-// they are summed up, half as many exchanges as one by one.
+// N query heads' sums with a page's bounds: L pieces of 16 columns.
+template <int L, int N>
+__device__ __forceinline__ float heads_bound(const uint4 (*q_pos)[L], const uint4 (*q_neg)[L],
+                                             const float* q_step, const uint4* bounds) {
+  int s[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = 0;
+#pragma unroll
+  for (int c = 0; c < L; ++c) {
+    const uint4 lo = bounds[c], hi = bounds[L + c];
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = dot16(q_neg[k][c], lo, dot16(q_pos[k][c], hi, s[k]));
+  }
+  float best = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < N; ++k) best = fmaxf(best, static_cast<float>(s[k]) * q_step[k]);
+  return best;
+}
+
+// The scores of one (token, kv head)'s pages, 32 neighbouring ones to a warp.
+// Every lane sends for the bounds of one page (a bulk copy of 2 d bytes to shared
+// memory, in rows 16 bytes longer, so that the lanes' pieces lie in different
+// banks), so a warp's pages are under way at once, and sums up its own page's:
+// the query heads' pieces are the same for all lanes, and no sum crosses them.
+// (With d / 16 lanes to a page and exchanges between them a round of four pages
+// took 156 instructions, and a batch of 16 over 64 to 128 K keys 24 us.)
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps)
     kv_score_kernel(const SelectArgs a, int chunks) {
-  constexpr int L = D / 16;       // lanes per page
-  constexpr int kPages = 32 / L;  // pages per warp and round
-  constexpr int kAhead = 4;
-  static_assert(kRun % (kPages * kAhead) == 0, "whole rounds");
+  constexpr int L = D / 16;  // 16-byte pieces of a row
+  __shared__ __align__(16) uint4 pages_s[kScoreWarps][32][2 * L + 1];
   __shared__ uint4 q_pos[kHeadsAtOnce][L], q_neg[kHeadsAtOnce][L];
   __shared__ float q_step[kHeadsAtOnce];
+  __shared__ uint64_t arrived[kScoreWarps];
+  __shared__ int gave_up;
   const PagesView& pg = a.pages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t bar = smem_u32(&arrived[warp]);
+  if (lane == 0) mbar_init(bar, 1);
+  if (threadIdx.x == 0) gave_up = 0;
+  fence_mbar_init();
+  __syncthreads();
   const int item = static_cast<int>(blockIdx.x / static_cast<unsigned>(chunks));
   const int chunk = static_cast<int>(blockIdx.x % static_cast<unsigned>(chunks));
   const int t = item / pg.kv_heads, g = item % pg.kv_heads;
   pdl_launch_dependents();
   const TokenPlace w = place_of(a, t);
   const int newest = w.pos >> pg.page_shift;  // full pages that the token sees
-  const int b0 = chunk * kScoreWarps * kRun;
+  const int b0 = chunk * kScoreWarps * 32;
   // without a choice to make, or pages of this stretch, there is nothing to score
   if (w.state < 1 || newest < a.n_select || b0 >= newest) return;
-  const int c0 = b0 + warp * kRun;
-  int pages = -1;
-  if (c0 + lane < newest) pages = __ldg(pg.table + static_cast<int64_t>(w.b) * pg.cols + c0 + lane);
-  const bool good = pages >= 0 && pages < pg.num_pages;
-  const int64_t at0 = static_cast<int64_t>(good ? pages : 0) * pg.kv_heads + g;
+  const int c = b0 + warp * 32 + lane;
+  int page = -1;
+  if (c < newest) page = __ldg(pg.table + static_cast<int64_t>(w.b) * pg.cols + c);
+  const bool good = page >= 0 && page < pg.num_pages;
+  const int64_t at = static_cast<int64_t>(good ? page : 0) * pg.kv_heads + g;
+  // a page behind the last, or a bad one, is not sent for: nothing comes of what
+  // lies in its place
+  const unsigned sent = __ballot_sync(0xffffffffu, good);
+  if (lane == 0) mbar_expect_tx(bar, __popc(sent) * 2 * D);
+  __syncwarp();
+  if (good) bulk_load(smem_u32(pages_s[warp][lane]), a.bounds + at * 2 * D, 2 * D, bar);
   float scale = 0.f;
-  if (good) scale = __ldg(a.bound_scale + at0);
-  const int part = lane % L;
-  // this lane's heads of four, after the sums
-  const int mine = (lane & L / 2 ? 2 : 0) + (lane & L / 4 ? 1 : 0);
-  float best[kRun / kPages];
-#pragma unroll
-  for (int i = 0; i < kRun / kPages; ++i) best[i] = -INFINITY;
+  if (good) scale = __ldg(a.bound_scale + at);
+  float best = -INFINITY;
   for (int h0 = 0; h0 < a.G; h0 += kHeadsAtOnce) {
     const int heads = min(kHeadsAtOnce, a.G - h0);
     if (h0) __syncthreads();
@@ -342,58 +373,28 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
       if (lane == 0) q_step[h] = step;
     }
     __syncthreads();
-#pragma unroll
-    for (int i0 = 0; i0 < kRun / kPages; i0 += kAhead) {
-      if (c0 + i0 * kPages >= newest) break;
-      uint4 lo[kAhead], hi[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        // a page behind the last, or a bad one, reads page 0's: nothing comes of it
-        const int64_t at = __shfl_sync(0xffffffffu, at0, (i0 + i) * kPages + lane / L);
-        const uint4* from = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + part;
-        lo[i] = __ldg(from);
-        hi[i] = __ldg(from + L);
+    if (h0 == 0 && !mbar_wait_warp(bar, 0, WaitCtl{&gave_up, a.err, a.limit_ns})) {
+      // the copies may land yet: not before they do, or the limit has passed
+      // once more, may the block end
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar, 0) && global_timer_ns() - t0 < a.limit_ns) {
       }
-      for (int h = 0; h < heads; h += 4) {
-        int s[kAhead][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // heads behind the last are the last once more
-          const int hk = min(h + k, heads - 1);
-          const uint4 qp = q_pos[hk][part], qn = q_neg[hk][part];
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) s[i][k] = dot16(qn, lo[i], dot16(qp, hi[i], 0));
-        }
-        const float step = q_step[min(h + mine, heads - 1)];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const bool upper = lane & L / 2, second = lane & L / 4;
-          int a0 = upper ? s[i][2] : s[i][0], a1 = upper ? s[i][3] : s[i][1];
-          a0 += __shfl_xor_sync(0xffffffffu, upper ? s[i][0] : s[i][2], L / 2);
-          a1 += __shfl_xor_sync(0xffffffffu, upper ? s[i][1] : s[i][3], L / 2);
-          int sum = (second ? a1 : a0) + __shfl_xor_sync(0xffffffffu, second ? a0 : a1, L / 4);
-#pragma unroll
-          for (int k = L / 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-          best[i0 + i] = fmaxf(best[i0 + i], static_cast<float>(sum) * step);
-        }
-      }
+      __syncwarp();
     }
-  }
-  // page l of the run to lane l, coalesced
-  float score = 0.f;
-#pragma unroll
-  for (int i = 0; i < kRun / kPages; ++i) {
-    float x = best[i];
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, L / 2));
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, L / 4));
-    const float v = __shfl_sync(0xffffffffu, x, lane % kPages * L);
-    if (lane / kPages == i) score = v;
+    const uint4* mine = pages_s[warp][lane];
+    int h = 0;
+    for (; h + 4 <= heads; h += 4)
+      best = fmaxf(best, heads_bound<L, 4>(q_pos + h, q_neg + h, q_step + h, mine));
+    if (h + 2 <= heads) {
+      best = fmaxf(best, heads_bound<L, 2>(q_pos + h, q_neg + h, q_step + h, mine));
+      h += 2;
+    }
+    if (h < heads) best = fmaxf(best, heads_bound<L, 1>(q_pos + h, q_neg + h, q_step + h, mine));
   }
   // + 0: a product that underflows has no sign
-  score = score * scale + 0.f;
-  if (c0 + lane < newest)
-    a.scores[(static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols + c0 + lane] =
-        good ? score : __uint_as_float(kBadScore);
+  if (c < newest)
+    a.scores[(static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols + c] =
+        good ? best * scale + 0.f : __uint_as_float(kBadScore);
 }
 
 // --------------------------------------------------------------------- choice
@@ -401,6 +402,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickKeys = 8192;  // that stay in shared memory; those behind are read again
+constexpr int kStaged = 2048;    // places whose pages are looked up together at the end
+constexpr int kClose = 512;      // scores of one bin that are compared with one another
 
 // fp32 in the order of unsigned whole numbers; a NaN, which finite bounds and
 // scales never give, below all others.
@@ -410,16 +413,24 @@ __device__ __forceinline__ unsigned rank_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One block per (token, kv head): the n_select - 1 largest scores by a search
-// for the smallest of them, eight bits at a time from the highest one in which
-// any two differ (scores share their exponent's first bits, and one bin's
-// counter would serialise them), then the pages in order.
+// The number that a key stands for (a NaN's is one).
+__device__ __forceinline__ float score_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// One block per (token, kv head): the n_select - 1 largest scores, then the
+// pages in order.  The smallest of them is looked for among evenly spaced bins
+// of the scores' range; the few scores of its bin are compared with one another.
+// Should they be many (equal scores, or one far from the rest), they are searched
+// by their bits, eight at a time.
 __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs a) {
   __shared__ unsigned keys[kPickKeys];
-  __shared__ int bins[256];
+  __shared__ int bins[kPickThreads];
+  __shared__ int staged[kStaged];
+  __shared__ unsigned close[kClose];
   __shared__ int counts[2][kPickWarps];
   __shared__ unsigned least[kPickWarps], most[kPickWarps];
-  __shared__ int found[2];
+  __shared__ int found[3];
   const PagesView& pg = a.pages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x / pg.kv_heads, g = blockIdx.x % pg.kv_heads;
@@ -430,7 +441,8 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
   const float* scores = a.scores + (static_cast<int64_t>(t) * pg.kv_heads + g) * pg.cols;
   int picked = 0;
   bool bad = w.state < 0;
-  for (int i = threadIdx.x; i < 256; i += kPickThreads) bins[i] = 0;
+  bins[threadIdx.x] = 0;
+  if (threadIdx.x == 0) found[2] = 0;
   pdl_wait();
   if (w.state == 1 && newest < a.n_select) {
     // every page there is
@@ -446,13 +458,22 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
     const int want = a.n_select - 1;
     bool wrong = false;
     unsigned lo = 0xffffffffu, hi = 0u;
-    for (int c = threadIdx.x; c < newest; c += kPickThreads) {
-      const float x = scores[c];
-      const unsigned key = rank_key(x);
-      wrong = wrong || __float_as_uint(x) == kBadScore;
-      if (c < kPickKeys) keys[c] = key;
-      lo = min(lo, key);
-      hi = max(hi, key);
+    constexpr int kAtOnce = 8;
+    for (int c0 = threadIdx.x; c0 < newest; c0 += kAtOnce * kPickThreads) {
+      float x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        x[k] = c0 + k * kPickThreads < newest ? scores[c0 + k * kPickThreads] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int c = c0 + k * kPickThreads;
+        if (c >= newest) break;
+        const unsigned key = rank_key(x[k]);
+        wrong = wrong || __float_as_uint(x[k]) == kBadScore;
+        if (c < kPickKeys) keys[c] = key;
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
     }
     auto key_of = [&](int c) { return c < kPickKeys ? keys[c] : rank_key(scores[c]); };
     if (threadIdx.x == 0) {
@@ -471,55 +492,110 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
       lo = min(lo, least[i]);
       hi = max(hi, most[i]);
     }
-    // the want-th largest key, and how many of the equal ones are in.  Above
-    // bit `top` all keys agree.
-    int top = lo == hi ? 0 : 32 - __clz(lo ^ hi);
-    unsigned prefix = top == 32 ? 0u : hi >> top << top;
+    // the want-th largest key, and how many of the equal ones are in
+    unsigned prefix = hi;
     int left = want;
-    while (top > 0 && want > 0) {
-      const int shift = max(top - 8, 0);
+    if (lo != hi && want > 0) {
+      // bins that grow with the score, whatever the rounding; a NaN's, or one of
+      // an infinite range, is the first
+      const float base = score_of(lo);
+      const float per = (kPickThreads - 1) / (score_of(hi) - base);
+      auto bin_of = [&](unsigned key) {
+        return min(max(__float2int_rd((score_of(key) - base) * per), 0), kPickThreads - 1);
+      };
+      for (int c = threadIdx.x; c < newest; c += kPickThreads) atomicAdd(&bins[bin_of(key_of(c))], 1);
+      __syncthreads();
+      // thread i: the scores in bin kPickThreads - 1 - i and those above
+      const int mine = bins[kPickThreads - 1 - threadIdx.x];
+      int incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += up;
+      }
+      if (lane == 31) counts[0][warp] = incl;
+      __syncthreads();
+      for (int i = 0; i < warp; ++i) incl += counts[0][i];
+      if (incl >= left && incl - mine < left) {
+        found[0] = kPickThreads - 1 - threadIdx.x;
+        found[1] = left - (incl - mine);
+      }
+      __syncthreads();
+      const int bin = found[0];
+      left = found[1];
       for (int c = threadIdx.x; c < newest; c += kPickThreads) {
         const unsigned key = key_of(c);
-        if (top == 32 || key >> top == prefix >> top)
-          atomicAdd(&bins[(key >> shift) & (0xffu >> (8 - (top - shift)))], 1);
+        if (bin_of(key) != bin) continue;
+        const int i = atomicAdd(&found[2], 1);
+        if (i < kClose) close[i] = key;
       }
+      bins[threadIdx.x] = 0;
       __syncthreads();
-      if (warp == 0) {
-        // lane l: bins 255 - 8 l and the seven below
-        int mine[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum += mine[i] = bins[255 - 8 * lane - i];
-          bins[255 - 8 * lane - i] = 0;
-        }
-        int incl = sum;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, incl, s);
-          if (lane >= s) incl += up;
-        }
-        int before = incl - sum;
-        if (before < left && incl >= left) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < left && before + mine[i] >= left) {
-              found[0] = 255 - 8 * lane - i;
-              found[1] = left - before;
-            }
-            before += mine[i];
+      const int n = found[2];
+      if (n <= kClose) {
+        for (int i = threadIdx.x; i < n; i += kPickThreads) {
+          const unsigned key = close[i];
+          int above = 0, equal = 0;
+          for (int k = 0; k < n; ++k) {
+            above += close[k] > key ? 1 : 0;
+            equal += close[k] == key ? 1 : 0;
+          }
+          if (above < left && above + equal >= left) {  // equal ones agree
+            found[0] = static_cast<int>(key);
+            found[1] = left - above;
           }
         }
+        __syncthreads();
+        prefix = static_cast<unsigned>(found[0]);
+        left = found[1];
+      } else {
+        prefix = 0u;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+          for (int c = threadIdx.x; c < newest; c += kPickThreads) {
+            const unsigned key = key_of(c);
+            if (bin_of(key) == bin && (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)))
+              atomicAdd(&bins[(key >> shift) & 255u], 1);
+          }
+          __syncthreads();
+          if (warp == 0) {
+            // lane l: bins 255 - 8 l and the seven below
+            int part[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              sum += part[i] = bins[255 - 8 * lane - i];
+              bins[255 - 8 * lane - i] = 0;
+            }
+            int upto = sum;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+              const int up = __shfl_up_sync(0xffffffffu, upto, s);
+              if (lane >= s) upto += up;
+            }
+            int before = upto - sum;
+            if (before < left && upto >= left) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (before < left && before + part[i] >= left) {
+                  found[0] = 255 - 8 * lane - i;
+                  found[1] = left - before;
+                }
+                before += part[i];
+              }
+            }
+          }
+          __syncthreads();
+          prefix |= static_cast<unsigned>(found[0]) << shift;
+          left = found[1];
+          __syncthreads();
+        }
       }
-      __syncthreads();
-      prefix |= static_cast<unsigned>(found[0]) << shift;
-      left = found[1];
-      top = shift;
     }
     // a warp takes a stretch of neighbouring columns: first its number of
     // larger and of equal keys, then the places
     const int stretch = (newest + kPickThreads - 1) / kPickThreads * 32;
     const int s0 = warp * stretch, s1 = min(newest, s0 + stretch);
     int above = 0, equal = 0;
+#pragma unroll 4
     for (int c = s0 + lane; c - lane < s1; c += 32) {
       const unsigned key = c < s1 ? key_of(c) : 0u;
       above += __popc(__ballot_sync(0xffffffffu, c < s1 && want > 0 && key > prefix));
@@ -544,10 +620,19 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const SelectArgs 
       const unsigned below = (1u << lane) - 1u;
       const int na = a0 + __popc(ma & below), ne = e0 + __popc(me & below);
       // of the equal ones before this column, at most `left` are in
-      if (is_above || (is_equal && ne < left)) out[na + min(ne, left)] = __ldg(row + c);
+      if (is_above || (is_equal && ne < left)) {
+        const int place = na + min(ne, left);
+        if (place < kStaged)
+          staged[place] = c;
+        else
+          out[place] = __ldg(row + c);
+      }
       a0 += __popc(ma);
       e0 += __popc(me);
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < min(want, kStaged); i += kPickThreads)
+      out[i] = __ldg(row + staged[i]);
     if (threadIdx.x == 0) out[want] = __ldg(row + newest);
     picked = a.n_select;
   }
@@ -598,7 +683,7 @@ mha_status kv_pages_bounds(const mha_kv_pages* pages, const mha_kv_scales* scale
   const int64_t full = T / pages->page_size + seqs;
   const int64_t units = (full < T ? full : T) * pages->kv_heads;
   const int64_t blocks = (units + kBoundWarps - 1) / kBoundWarps;
-  if (blocks > 0x7fffffffLL) return MHA_ERR_UNSUPPORTED;
+  if (units > 0x7fffffffLL) return MHA_ERR_UNSUPPORTED;
   const unsigned n = static_cast<unsigned>(blocks);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64 && scales)
@@ -643,9 +728,9 @@ mha_status kv_pages_select(const void* Q, int64_t q_token_stride, const mha_kv_p
   const int64_t at = static_cast<int64_t>(pages->num_pages) * Hkv * layer;
   const SelectArgs a{static_cast<const __nv_bfloat16*>(Q), q_token_stride, pages_view(*pages, layer),
                      q_offsets, bounds + at * 2 * d, bound_scale + at, T, H, G, n_select, selected,
-                     lengths, static_cast<float*>(workspace), ctl.err};
+                     lengths, static_cast<float*>(workspace), ctl.err, ctl.limit_ns};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int chunks = (pages->table_cols + kScoreWarps * kRun - 1) / (kScoreWarps * kRun);
+  const int chunks = (pages->table_cols + kScoreWarps * 32 - 1) / (kScoreWarps * 32);
   const int64_t blocks = items * chunks;
   if (blocks > 0x7fffffffLL) return MHA_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>(blocks);
