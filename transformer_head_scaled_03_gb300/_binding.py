@@ -783,26 +783,25 @@ def kv_pages_select(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, boun
     on = _launch_on(stream, Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale,
                     *_given(K_scale, V_scale, workspace), *(() if out is None else out))
     dev, Hkv = _lib or lib(), pages.kv_heads
+    n = T * Hkv * n_select
+    need = dev.kv_pages_select_workspace_bytes(T, Hkv, pages.table_cols) if workspace is None else 0
     if out is None:
-        # one allocation: the two tables, and the workspace 16 bytes on
-        n = T * Hkv * n_select
-        own = 0 if workspace is not None else dev.kv_pages_select_workspace_bytes(
-            T, Hkv, pages.table_cols) // 4
+        # one allocation: the two tables, and the workspace behind them
         at = -(-(n + T) // 4) * 4
-        both = _new(stream, (at + own,), torch.int32, Q.device)
-        out = both[:n].view(T, Hkv, n_select), both[n:n + T]
-        if workspace is None:
-            workspace = both[at:]
+        own = _new(stream, (at + need // 4,), torch.int32, Q.device)
+        out = own.as_strided((T, Hkv, n_select), (Hkv * n_select, n_select, 1)), own.narrow(0, n, T)
+        ws, size = own.data_ptr() + 4 * at, need
     else:
         _int32("selected", out[0], T, Hkv, n_select)
         _int32("lengths", out[1], T)
         if workspace is None:
-            workspace = _new(stream, (dev.kv_pages_select_workspace_bytes(
-                T, Hkv, pages.table_cols) or 16,), torch.uint8, Q.device)
+            own = _new(stream, (need or 16,), torch.uint8, Q.device)
+            ws, size = own.data_ptr(), need
+    if workspace is not None:
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = dev.kv_pages_select(Q.data_ptr(), q_ts, pages, layer, q_offsets.data_ptr(), bounds.data_ptr(),
                              bound_scale.data_ptr(), T, H, n_select, out[0].data_ptr(),
-                             out[1].data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), on)
+                             out[1].data_ptr(), ws, size, on)
     _check(st, "kv_pages_select")
     return out
 
