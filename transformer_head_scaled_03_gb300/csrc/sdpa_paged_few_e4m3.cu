@@ -48,8 +48,11 @@ struct Few8Cfg {
   static_assert(U == 4 || U == 8 || U == 16, "slots");
   static constexpr int N = 2 * U < 16 ? 16 : 2 * U;  // the products' columns
   static constexpr uint32_t kTmemCols = N == 16 ? 64u : 128u;  // S^T x 2, O^T x 2
-  static constexpr int NR = D == 128 ? (kAlone ? 12 : 6) : kAlone ? 22 : 11;
-  static constexpr int kCtas = kAlone ? 1 : 2;
+  // Two CTAs share an SM, or three with few slots at d = 64, where a tile is half
+  // the bytes for the same softmax (16 sequences of 16 to 32 K keys, 32 heads on
+  // 8: 83 -> 76 us; at d = 128 three took 121 us instead of 117).
+  static constexpr int kCtas = kAlone ? 1 : D == 64 && U == 4 ? 3 : 2;
+  static constexpr int NR = D == 128 ? (kAlone ? 12 : 6) : kAlone ? 22 : kCtas == 3 ? 7 : 11;
   static constexpr int kTile = kKeys * D;
   static constexpr int kPBuf = N * 128;  // W^T of one tile: N rows x 128 keys
   static constexpr int kOffRing = 0;
@@ -70,9 +73,11 @@ struct Few8Cfg {
   static constexpr int bDrain = 1 + 2 * NR + 8;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kOffQs = kOffMisc + 16;  // a row's scale, [16]
+  // of every slot, [16]: its row's scale times the softmax's, its last key
+  static constexpr int kOffQs = (kOffMisc + 16 + 15) / 16 * 16;
+  static constexpr int kOffLast = kOffQs + kSlots * 4;
   // lengths and offsets of the sequences, while they are ranked
-  static constexpr int kOffSeq = kOffQs + kSlots * 4;
+  static constexpr int kOffSeq = kOffLast + kSlots * 4;
   static constexpr int kSeqBytes = (2 * kMaxSortedBatch + 2) * 4;
   // the M = 128 operand of a d = 64 product reads the 8 KB after a V tile as
   // its unused upper half: there is that much after the last slot
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
   }
   float* red = reinterpret_cast<float*>(gbase + C::kOffRed);
   float* q_scale = reinterpret_cast<float*>(gbase + C::kOffQs);
+  int* last_key = reinterpret_cast<int*>(gbase + C::kOffLast);
   float* xm = reinterpret_cast<float*>(gbase + C::kOffX);
   float* xl = xm + kSlots;
   float* xo = xl + kSlots;
@@ -356,7 +362,10 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
       for (int s = 1; s < 8; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
       float inv;
       const float scale = part_scale_of(top, &inv);
-      if (part == 0) q_scale[qr] = scale * p.scale_log2;
+      if (part == 0) {
+        q_scale[qr] = scale * p.scale_log2;
+        last_key[qr] = qr >= rows ? -1 : p.causal ? len - seq.n + i : len - 1;
+      }
       if (qr < U) {
         uint32_t hi[n / 4], lo[n / 4];
 #pragma unroll
@@ -395,20 +404,18 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
     float sk, sv;
     scales_of(page, sk, sv);
 
-    // the last key each slot sees; -1 for a slot not in use
-    int last[U];
-    float qs[U];
     float m[U], l[U], acc[U], alpha_prev[U];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      last[q] = q >= rows ? -1 : p.causal ? len - seq.n + div_by_group(p, q) : len - 1;
-      qs[q] = q_scale[q];
       m[q] = -INFINITY;
       l[q] = 0.f;
       acc[q] = 0.f;
       alpha_prev[q] = 1.f;
     }
     float c = 0.f;  // the largest value scale so far
+    // keys that every slot sees (one not in use may see any: its sums are not
+    // stored)
+    const int all_see = p.causal ? len - seq.n + 1 : len;
     // W^T store address of key r: 16-byte piece and byte of a 128-byte row
     const int piece = r >> 4;
     uint8_t* p_key = gbase + C::kOffP + (r & 15);
@@ -427,9 +434,17 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
         uint32_t sr[2 * U];
         tmem_ld_cols<2 * U>(tS + buf * C::N, sr);
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-          const float x = fmaf(__uint_as_float(sr[U + q]), 1.f / kQUp, __uint_as_float(sr[q]));
-          s[q] = key <= last[q] ? x * (sk * qs[q]) : -INFINITY;
+        for (int q = 0; q < U; q += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(q_scale + q);
+          const float qs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            s[q + k] = fmaf(__uint_as_float(sr[U + q + k]), 1.f / kQUp, __uint_as_float(sr[q + k])) *
+                       (sk * qs[k]);
+        }
+        if ((t_begin + j + 1) * kKeys > all_see) {
+#pragma unroll
+          for (int q = 0; q < U; ++q) s[q] = key <= last_key[q] ? s[q] : -INFINITY;
         }
       }
       float* rb = red + buf * 4 * C::kRedRow;
@@ -613,23 +628,22 @@ cudaError_t launch_as(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
 }
 
 template <int D, int U>
-cudaError_t launch_slots(const PagedSdpaArgs& a, bool alone, const DeviceCtl& ctl) {
-  return alone ? launch_as<D, U, true>(a, ctl) : launch_as<D, U, false>(a, ctl);
-}
-
-template <int D>
-cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
+cudaError_t launch_slots(PagedSdpaArgs a, const DeviceCtl& ctl) {
   const int64_t clusters = static_cast<int64_t>(a.pages.B) * a.pages.kv_heads;
   if (a.splits == 0)
     a.splits = paged_default_splits(
         clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads,
-        Few8Cfg<D, 16, false>::kSmemBytes);
+        Few8Cfg<D, U, false>::kSmemBytes);
   const bool alone =
-      clusters <= paged_resident_clusters(kThreads, Few8Cfg<D, 16, true>::kSmemBytes, a.splits);
+      clusters <= paged_resident_clusters(kThreads, Few8Cfg<D, U, true>::kSmemBytes, a.splits);
+  return alone ? launch_as<D, U, true>(a, ctl) : launch_as<D, U, false>(a, ctl);
+}
+
+template <int D>
+cudaError_t launch_impl(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
   const int64_t rows = static_cast<int64_t>(a.max_new) * a.G;
-  if (rows <= 4) return launch_slots<D, 4>(a, alone, ctl);
-  if (rows <= 8) return launch_slots<D, 8>(a, alone, ctl);
-  return launch_slots<D, 16>(a, alone, ctl);
+  return rows <= 4 ? launch_slots<D, 4>(a, ctl)
+                   : rows <= 8 ? launch_slots<D, 8>(a, ctl) : launch_slots<D, 16>(a, ctl);
 }
 
 }  // namespace
