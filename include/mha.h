@@ -374,13 +374,14 @@ mha_status sdpa_paged(const void *Q, int64_t q_token_stride,
 
 /*
  * sdpa_paged_e4m3 -- sdpa_paged over a cache in 8 bits.  Q is bf16; the rest is
- * as for sdpa_paged, but for the products' operands: a query row meets the
+ * as for sdpa_paged, but for the products' operands.  A query row meets the
  * keys' codes as two e4m3 parts, which together are off by at most 2^-18 of
- * the row's largest element, and the weights, times the values' scales over
- * the largest of them that the CTA has met, meet the values' codes as two
- * e4m3 parts (up to 16 rows, see max_new: off by 2^-8 of the weight or 2^-23 of
- * the largest one) or in bf16 against values in bf16 (more rows: powers of two
- * as scales are exact there, others round a value by 2^-8).
+ * the row's largest element.  The weights, times the values' scales, meet the
+ * values' codes as two e4m3 parts (up to 16 rows, see max_new: off by 2^-8 of a
+ * weight, or 2^-23 of the largest weight times the largest scale) or in fp16
+ * (more rows: off by 2^-11 of a weight, or 2^-31 of the largest product of
+ * weight and scale; the value scales of one sequence, but for zeros, lie
+ * within 2^100 of each other).  An infinity in a query gives NaN in its row.
  */
 mha_status sdpa_paged_e4m3(const void *Q, int64_t q_token_stride,
                            const mha_kv_pages *pages,
@@ -601,7 +602,8 @@ mha_status kv_pages_compact_e4m3(const mha_kv_pages *src,
  * bound_scale is s times the page's key scale.  Called after each append (of
  * whole sequences at first: q_offsets from their lengths) it keeps the bounds
  * of all full pages; pages that are shared keep theirs, and a page that a fork
- * copies gets its own once it is full.
+ * copies gets its own once it is full.  A compaction moves pages, not bounds:
+ * after it they are made anew, for whole sequences.
  *   scales : of a cache in 8 bits (dtype MHA_E4M3); NULL for MHA_BF16.
  *   T : the packed tokens, q_offsets as for sdpa_paged.
  * d is 64 or 128.  Keys must be finite.

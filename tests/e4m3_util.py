@@ -37,21 +37,19 @@ def codes_of(t):
     return t.view(torch.uint8).cpu().numpy()
 
 
-def attention_bound(O, A, Q, K, V_codes_max, v_scale_max, keys, scale, bf16_out, pow2):
+def attention_bound(O, A, Q, K, v_scale_max, keys, scale, bf16_out):
     """How far an attention over pages in 8 bits may be off, from the arithmetic.
 
-    Weights: two e4m3 parts are off by (2^-4)^2 = 2^-8 of a weight, or bf16 by
-    2^-8 of it; fp32 scores, exponentials and sums by 2^-10, as for the bf16
-    cache.  Values in bf16 under scales that are no powers of two: 2^-8 once
-    more.  The parts' smallest half steps: 2^-10 / 2^5 against a largest weight
-    of 2^8, so 2^-23 of the largest weight times scale for each key, times its
-    code (at most 448); the weights' sum is at least 1 in the same units.
+    Weights: two e4m3 parts are off by (2^-4)^2 = 2^-8 of a weight (fp16, with
+    more rows, by 2^-11); fp32 scores, exponentials and sums by 2^-10, as for the
+    bf16 cache.  The parts' smallest half steps: 2^-10 / 2^5 against a largest
+    weight of 2^8, so 2^-23 of the largest weight times scale for each key (fp16:
+    2^-25 against 2^6 or more), times its code (at most 448); the weights' sum is
+    at least 1 in the same units.
     Scores: two parts of q are off by 2^-18 of the row's largest element, so a
     score by 2^-18 max|q| max_j sum_c |k_jc| scale, and a weight by twice that."""
     q_max = np.abs(Q).max(-1)[..., None]
     k_sum = np.abs(K).sum(-1).max()
     b = (2.0 ** -8 + 2.0 ** -10 + 2 * 2.0 ** -18 * q_max * k_sum * scale) * A
-    if not pow2:
-        b = b + 2.0 ** -8 * A
-    b = b + keys * 2.0 ** -23 * v_scale_max * V_codes_max + 1e-30
+    b = b + keys * 2.0 ** -23 * v_scale_max * 448 + 1e-30
     return b + 2.0 ** -8 * np.abs(O) if bf16_out else b

@@ -301,15 +301,14 @@ def selected_case(seed, T, H, Hkv, ps, d, n, lens, e8, pow2=True):
     else:
         K, V, *_ = make_pages(rng, [P * ps], [1], Hkv, ps, d, bf16=True, spare=0)
         vs, pools, sc = np.ones((P, Hkv)), (dev(K, BF), dev(V, BF)), {}
-    return Q, K, V, vs, sel, np.asarray(lens, np.int32), pools, sc, pow2
+    return Q, K, V, vs, sel, np.asarray(lens, np.int32), pools, sc
 
 
 def check_selected(got, x, e8, scale=0.0):
-    Q, K, V, vs, sel, lens, _, _, pow2 = x
+    Q, K, V, vs, sel, lens, _, _ = x
     O, A = ref.sdpa_selected(Q, K, V, sel, lens, scale)
     if e8:
-        b = attention_bound(O, A, Q, K, 448, vs.max(), lens.max(), scale or Q.shape[-1] ** -0.5,
-                            got.dtype == BF, pow2)
+        b = attention_bound(O, A, Q, K, vs.max(), lens.max(), scale or Q.shape[-1] ** -0.5, got.dtype == BF)
     else:
         b = (2.0 ** -8 + 2.0 ** -10) * A + 1e-30 + (2.0 ** -8 * np.abs(O) if got.dtype == BF else 0)
     used = lens > 0
@@ -334,7 +333,7 @@ SELECTED = [
 def test_selected(c, e8):
     T, H, Hkv, ps, d, n, lens, splits, odt = c
     x = selected_case(570 + SELECTED.index(c), T, H, Hkv, ps, d, n, lens, e8, SELECTED.index(c) % 2 == 0)
-    Q, _, _, _, sel, rows, pools, sc, _ = x
+    Q, _, _, _, sel, rows, pools, sc = x
     out = torch.full(Q.shape, 7.0, dtype=odt, device="cuda")
     mha.sdpa_paged_selected(dev(Q, BF), *pools, i32(sel), i32(rows), out_dtype=odt, num_splits=splits, out=out,
                             **sc)
@@ -347,7 +346,7 @@ def test_selected(c, e8):
 @pytest.mark.parametrize("H", [4, 40])
 def test_selected_reports_bad_entries(e8, H):
     x = selected_case(590, 3, H, 2, 16, 64, 6, [90, 80, 70], e8)
-    Q, K, V, vs, sel, rows, pools, sc, _ = x
+    Q, K, V, vs, sel, rows, pools, sc = x
 
     def call(sel=sel, rows=rows):
         out = torch.full(Q.shape, 7.0, dtype=F32, device="cuda")
@@ -373,7 +372,7 @@ def test_selected_reports_bad_entries(e8, H):
 @pytest.mark.parametrize("e8", [False, True])
 def test_no_tokens(e8):
     x = selected_case(591, 1, 4, 2, 16, 64, 6, [90], e8)
-    Q, _, _, _, sel, rows, pools, sc, _ = x
+    Q, _, _, _, sel, rows, pools, sc = x
     out = mha.sdpa_paged_selected(dev(Q[:0], BF), *pools, i32(sel[:0]), i32(rows[:0]), **sc)
     assert out.shape == (0, 4, 64) and mha.mha_check() == mha.MHA_OK
 
@@ -443,8 +442,7 @@ def test_serving_steps_over_selected_pages(e8, H, Hkv, d, ps):
             assert np.array_equal(count.cpu().numpy(), rows_seen)
             held = [p for b in range(B) for p in tb[b, :-(-int(ln[b]) // ps)]]
             K, V = (np.where(np.isfinite(a), a, 0.0) for a in (K, V))
-            x = (to_np(qo), K[:, :] if not held else K, V, vs[held] if held else vs, want, rows_seen, None, None, True)
-            check_selected(O, x, e8)
+            check_selected(O, (to_np(qo), K, V, vs[held], want, rows_seen, None, None), e8)
 
     for new in ([70, 33, 1], [100, 0, 40], [1, 1, 1], [16, 2, 0]):
         lens += i32(new)
@@ -459,6 +457,29 @@ def test_serving_steps_over_selected_pages(e8, H, Hkv, d, ps):
     for y, (qo, _, _, O) in enumerate(outs):
         whole = mha.sdpa_paged(qo, kp, vp, table, lens, offs, max_new=1, layer=y, **sc)
         assert float((whole.float() - O.float()).abs().max()) <= 2.0 ** -6
+    # compaction moves pages, scales with them; their bounds are made anew
+    shape2 = (layers, P + 5, Hkv, ps, d)
+    k2, v2 = (torch.zeros(shape2, dtype=torch.uint8 if e8 else BF, device="cuda").view(kp.dtype)
+              for _ in range(2))
+    t2 = torch.full_like(table, -1)
+    sc2 = {k: torch.full(shape2[:3], 9.0, device="cuda") for k in sc}
+    live = mha.kv_pages_compact(kp, vp, table, lens, k2, v2, t2, **sc, **{k + "_out": v for k, v in sc2.items()})
+    assert int(live) == sum(-(-int(n) // ps) for n in lens)
+    # what lies behind the held rows stays what it was at first: NaN
+    k2.view(torch.uint8)[:, int(live):] = 0xff
+    v2.view(torch.uint8)[:, int(live):] = 0xff
+    spare = iter(range(int(live), P + 5))
+    for b in range(B):
+        for j in range(-(-int(lens[b]) // ps), cols):
+            t2[b, j] = next(spare, -1)
+    kp, vp, table, sc, P = k2, v2, t2, sc2, P + 5
+    bnd, bs = torch.zeros((layers, P, Hkv, 2, d), dtype=torch.int8, device="cuda"), torch.zeros(
+        (layers, P, Hkv), device="cuda")
+    whole = i32(np.concatenate(([0], np.cumsum(lens.cpu().numpy()))))
+    for y in range(layers):
+        mha.kv_pages_bounds(kp, vp, table, lens, whole, bnd, bs, int(whole[-1]), layer=y, **sc)
+    lens += 1
+    check(step(q, k, v, offs, None), [0, 1, 2, 3])
     # a captured step follows the lengths
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())

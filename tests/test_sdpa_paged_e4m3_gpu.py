@@ -32,7 +32,7 @@ class Case:
             rng, lens, new, Hkv, ps, d, pow2, **kw)
         self.Q = round_to_bf16(rng.standard_normal((self.offs[-1], H, d), dtype=np.float32)
                                * np.float32(q_scale))
-        self.lens, self.pow2 = np.asarray(lens, np.int32), pow2
+        self.lens = np.asarray(lens, np.int32)
 
     def args(self, Q=None, table=None, lens=None, offs=None):
         pick = lambda x, y: y if x is None else x
@@ -53,8 +53,8 @@ class Case:
         O, A = paged.sdpa_paged(self.Q, K, V, self.table, self.lens, self.offs, causal, scale)
         held = [p for row in self.table for p in row if p >= 0]
         bound = lambda dtype: attention_bound(
-            O, A, self.Q, K[held], 448, at(self.vs)[held].max(), self.lens.max(),
-            scale or self.Q.shape[-1] ** -0.5, dtype == BF, self.pow2)
+            O, A, self.Q, K[held], at(self.vs)[held].max(), self.lens.max(),
+            scale or self.Q.shape[-1] ** -0.5, dtype == BF)
         return O, bound
 
 
