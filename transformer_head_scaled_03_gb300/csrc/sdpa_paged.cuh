@@ -39,14 +39,15 @@ struct PagedParams {
   const int32_t* kv_len;
   const int32_t* q_offsets;
   void* O;
-  const float* k_scale;  // of a cache in 8 bits, [num_pages, kv_heads]
-  const float* v_scale;
-  int B, cols, num_pages, page_shift, kv_heads, head_tables;
+  int B, cols, num_pages, page_shift, kv_heads;
   int T, H, G, max_new, causal, out_f32, splits;
   float scale_log2;  // scale * log2(e)
   float inv_G;       // 1 / G
   unsigned* err;
   uint64_t limit_ns;
+  const float* k_scale;  // of a cache in 8 bits, [num_pages, kv_heads]
+  const float* v_scale;
+  int head_tables;       // the page table has a row for every kv head
 };
 
 // x / G for 0 <= x < 512: the quotient's fraction is a multiple of 1/G, and
@@ -57,12 +58,12 @@ __device__ __forceinline__ int div_by_group(const PagedParams& p, int x) {
 }
 
 inline PagedParams paged_params(const PagedSdpaArgs& a, const DeviceCtl& ctl) {
-  return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.k_scale,
-                     a.pages.v_scale, a.pages.B, a.pages.cols, a.pages.num_pages,
-                     a.pages.page_shift, a.pages.kv_heads, a.head_tables, a.T, a.H, a.G,
+  return PagedParams{a.pages.table, a.pages.kv_len, a.q_offsets, a.O, a.pages.B, a.pages.cols,
+                     a.pages.num_pages, a.pages.page_shift, a.pages.kv_heads, a.T, a.H, a.G,
                      a.max_new, a.causal, a.out_f32, a.splits,
                      static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634),
-                     1.f / static_cast<float>(a.G), ctl.err, ctl.limit_ns};
+                     1.f / static_cast<float>(a.G), ctl.err, ctl.limit_ns, a.pages.k_scale,
+                     a.pages.v_scale, a.head_tables};
 }
 
 // The tensor maps of Q [T, H, d], of `tokens` tokens and one group of heads

@@ -22,8 +22,7 @@ struct RowsBlock {
 // order, so long ones do not trail alone at the end; up to kMaxSorted
 // sequences, ranked by every CTA itself); in a sequence head by head (a
 // head's blocks run at about the same time and share its pages in L2), in a
-// head from the last tokens to the first, which see fewer keys.  Without
-// offsets every sequence is one token and one block, taken as they come.
+// head from the last tokens to the first, which see fewer keys.
 // The whole CTA calls this; barriers and tensor memory that were set up before
 // are visible to it afterwards.  `scratch`: shared memory, 4 * (3 *
 // kMaxSorted + 1) bytes, that the copies to follow may write over; pick: three
@@ -61,15 +60,7 @@ __device__ __forceinline__ RowsBlock rows_block(const PagedParams& p, uint8_t* s
   if (warp == 0) {
     int64_t rest = blockIdx.x / static_cast<unsigned>(p.splits);
     int found = -1, head = 0, blk = 0;
-    if (!p.q_offsets) {
-      // a token to a block: no search
-      const int b = static_cast<int>(rest / p.kv_heads);
-      if (b < p.B && seq_of(b).n > 0) {
-        found = b;
-        head = static_cast<int>(rest - static_cast<int64_t>(b) * p.kv_heads);
-      }
-    }
-    for (int b0 = 0; p.q_offsets && b0 < p.B && found < 0; b0 += 32) {
+    for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
       int seq_b = b0 + lane;
       int n = 0;
       if (seq_b < p.B) {
