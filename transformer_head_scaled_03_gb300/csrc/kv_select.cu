@@ -8,6 +8,12 @@
 // four products to an instruction, and two pages' rows of d bytes stand for
 // 2 * page_size rows of keys and values.  Exact sums make the choice, and so
 // the attention over it, the same for every order of summation.
+//
+// Bound by latency: a few dependent look-ups, then one round of loads.  Measured
+// (32 query heads on 8 kv heads, d = 128), in a graph: bounds of 2,250 pages of 32
+// rows in 8 bits 20 us (78 MB, 3.9 TB/s), of the few that a decoding step fills 3
+// us; 64 of 2,048 pages chosen for one token 8.6 us; 128 of 2,048 to 4,096 for 16
+// tokens 30 us, of which the scores (100 MB) take about 20.
 #include <stdint.h>
 
 #include <cuda_bf16.h>

@@ -18,8 +18,12 @@
 //   s_j = q . codes_j * kscale_j,  m = max s,  p_j = 2^(s_j - m),  l = sum p_j
 //   w_j = 256 p_j vscale_j / c,    o = c / 256 * sum_j w_j codes_j / l
 //
-// Half the bytes of the bf16 form for the same tiles: bound by HBM, with 16 KB
-// slots (d = 128) in the ring.
+// Half the bytes of the bf16 form for the same tiles: bound by HBM up to eight
+// rows, by the softmax's chain with more.  Measured: 16 sequences of 16 to 32 K
+// tokens, 32 heads on 8 kv heads, d = 128: 117 us, 6.9 TB/s of cache (the bf16
+// cache: 213 us); 64 heads on 8 120 us, 128 on 8 143 us (190 with the slots'
+// scales and last keys in registers, which spilled); d = 64 77 us; 64 sequences
+// of 200 to 1000 tokens 26 us; one token over 700 keys 8 us on the device.
 #include <math.h>
 #include <stdint.h>
 

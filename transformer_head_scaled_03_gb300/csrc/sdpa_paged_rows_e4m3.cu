@@ -20,6 +20,14 @@
 // loop waits for; a V tile is converted once for all 256 rows of a CTA.  With
 // the value scales multiplied in there, in bf16, the two warps took longer than
 // the softmax (55 instructions for 16 codes): 947 us for the 4,096-token chunks.
+//
+// Bound by the tensor core and the shared memory that feeds it: a product of 8-bit
+// operands reads 128 bytes a clock, all there are, and so the second part of Q is
+// a tenth of the time (603 us without it, 675 with), the conversion 4 %.
+// Measured: two sequences, 4,096 new of 8,192 tokens, 32 heads on 8, d = 128:
+// 667 us, 1.24 PFLOP/s (the bf16 cache: 570); six chunks of 90 to 444 tokens over
+// 900 to 7,800 keys, 40 heads on 8: 165 us (147); 16 new tokens each over 30 K
+// keys, four sequences: 90 us (101).
 #include <math.h>
 #include <stdint.h>
 
@@ -375,35 +383,28 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
         const uint8_t* from = gbase + C::kOffV + vs * C::kTile;
         uint8_t* to = gbase + C::kOffW + w * C::kV16Bytes + c / 4 * C::kVBlock;
         const int held = len - (j0 + j) * BN;
-        constexpr int kStep = C::kConvThreads / kPieces, kAtOnce = 2;
+        // a short loop: unrolled, its instructions push the softmax's out of the
+        // instruction cache (1,077 us for the 4,096-token chunks, fully unrolled,
+        // where two vectors at a time took 776)
 #pragma unroll 1
-        for (int r0 = 0; r0 < BN; r0 += kAtOnce * kStep) {
-          uint4 u[kAtOnce];
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            const int r = r0 + k * kStep + ct / kPieces;
-            u[k] = *reinterpret_cast<const uint4*>(from + piece_at<D>(r, c));
-            if (r >= held || v_scales[vs * kPageSlots + (r >> shift)] == 0.f)
-              u[k] = make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            const int r = r0 + k * kStep + ct / kPieces;
-            uint32_t v[8];
-            codes_to_half(u[k].x, v);
-            codes_to_half(u[k].y, v + 2);
-            codes_to_half(u[k].z, v + 4);
-            codes_to_half(u[k].w, v + 6);
-            const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]);
-            const uint4 hi = make_uint4(v[4], v[5], v[6], v[7]);
-            // keys r in rows of 128 bytes (64 columns), 16-byte pieces swizzled;
-            // lanes of the other 64 columns (the same banks) take theirs the other
-            // way round
-            uint8_t* dst = to + r * 128;
-            const int p0 = c % 4 * 2, odd = c >> 2;
-            *reinterpret_cast<uint4*>(dst + (((p0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + (((p0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
-          }
+        for (int r = ct / kPieces; r < BN; r += C::kConvThreads / kPieces) {
+          uint4 u = *reinterpret_cast<const uint4*>(from + piece_at<D>(r, c));
+          if (r >= held || v_scales[vs * kPageSlots + (r >> shift)] == 0.f)
+            u = make_uint4(0u, 0u, 0u, 0u);
+          uint32_t v[8];
+          codes_to_half(u.x, v);
+          codes_to_half(u.y, v + 2);
+          codes_to_half(u.z, v + 4);
+          codes_to_half(u.w, v + 6);
+          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]);
+          const uint4 hi = make_uint4(v[4], v[5], v[6], v[7]);
+          // keys r in rows of 128 bytes (64 columns), 16-byte pieces swizzled;
+          // lanes of the other 64 columns (the same banks) take theirs the other
+          // way round
+          uint8_t* dst = to + r * 128;
+          const int p0 = c % 4 * 2, odd = c >> 2;
+          *reinterpret_cast<uint4*>(dst + (((p0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + (((p0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(C::bWF(w)));
