@@ -83,7 +83,8 @@ int paged_resident_clusters(int threads, int smem_bytes, int splits) {
   return e.fits[splits];
 }
 
-int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes) {
+int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes,
+                         bool graded) {
   // Time in units of one 128-key tile: a CTA's tiles, its set-up and first
   // loads (4), and the merge (3).  Waves of clusters: lengths differ and long
   // sequences go first, so a partial last wave costs something between its
@@ -95,6 +96,14 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
   // sequences of 200 to 1000 tokens take 45 us with room for 1 K or 32 K tokens
   // each and 80 us with room for 128 K; 16 of 16 to 32 K take 240 us with room
   // for 32 K as for 1 M.
+  // Graded: one sequence of 2 K keys takes 16.4, 11.4, 9.0, 8.1 and 9.9 us on 1, 2,
+  // 4, 8 and 16 CTAs per head, so a merge counts for about as many tiles as
+  // the splits' binary logarithm and one, and for seven beyond eight CTAs (few
+  // such clusters fit the GPCs).
+  auto merge_of = [graded](int s) -> double {
+    if (!graded) return s > 1 ? 3 : 0;
+    return s == 1 ? 0 : s == 2 ? 1.8 : s <= 4 ? 2.7 : s <= 8 ? 3.7 : 7;
+  };
   const double tiles = static_cast<double>(capacity) / 128;
   int best = 1;
   double least = 0;
@@ -103,7 +112,7 @@ int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem
     if (fits < 1) continue;
     const double waves = static_cast<double>(blocks) / fits;
     const double cost = (waves <= 1 ? 1 : 0.5 * (ceil(waves) + waves)) *
-                        (tiles / s + 4 + (s > 1 ? 3 : 0));
+                        (tiles / s + 4 + merge_of(s));
     if (s == 1 || cost < least) {
       best = s;
       least = cost;

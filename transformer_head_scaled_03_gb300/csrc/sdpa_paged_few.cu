@@ -548,7 +548,7 @@ cudaError_t launch_impl(PagedSdpaArgs a, const DeviceCtl& ctl) {
   if (a.splits == 0)
     a.splits = paged_default_splits(
         clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads,
-        FewCfg<D, false>::kSmemBytes);
+        FewCfg<D, false>::kSmemBytes, a.head_tables);
   const bool alone =
       clusters <= paged_resident_clusters(kThreads, FewCfg<D, true>::kSmemBytes, a.splits);
   // the softmax's work per tile goes with the slots: 4, 8 or all 16 of them

@@ -637,7 +637,7 @@ cudaError_t launch_slots(PagedSdpaArgs a, const DeviceCtl& ctl) {
   if (a.splits == 0)
     a.splits = paged_default_splits(
         clusters, static_cast<int64_t>(a.pages.cols) << a.pages.page_shift, kThreads,
-        Few8Cfg<D, U, false>::kSmemBytes);
+        Few8Cfg<D, U, false>::kSmemBytes, true);
   const bool alone =
       clusters <= paged_resident_clusters(kThreads, Few8Cfg<D, U, true>::kSmemBytes, a.splits);
   return alone ? launch_as<D, U, true>(a, ctl) : launch_as<D, U, false>(a, ctl);
