@@ -152,6 +152,7 @@ SELECTS = [
     ([2000], [2], 14, 2, 16, 128, 100), ([300], [1], 128, 1, 16, 64, 7), ([300, 600], [2, 1], 33, 3, 16, 128, 9),
     ([9000], [1], 2, 1, 16, 64, 300), ([1000, 260], [1, 1], 4, 4, 256, 64, 2), ([100], [1], 4, 2, 16, 64, 50),
     ([16 * 40] * 40, [1] * 40, 2, 1, 16, 64, 6),
+    ([50000, 33], [1, 1], 2, 1, 16, 64, 40), ([16 * 9000 + 5], [1], 1, 1, 16, 64, 3000),    # thousands of pages
 ]
 
 
@@ -178,6 +179,31 @@ def test_equal_scores_go_to_the_first_pages():
     x[6][:] = 0.0            # no score at all
     want, _ = ref.select(x[0], *x[1:], 20)
     assert np.array_equal(run_select(x, 20)[0].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("pages", [700, 9000])
+def test_one_score_far_from_the_rest(pages):
+    """An outlier, infinite scores, and more equal scores than are compared with
+    one another: the search by bits."""
+    x = select_case(570, [16 * pages + 3], [1], 1, 1, 16, 64)
+    Q, ps, table, lens, offs, b, s = x
+    first = s.copy()
+    for far in (2.0 ** 100, 3e38, np.inf):
+        s[:] = first
+        s[table[0, 17], 0] = far
+        s[table[0, 400], 0] = far / 4
+        for n in (1, 2, 3, 300, pages - 5):
+            with np.errstate(invalid="ignore"):
+                want, rows = ref.select(Q, *x[1:], n)
+            sel, got = run_select(x, n)
+            assert np.array_equal(sel.cpu().numpy(), want) and np.array_equal(got.cpu().numpy(), rows)
+    b[table[0, 5:]] = b[table[0, 5]]        # and nearly all equal beside it
+    s[:] = 0.5
+    s[table[0, 3], 0] = 2.0 ** 90
+    for n in (1, 2, 5, 600, pages - 2):
+        want, rows = ref.select(Q, *x[1:], n)
+        assert np.array_equal(run_select(x, n)[0].cpu().numpy(), want)
+    assert mha.mha_check() == mha.MHA_OK
 
 
 def test_queries_of_zeros_any_size_and_not_finite():
