@@ -13,7 +13,7 @@
 // (32 query heads on 8 kv heads, d = 128), in a graph: bounds of 2,250 pages of 32
 // rows in 8 bits 20 us (78 MB, 3.9 TB/s), of the few that a decoding step fills 3
 // us; 64 of 2,048 pages chosen for one token 8.6 us; 128 of 2,048 to 4,096 for 16
-// tokens 30 us, of which the scores (100 MB) take about 20.
+// tokens 30 us (the scores read 100 MB; 25 us of them under a profiler).
 #include <stdint.h>
 
 #include <cuda_bf16.h>
@@ -301,9 +301,10 @@ __device__ __forceinline__ float heads_bound(const uint4 (*q_pos)[L], const uint
 // The warp's pages are copied to shared memory, all under way at once, in rows 16
 // bytes longer, so that the lanes' pieces lie in different banks; then each lane
 // sums up its own page's: the query heads' pieces are the same for all lanes,
-// and no sum crosses them.  (With d / 16 lanes to a page and exchanges between
-// them a round of four pages took 156 instructions.  A bulk copy per page,
-// issued lane by lane, took ten each.)
+// and no sum crosses them.  (128 of 2,048 to 4,096 pages for 16 tokens, under a
+// profiler: with d / 16 lanes to a page and exchanges between them 29 us and 15.3
+// million warp instructions, with a bulk copy per page, issued lane by lane, 27 us
+// and 12.8 million, as it is 25 us and 11.6 million.)
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps)
     kv_score_kernel(const SelectArgs a, int chunks) {

@@ -18,12 +18,13 @@
 // Weights as two e4m3 parts would spare the converting warps, but cost the
 // softmax six instructions a pair of weights instead of one, and it is what the
 // loop waits for; a V tile is converted once for all 256 rows of a CTA.  With
-// the value scales multiplied in there, in bf16, the two warps took longer than
-// the softmax (55 instructions for 16 codes): 947 us for the 4,096-token chunks.
+// the value scales multiplied in there, in bf16, the two warps then held the
+// loop up: 947 us for the 4,096-token chunks (641 without the conversion).
 //
-// Bound by the tensor core and the shared memory that feeds it: a product of 8-bit
-// operands reads 128 bytes a clock, all there are, and so the second part of Q is
-// a tenth of the time (603 us without it, 675 with), the conversion 4 %.
+// Bound by the chain softmax, P V, next scores: the tensor pipe is busy 55 % of the
+// time, and a softmax warp waits longer for its scores than it works on them.  The
+// second part of Q is a tenth of the time (603 us without it, 675 with), the
+// conversion 4 % (646).
 // Measured: two sequences, 4,096 new of 8,192 tokens, 32 heads on 8, d = 128:
 // 667 us, 1.24 PFLOP/s (the bf16 cache: 570); six chunks of 90 to 444 tokens over
 // 900 to 7,800 keys, 40 heads on 8: 165 us (147); 16 new tokens each over 30 K
@@ -701,8 +702,8 @@ cudaError_t launch_as(PagedSdpaArgs a, const DeviceCtl& ctl) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Eight pages to a tile cost 4 to 8 % of the two-tile kernels' time (chunks of 90
-// to 444 tokens, 40 heads on 8, d = 128: 175 us instead of 166), so pages of 32
+// Eight pages to a tile cost the two-tile kernels 4 to 5 % (4,096-token chunks 704
+// us instead of 674; chunks of 90 to 444 tokens 175 instead of 166), so pages of 32
 // rows or more take a kernel of their own; of the one-tile kernels, which wait
 // for memory, it is nothing.
 template <int D>
