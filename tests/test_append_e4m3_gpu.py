@@ -161,6 +161,20 @@ def test_zeros_tiny_and_not_finite_values():
     assert np.array_equal(ref.VALUES[got], ref.VALUES[wv], equal_nan=True)
 
 
+def test_zeros_behind_rows_of_the_smallest_scales():
+    """A scale below the smallest normal number has no inverse in fp32: the page
+    keeps it, and the new rows are zeros all the same."""
+    x = Append(423, [9, 20], [1, 3], 2, 2, 16, 64, 64, mha.ROPE_HALF)
+    x.v[:] = 0
+    x.vs[:] = np.float32(1e-40)
+    state = x.state()
+    x.run(state)
+    assert mha.mha_check() == mha.MHA_OK
+    wv, wvs = ref.append(x.vc, x.vs, x.v, x.table, x.lens, x.offs)
+    assert np.array_equal(to_np(state[3]), wvs.astype(np.float32))
+    assert np.array_equal(ref.VALUES[codes_of(state[1])], ref.VALUES[wv], equal_nan=True)
+
+
 @pytest.mark.parametrize("new", [1, 30])
 def test_bad_entries_touch_nothing(new):
     """A bad page or length, a position behind the table, bad offsets: those

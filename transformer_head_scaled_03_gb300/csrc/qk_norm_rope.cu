@@ -944,7 +944,8 @@ __device__ __forceinline__ void append_e4m3_unit(const PagedArgs& p, int64_t uni
     for (int k = 0; k < NW; ++k) top = fmaxf(top, tops[k]);
   }
   const float s = fmaxf(old, e4m3_scale_of(top));
-  const float inv = s > 0.f ? 1.f / s : 0.f;
+  // (a scale that was there may have no inverse: then the new rows are zeros)
+  const float inv = s > 0.f ? fminf(1.f / s, 0x1p127f) : 0.f;
   if (old > 0.f && s > old) {
     const int vecs = r0 * D / 16;
     for (int v = warp * 32 + lane; v < vecs; v += 32 * NW) {
