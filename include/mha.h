@@ -629,7 +629,8 @@ mha_status kv_pages_bounds(const mha_kv_pages *pages,
  * (a sum of max(qi_c lo_c, qi_c hi_c), as lo <= hi).
  * The sums are whole numbers, the products in fp32 in that order, so equal
  * calls select equal pages on every device.  Elements of q that are not
- * finite count as 0.
+ * finite count as 0; a product beyond fp32 is an infinity, and one of those
+ * with a bound_scale of 0 counts least.
  *   Q : bf16, T packed tokens as for sdpa_paged.
  *   bounds, bound_scale : of all the layers; `layer` picks.
  *   selected : device int32 [T, kv_heads, n_select], page numbers in the order

@@ -219,6 +219,36 @@ def test_queries_of_zeros_any_size_and_not_finite():
     assert np.array_equal(sel.cpu().numpy(), want) and np.array_equal(got.cpu().numpy(), rows)
 
 
+def test_products_beyond_fp32_are_no_bad_pages():
+    """The largest queries: products in fp32 as documented, so infinities, which
+    times a page's scale of 0 are NaN and count least."""
+    x = select_case(562, [900], [3], 2, 1, 16, 64)
+    Q, ps, table, lens, offs, b, s = x
+    Q[:] = round_to_bf16(np.sign(Q) * np.float32(2.0 ** 126) * (1 + np.abs(Q) / 8))
+    s[table[0, 3:50:5]] = 0
+    n = 12
+    sel, got = run_select(x, n)
+    assert mha.mha_check() == mha.MHA_OK
+    assert got.tolist() == [(n - 1) * ps + p % ps + 1 for p in (897, 898, 899)]
+    f = np.float32
+    with np.errstate(over="ignore", invalid="ignore"):
+        for t in range(3):
+            newest = (897 + t) // ps
+            page = table[0, :newest]
+            best = np.full(newest, -np.inf, f)
+            for h in range(2):
+                step = ref.pow2_at_least(np.abs(Q[t, h]).max(), 127.0)
+                qi = np.rint(Q[t, h] / step)
+                v = np.maximum(qi, 0) @ b[page, 0, 1].T.astype(float) \
+                    + np.minimum(qi, 0) @ b[page, 0, 0].T.astype(float)
+                best = np.maximum(best, f(v) * f(step))
+            score = best * s[page, 0].astype(f)
+            key = np.where(np.isnan(score), -np.inf, score)
+            order = sorted(range(newest), key=lambda c: (bool(np.isnan(score[c])), -key[c], c))[:n - 1]
+            assert np.isnan(score).any() and np.isinf(score).any()
+            assert sel[t, 0].tolist() == [table[0, c] for c in sorted(order)] + [table[0, newest]]
+
+
 def test_what_lies_behind_the_newest_page_is_never_used():
     """Bounds and scales of spare, partly filled and later pages, and entries
     behind the last page, may hold anything."""

@@ -263,8 +263,9 @@ __device__ __forceinline__ TokenPlace place_of(const SelectArgs& a, int t) {
 
 constexpr int kScoreWarps = 4;
 constexpr int kHeadsAtOnce = 16;  // query heads in shared memory at a time
-// the score that marks a bad page number (a NaN no product gives)
-constexpr unsigned kBadScore = 0x7fffffffu;
+// the score that marks a bad page number (a NaN that no product gives: theirs is
+// 0x7fffffff)
+constexpr unsigned kBadScore = 0xffc00001u;
 
 // 16 bytes from global to shared memory, not waited for.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -396,8 +397,8 @@ constexpr int kPickKeys = 8192;  // that stay in shared memory; those behind are
 constexpr int kStaged = 2048;    // places whose pages are looked up together at the end
 constexpr int kClose = 512;      // scores of one bin that are compared with one another
 
-// fp32 in the order of unsigned whole numbers; a NaN, which finite bounds and
-// scales never give, below all others.
+// fp32 in the order of unsigned whole numbers; a NaN (an infinity times a scale of
+// 0) below all others.
 __device__ __forceinline__ unsigned rank_key(float x) {
   const unsigned u = __float_as_uint(x);
   if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
