@@ -9,6 +9,7 @@
 //          bf16's, so both take the time of one in bf16)
 //   s    = S_t f           f = the key's page scale, the row's and the softmax's
 //   W_t  = 2^(s + v - R)   v = log2 of the value scale over the CTA's first one
+//                          above 0 (a scale of 0: 60 less than the largest so far)
 //   O_t += W_t V_codes     kind::f16, W in fp16 from TMEM, the codes in fp16
 //          (every one is exact) from shared memory, where two warps of their own
 //          write them
@@ -239,11 +240,13 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
         cur.fetch(p, row, j0 * BN, len, lane);
         nxt.fetch(p, row, (j0 + 1) * BN, n_kv > 1 ? len : 0, lane);
         scales_of(cur, sk, sv);
-        // value scales count against the first page's, so that sums stay in range
-        // whatever size they are; those of a sequence lie within 2^100 of each other
-        float first = __shfl_sync(0xffffffffu, sv, 0);
-        if (!(first > 0.f)) first = 1.f;
-        if (lane == 0) *v_first = first;
+        // value scales count against the first one above 0, so that sums stay in
+        // range whatever size they are; those of a sequence lie within 2^100 of each
+        // other.  A page of scale 0 (its codes become zeros) takes 2^-60 of the largest
+        // so far: its keys count in the sum, and do not raise R above the weights that
+        // meet values unless they outweigh those by 2^60; and 2^-72 of the largest
+        // weight is still in range.
+        float first = 0.f, most = 1.f;
         int k_issued = 0, v_issued = 0;
         for (int j = 0; j < n_kv; ++j) {
           const int ks = j % NK, vs = j % NV;
@@ -254,9 +257,19 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
           }
           const uint32_t bytes = cur.bytes(p);
           if (!mbar_wait_warp(bar(C::bKE(ks)), ((j / NK) & 1) ^ 1u, ctl)) break;
+          if (first == 0.f) {
+            const unsigned some = __ballot_sync(0xffffffffu, sv > 0.f);
+            if (some) first = __shfl_sync(0xffffffffu, sv, __ffs(some) - 1);
+          }
+          const bool none = !(sv > 0.f);
+          float ratio = none ? 1.f : fminf(fmaxf(sv / first, 0x1p-100f), 0x1p100f);
+          most = fmaxf(most, ratio);  // this lane's
+          if (__any_sync(0xffffffffu, none && cur.mine)) {
+            // (the order of numbers above 0 is that of their bits)
+            most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+            if (none) ratio = most * 0x1p-60f;
+          }
           if (lane < kPageSlots) {
-            // the codes of a page whose scale is 0 become zeros: any weight will do
-            const float ratio = sv > 0.f ? fminf(fmaxf(sv / first, 0x1p-100f), 0x1p100f) : 1.f;
             k_scales[j % C::NS * kPageSlots + lane] =
                 make_float4(sk, log2f(ratio), 1.f / ratio, 0.f);
           }
@@ -281,6 +294,7 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
         }
         __syncwarp();
         if (lane == 0) {
+          *v_first = first > 0.f ? first : 1.f;
           mbar_arrive(bar(C::bLoaded));
           // let every issued copy land before the CTA can exit
           for (int j = max(0, k_issued - NK); j < k_issued; ++j)
@@ -625,6 +639,8 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
       if (!mbar_wait_warp(bar(C::bLoaded), 0, ctl)) zero = true;
       if (*bad_page) zero = true;
     }
+    const bool some = have && l != 0.f;                // NaN stays NaN
+    const float inv_l = some ? *v_first / l : 0.f;
     if (p.splits > 1) {
       // the partial outputs go where Q and the stages were: not before every
       // product of the CTA has read them
@@ -633,24 +649,25 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
       float* xo = reinterpret_cast<float*>(gbase) + (t * kBlockM + r) * (D + 4);
       float* xm = reinterpret_cast<float*>(gbase + C::kOffM);
       if (!ok || (n_t > 0 && !have)) *bad_page = 1;  // a failed split spoils the row
-      xm[t * kBlockM + r] = have ? ref : -INFINITY;
-      xm[(NQT + t) * kBlockM + r] = have ? l : 0.f;
+      // a split's outputs are merged as they would be alone, with the logarithm of
+      // its sum: the references of splits, which hold value scales, may lie further
+      // apart than fp32 reaches
+      xm[t * kBlockM + r] = some ? ref + __log2f(l) : -INFINITY;
+      xm[(NQT + t) * kBlockM + r] = some ? 1.f : 0.f;
       if (have && warp_in_use) {
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
           tmem_ld32(tO + cb * 32, o);
           tmem_ld_wait(o);
-          const float first = *v_first;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<float4*>(xo + cb * 32 + 4 * c) =
-                make_float4(__uint_as_float(o[4 * c]) * first, __uint_as_float(o[4 * c + 1]) * first,
-                            __uint_as_float(o[4 * c + 2]) * first, __uint_as_float(o[4 * c + 3]) * first);
+                make_float4(__uint_as_float(o[4 * c]) * inv_l, __uint_as_float(o[4 * c + 1]) * inv_l,
+                            __uint_as_float(o[4 * c + 2]) * inv_l, __uint_as_float(o[4 * c + 3]) * inv_l);
         }
       }
     } else if (warp_in_use) {
-      const float inv_l = !zero && l != 0.f ? *v_first / l : 0.f;  // NaN stays NaN
       const int64_t row0 = static_cast<int64_t>(seq.q0 + i0 + t * tile_tokens) * p.H + g * p.G;
       rows_store<D>(p, tO, zero, inv_l, quarter, tile_rows, row0,
                     gbase + C::kOffQ + t * C::kQTileBytes);
