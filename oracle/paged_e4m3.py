@@ -85,7 +85,7 @@ def append(codes, scales, x, table, lengths, offsets, positions_below=None):
                     old = scales[page, g] if older else 0.0
                     fin = np.abs(rows[np.isfinite(rows)])
                     s = max(old, pow2_at_least(fin.max() if fin.size else 0.0, 448.0))
-                    if old and s > old:
+                    if older and s > old:
                         codes[page, g, :older] = encode(VALUES[codes[page, g, :older]] * (old / s))
                     codes[page, g, older:older + z - a] = encode(rows / s if s else 0 * rows)
                     scales[page, g] = s

@@ -946,7 +946,7 @@ __device__ __forceinline__ void append_e4m3_unit(const PagedArgs& p, int64_t uni
   const float s = fmaxf(old, e4m3_scale_of(top));
   // (a scale that was there may have no inverse: then the new rows are zeros)
   const float inv = s > 0.f ? fminf(1.f / s, 0x1p127f) : 0.f;
-  if (old > 0.f && s > old) {
+  if (r0 > 0 && s > old) {  // under an old scale of 0: to zeros
     const int vecs = r0 * D / 16;
     for (int v = warp * 32 + lane; v < vecs; v += 32 * NW) {
       uint4* c = reinterpret_cast<uint4*>(to) + v;
