@@ -37,6 +37,13 @@ __device__ __forceinline__ float step_of(float x) {
   return __uint_as_float(static_cast<unsigned>(e + 127) << 23);
 }
 
+// Whether a sequence's offsets are bad, or its length for the new tokens they say.
+__device__ __forceinline__ bool bad_sequence(const PagesView& pg, int T, int q0, int q1, int len) {
+  const int n = q1 - q0;
+  return q0 < 0 || q1 < q0 || q1 > T ||
+         (n > 0 && (len < n || len > (static_cast<int64_t>(pg.cols) << pg.page_shift)));
+}
+
 // ---------------------------------------------------------------------- bounds
 
 struct BoundsArgs {
@@ -62,8 +69,7 @@ __device__ __forceinline__ bool full_page_of(const BoundsArgs& a, int rest, bool
     if (b < pg.B) {
       const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1);
       const int len = __ldg(pg.kv_len + b), n = q1 - q0;
-      const bool bad = q0 < 0 || q1 < q0 || q1 > a.T ||
-                       (n > 0 && (len < n || len > (static_cast<int64_t>(pg.cols) << pg.page_shift)));
+      const bool bad = bad_sequence(pg, a.T, q0, q1, len);
       if (bad && report) atomicOr(a.err, kErrPages);
       if (!bad && n > 0) {
         first = (len - n) >> pg.page_shift;
@@ -437,6 +443,14 @@ __global__ void __launch_bounds__(kThreads) kv_pick_kernel(const SelectArgs a) {
   bool bad = w.state < 0;
   bins[threadIdx.x] = 0;
   if (threadIdx.x == 0) found[2] = 0;
+  // no token need resolve to a sequence whose offsets descend: the first block
+  // looks at all of them, while the scores are computed
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < pg.B; b += kThreads)
+      if (bad_sequence(pg, a.T, __ldg(a.q_offsets + b), __ldg(a.q_offsets + b + 1),
+                       __ldg(pg.kv_len + b)))
+        atomicOr(a.err, kErrPages);
+  }
   pdl_wait();
   if (w.state == 1 && newest < a.n_select) {
     // every page there is
