@@ -807,6 +807,28 @@ __device__ __forceinline__ float finite_max(const float2 (&v)[4]) {
   return m;
 }
 
+// q, a number rounded to fp32 that is to be rounded again, to e4m3, and what it
+// is short of the exact one (its sign counts): where the first rounding has landed
+// on a tie of the second, a unit of it towards the exact number keeps the second
+// from taking that for a tie.  A tie has five significant bits at most.
+__device__ __forceinline__ float off_tie(float q, float rest) {
+  const unsigned u = __float_as_uint(q);
+  if (rest == 0.f || (u & 0x7ffffu) || (u << 1) == 0u) return q;
+  return __uint_as_float((rest > 0.f) == (q > 0.f) ? u + 1u : u - 1u);
+}
+
+// v / s for a scale that is no power of two, as far as rounding it to e4m3 tells
+// (inv: 1 / s, rounded).
+__device__ __forceinline__ void divide(float2 (&v)[4], float s, float inv) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& x = i & 1 ? v[i / 2].y : v[i / 2].x;
+    const float q0 = x * inv;
+    const float q = fmaf(fmaf(-q0, s, x), inv, q0);
+    x = off_tie(copysignf(q, x), fmaf(-q, s, x));
+  }
+}
+
 // Sixteen codes times r.
 __device__ __forceinline__ uint4 rescale16(uint4 u, float r) {
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -817,7 +839,8 @@ __device__ __forceinline__ uint4 rescale16(uint4 u, float r) {
     for (int k = 0; k < 2; ++k) {
       const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
           static_cast<__nv_fp8x2_storage_t>(w[i] >> (16 * k) & 0xffffu), __NV_E4M3)));
-      o |= e4m3x2(f.x * r, f.y * r) << (16 * k);
+      const float x = f.x * r, y = f.y * r;
+      o |= e4m3x2(off_tie(x, fmaf(f.x, r, -x)), off_tie(y, fmaf(f.y, r, -y))) << (16 * k);
     }
     w[i] = o;
   }
@@ -953,10 +976,17 @@ __device__ __forceinline__ void append_e4m3_unit(const PagedArgs& p, int64_t uni
       *c = rescale16(*c, old * inv);
     }
   }
-  auto put = [&](int row, const float2 (&a)[4], const float2 (&b)[4]) {
+  // products with the inverse are exact but for a scale that the append did not make
+  const bool uneven = __float_as_uint(s) & 0x7fffffu;
+  auto put = [&](int row, float2 (&a)[4], float2 (&b)[4]) {
     if (row >= r1) return;
-    store8_e4m3(to + row * D + at.a, a, inv);
-    store8_e4m3(to + row * D + at.b, b, inv);
+    if (uneven) {
+      divide(a, s, inv);
+      divide(b, s, inv);
+    }
+    const float by = uneven ? 1.f : inv;
+    store8_e4m3(to + row * D + at.a, a, by);
+    store8_e4m3(to + row * D + at.b, b, by);
   };
 #pragma unroll
   for (int k = 0; k < kKept; ++k)
