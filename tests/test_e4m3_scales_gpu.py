@@ -15,6 +15,7 @@ import oracle.paged as paged
 import oracle.paged_e4m3 as ref
 import transformer_head_scaled_03_gb300 as mha
 from transformer_head_scaled_03_gb300 import build as mha_build
+from transformer_head_scaled_03_gb300.inputs import round_to_bf16
 from tests.gpu_util import to_np
 from tests.test_sdpa_paged_e4m3_gpu import Case
 
@@ -77,7 +78,7 @@ def test_large_values_of_little_weight_and_a_page_of_zeros(new, d, ps, splits):
     """The first page's values are 2^34 times the others', and its keys such that
     they hardly count; a later page's scale is 0."""
     x = Case(901, [400], [new], 4, 2, ps, d)
-    x.Q[...] = np.abs(x.Q) / 2 + 0.5
+    x.Q[...] = round_to_bf16(np.abs(x.Q) / 2 + 0.5)
     first = x.table[0, 0]
     x.kc[first], x.ks[first] = ref.encode(-448.0), 2.0 ** -7
     x.vs[first] *= 2.0 ** 34
@@ -101,3 +102,22 @@ def test_zeros_under_a_scale_of_zero_keep_their_weight(new, d, ps, splits):
     check(x.run(out_dtype=F32, max_new=new, num_splits=splits), expected(x, 2.0 ** -31), f"{new} {d}, a third")
     x.vs[pages] = 0
     assert torch.all(x.run(out_dtype=F32, max_new=new, num_splits=splits) == 0)
+
+
+@pytest.mark.parametrize("new,d,ps,splits", TILES)
+@pytest.mark.parametrize("faint", [False, True])
+def test_zeros_first_and_large_values_late(new, d, ps, splits, faint):
+    """Two key tiles of scale 0, then values 2^90 apart; or one whose values are
+    the smaller ones under keys that hardly count, and then the larger ones."""
+    x = Case(903, [700], [new], 4, 2, ps, d)
+    x.Q[...] = round_to_bf16(np.abs(x.Q) / 2 + 0.5)
+    pages = x.table[0, :-(-700 // ps)]
+    zeros, small = pages[:256 // ps], pages[256 // ps:384 // ps] if faint else pages[256 // ps::2]
+    x.vs[pages] *= 2.0 ** 45
+    x.vs[small] *= 2.0 ** -90
+    x.vs[zeros] = 0
+    if faint:
+        x.kc[small], x.ks[small] = ref.encode(-448.0), 2.0 ** -6
+    scale = 8.0 / d
+    check(x.run(out_dtype=F32, max_new=new, num_splits=splits, scale=scale),
+          expected(x, 2.0 ** -31, scale), f"{new} {d}")

@@ -574,9 +574,12 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
         }
         float alpha = 1.f;
         if (mt > ref && (ref == -INFINITY || mt - ref > kHead + kRescaleLog2)) {
-          alpha = ex2_approx(ref - (mt - kHead));  // 0 when ref = -inf
+          // 0 when ref = -inf; in two steps for l, which keys of scale 0 may have
+          // made as large as the reference moves beyond fp32
+          const float half = ex2_approx(0.5f * (ref - (mt - kHead)));
+          alpha = half * half;
           ref = mt - kHead;
-          l *= alpha;
+          l = l * half * half;
         }
         // Rescale the partial output when the reference moved.  P.V of the
         // previous tile is complete: it was issued before this tile's S,
