@@ -378,10 +378,12 @@ mha_status sdpa_paged(const void *Q, int64_t q_token_stride,
  * keys' codes as two e4m3 parts, which together are off by at most 2^-18 of
  * the row's largest element.  The weights, times the values' scales, meet the
  * values' codes as two e4m3 parts (up to 16 rows, see max_new: off by 2^-8 of a
- * weight, or 2^-23 of the largest weight times the largest scale) or in fp16
- * (more rows: off by 2^-11 of a weight, or 2^-31 of the largest product of
- * weight and scale; the value scales of one sequence, but for zeros, lie
- * within 2^100 of each other).  An infinity in a query gives NaN in its row.
+ * weight, or 2^-23 of the row's largest product of weight and scale) or in
+ * fp16 (more rows: off by 2^-11 of a weight, or 2^-31 of that product).  A key
+ * whose scale is 0 counts in that product with 2^-30 of the others' (up to 16
+ * rows) or 2^-60.  The value scales of one sequence, but for zeros, lie within
+ * 2^100 of each other, 2^70 where some are 0.  An infinity in a query gives
+ * NaN in its row.
  */
 mha_status sdpa_paged_e4m3(const void *Q, int64_t q_token_stride,
                            const mha_kv_pages *pages,

@@ -121,3 +121,50 @@ def test_zeros_first_and_large_values_late(new, d, ps, splits, faint):
     scale = 8.0 / d
     check(x.run(out_dtype=F32, max_new=new, num_splits=splits, scale=scale),
           expected(x, 2.0 ** -31, scale), f"{new} {d}")
+
+
+FEW = [(1, 64, 16, 1), (1, 128, 64, 1), (2, 128, 16, 4), (4, 64, 32, 3), (8, 128, 16, 1), (3, 64, 64, 7)]
+
+
+@pytest.mark.parametrize("new,d,ps,splits", FEW)
+@pytest.mark.parametrize("seed", range(3))
+def test_few_rows_hold_weights_against_their_own_products(new, d, ps, splits, seed):
+    """Values 2^34 times the others' under keys that hardly count, in the first
+    page, the last full one, or a page that only the newest token sees."""
+    n = 400 if seed < 2 else 384 - ps + 1
+    x = Case(910 + seed, [n], [new], 4, 2, ps, d)
+    x.Q[...] = round_to_bf16(np.abs(x.Q) / 2 + 0.5)
+    pages = x.table[0, :-(-n // ps)]
+    far = [pages[0], pages[-2], pages[-1]][seed]
+    if seed < 2:
+        x.kc[far], x.ks[far] = ref.encode(-448.0), 2.0 ** -7
+    x.vs[far] *= 2.0 ** 34
+    x.vs[pages[3]] = 0
+    scale = 8.0 / d
+    check(x.run(out_dtype=F32, max_new=new, num_splits=splits, scale=scale),
+          expected(x, 2.0 ** -23, scale), f"{new} {d}")
+
+
+@pytest.mark.parametrize("new,d,ps,splits", FEW)
+@pytest.mark.parametrize("faint", [None, False, True])
+def test_few_rows_count_zeros_like_any_keys(new, d, ps, splits, faint):
+    """Half the pages of scale 0; or the first two key tiles, then values 2^90
+    apart, the smaller ones under keys that hardly count or not."""
+    x = Case(913, [700], [new], 4, 2, ps, d)
+    x.Q[...] = round_to_bf16(np.abs(x.Q) / 2 + 0.5)
+    pages = x.table[0, :-(-700 // ps)]
+    if faint is None:
+        x.vs[pages[1::4]] *= 2.0 ** 90
+        x.vs[pages[::2]] = 0
+    else:
+        small = pages[256 // ps:384 // ps] if faint else pages[256 // ps::2]
+        x.vs[pages] *= 2.0 ** 45
+        x.vs[small] *= 2.0 ** -90
+        x.vs[pages[:256 // ps]] = 0
+        if faint:
+            x.kc[small], x.ks[small] = ref.encode(-448.0), 2.0 ** -6
+    scale = 8.0 / d
+    check(x.run(out_dtype=F32, max_new=new, num_splits=splits, scale=scale),
+          expected(x, 2.0 ** -23, scale), f"{new} {d}")
+    x.vs[:] = 0
+    assert torch.all(x.run(out_dtype=F32, max_new=new, num_splits=splits) == 0)

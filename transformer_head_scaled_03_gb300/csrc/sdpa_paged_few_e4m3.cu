@@ -12,11 +12,13 @@
 // two e4m3 parts (ptx_e4m3.cuh), which lie side by side on the products' N
 // side, 2 U columns for U query slots: a row of Q over a power of two that
 // brings its largest element to 224..448, and the weights.  A page's key scale
-// multiplies its scores, a thread's own; its value scale multiplies the
-// weights, over the largest value scale that the CTA has met (c), which is
-// carried like the running maximum:
-//   s_j = q . codes_j * kscale_j,  m = max s,  p_j = 2^(s_j - m),  l = sum p_j
-//   w_j = 256 p_j vscale_j / c,    o = c / 256 * sum_j w_j codes_j / l
+// multiplies its scores, a thread's own; its value scale v joins the score, over
+// one value scale c of the CTA, so that a weight's parts are held against the
+// largest product of weight and value scale of its own row:
+//   t_j = q . codes_j * kscale_j + log2(v_j / c),   m = max t
+//   w_j = 256 * 2^(t_j - m),  l = sum w_j c / v_j,  o = c * sum_j w_j codes_j / l
+// A key whose value scale is 0 meets no values (its w is 0): it is in l, and in m as if
+// its scale were 2^-30 c, which keeps l in range.
 //
 // Half the bytes of the bf16 form for the same tiles: bound by HBM up to eight
 // rows, by the softmax's chain with more.  Measured: 16 sequences of 16 to 32 K
@@ -333,6 +335,16 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
       sv = good ? __ldg(p.v_scale + at) : 0.f;
     };
     int page = page_of(0), page1 = page_of(1);
+    // c: the largest value scale of the first tile that has one above 0, from the
+    // warps' largest, which are handed over with other things
+    float c = 0.f;
+    auto largest_of_warps = [](const float* at) {
+      at += kSlots;
+      return fmaxf(fmax3(at[0], at[C::kRedRow], at[2 * C::kRedRow]), at[3 * C::kRedRow]);
+    };
+    float* lsum = red + 2 * 4 * C::kRedRow;
+    float sk, sv;
+    scales_of(page, sk, sv);
 
     if (T > 0) {
       // Q as two parts: eight threads to a row, D / 8 columns each
@@ -403,10 +415,11 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(C::bQ));
+      const float wc = warp_max_f32(sv);
+      if (lane == 0) lsum[warp * C::kRedRow + kSlots] = wc;
       softmax_bar();  // the rows' scales are there
+      c = largest_of_warps(lsum);
     }
-    float sk, sv;
-    scales_of(page, sk, sv);
 
     float m[U], l[U], acc[U], alpha_prev[U];
 #pragma unroll
@@ -416,7 +429,6 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
       acc[q] = 0.f;
       alpha_prev[q] = 1.f;
     }
-    float c = 0.f;  // the largest value scale so far
     // keys that every slot sees (one not in use may see any: its sums are not
     // stored)
     const int all_see = p.causal ? len - seq.n + 1 : len;
@@ -431,6 +443,12 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
       float sk1, sv1;
       scales_of(page1, sk1, sv1);
       page1 = page_of(j + 2);
+      float* rb = red + buf * 4 * C::kRedRow;
+      // value scales of a sequence, but for zeros, lie within 2^100 of each other
+      const bool none = !(sv > 0.f);
+      const float ratio = none ? 0x1p-30f : fminf(fmaxf(sv / c, 0x1p-100f), 0x1p100f);
+      const float v = __log2f(ratio), iv = ex2_approx(-v);
+      const float times = none ? 0.f : kWTop;
       if (!(ok = mbar_wait_warp(bar(C::bS(buf)), par, ctl))) break;
       tc_fence_after();
       float s[U];
@@ -443,37 +461,33 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
           const float qs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            s[q + k] = fmaf(__uint_as_float(sr[U + q + k]), 1.f / kQUp, __uint_as_float(sr[q + k])) *
-                       (sk * qs[k]);
+            s[q + k] = fmaf(
+                fmaf(__uint_as_float(sr[U + q + k]), 1.f / kQUp, __uint_as_float(sr[q + k])),
+                sk * qs[k], v);
         }
         if ((t_begin + j + 1) * kKeys > all_see) {
 #pragma unroll
           for (int q = 0; q < U; ++q) s[q] = key <= last_key[q] ? s[q] : -INFINITY;
         }
       }
-      float* rb = red + buf * 4 * C::kRedRow;
       {
         float wm[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) wm[q] = warp_max_f32(s[q]);
-        const float wc = warp_max_f32(sv);
         if (lane == 0) {
           float4* dst = reinterpret_cast<float4*>(rb + warp * C::kRedRow);
 #pragma unroll
           for (int i = 0; i < U / 4; ++i)
             dst[i] = make_float4(wm[4 * i], wm[4 * i + 1], wm[4 * i + 2], wm[4 * i + 3]);
-          rb[warp * C::kRedRow + kSlots] = wc;
+        }
+        if (c == 0.f) {  // the same for every thread: the next tile's
+          const float wc = warp_max_f32(sv1);
+          if (lane == 0) rb[warp * C::kRedRow + kSlots] = wc;
         }
       }
       mbar_arrive(bar(C::bRed(buf)));
       if (!(ok = mbar_wait_warp(bar(C::bRed(buf)), par, ctl))) break;
-      const float c_new =
-          fmaxf(c, fmaxf(fmax3(rb[kSlots], rb[C::kRedRow + kSlots], rb[2 * C::kRedRow + kSlots]),
-                         rb[3 * C::kRedRow + kSlots]));
-      // the partial outputs are sums of weights over c
-      const float shrink = c == c_new ? 1.f : c / c_new;
-      const float up = c_new > 0.f ? sv / c_new * kWTop : 0.f;
-      c = c_new;
+      if (c == 0.f) c = largest_of_warps(rb);
       float alpha[U];
 #pragma unroll
       for (int i = 0; i < U / 4; ++i) {
@@ -492,10 +506,9 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
           const float at = mn == -INFINITY ? 0.f : mn;  // a slot with no visible key yet
           alpha[q] = ex2_approx(m[q] - at);
           const float pq = ex2_approx(s[q] - at);
-          l[q] = fmaf(l[q], alpha[q], pq);
+          l[q] = fmaf(pq, iv, l[q] * alpha[q]);
           m[q] = mn;
-          s[q] = pq * up;
-          alpha[q] *= shrink;
+          s[q] = pq * times;
         }
       }
       // W^T(j): rows q (first parts) and U + q (second), key r, 128-byte swizzle
@@ -563,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
 #pragma unroll
       for (int sh = 16; sh > 0; sh >>= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], sh);
     }
-    float* lsum = red + 2 * 4 * C::kRedRow;
     if (lane == 0) {
       float4* dst = reinterpret_cast<float4*>(lsum + warp * C::kRedRow);
 #pragma unroll
@@ -573,21 +585,28 @@ __global__ void __launch_bounds__(kThreads, Few8Cfg<D, U, kAlone>::kCtas)
     softmax_bar();
     const bool failed = *abort_flag != 0;
     if (failed) *bad_page = 1;  // a failed split spoils the rows
+    auto sum_of = [&](int q) {
+      return lsum[q] + lsum[C::kRedRow + q] + lsum[2 * C::kRedRow + q] + lsum[3 * C::kRedRow + q];
+    };
+    // a split's outputs are merged as they would be alone, with the logarithm of its
+    // sum: the maxima of splits, which hold value scales, may lie further apart than
+    // fp32 reaches
     if (threadIdx.x < kSlots) {
       const int q = threadIdx.x;
-      const bool none = failed || q >= U;
       float mq = -INFINITY;
 #pragma unroll
       for (int k = 0; k < U; ++k) mq = k == q ? m[k] : mq;
-      xm[q] = none ? -INFINITY : mq;
-      xl[q] = none ? 0.f
-                   : lsum[q] + lsum[C::kRedRow + q] + lsum[2 * C::kRedRow + q] +
-                         lsum[3 * C::kRedRow + q];
+      const float sum = failed || q >= U ? 0.f : sum_of(q);
+      xm[q] = sum != 0.f ? mq + __log2f(sum) : -INFINITY;  // NaN stays NaN
+      xl[q] = sum != 0.f ? 1.f : 0.f;
     }
     if (o_rows && r < D) {
       const float back = c * (1.f / kWTop);
 #pragma unroll
-      for (int q = 0; q < U; ++q) xo[q * D + r] = acc[q] * back;
+      for (int q = 0; q < U; ++q) {
+        const float sum = sum_of(q);
+        xo[q * D + r] = sum != 0.f ? acc[q] * (back / sum) : 0.f;
+      }
     }
   }
 
