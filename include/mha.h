@@ -510,7 +510,7 @@ mha_status qk_norm_rope_paged(const void *Q, int64_t q_token_stride,
  * (x / s below 2^-6).  "Older" are the sequence's rows of that page ahead of
  * its new ones; what lies behind its length is not touched.  x is the normed,
  * rotated key or the value in fp32; elements that are not finite are stored
- * as NaN.
+ * as NaN, and are NaN under a scale of 0, too.
  */
 mha_status qk_norm_rope_paged_e4m3(
     const void *Q, int64_t q_token_stride, const void *K,

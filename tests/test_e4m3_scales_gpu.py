@@ -17,6 +17,7 @@ import transformer_head_scaled_03_gb300 as mha
 from transformer_head_scaled_03_gb300 import build as mha_build
 from transformer_head_scaled_03_gb300.inputs import round_to_bf16
 from tests.gpu_util import to_np
+from tests.paged_util import i32
 from tests.test_sdpa_paged_e4m3_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -168,3 +169,33 @@ def test_few_rows_count_zeros_like_any_keys(new, d, ps, splits, faint):
           expected(x, 2.0 ** -23, scale), f"{new} {d}")
     x.vs[:] = 0
     assert torch.all(x.run(out_dtype=F32, max_new=new, num_splits=splits) == 0)
+
+
+@pytest.mark.parametrize("new,d,ps,splits", FEW + TILES)
+def test_values_that_are_not_finite_beside_zeros_show(new, d, ps, splits):
+    """A page of zeros but for an infinity, which the append stores as NaN under a
+    scale of 0: its column is NaN in whatever sees it, and no other is."""
+    x = Case(920, [400], [new], 4, 2, ps, d)
+    held = [x.table[0, 0], x.table[0, 2]]
+    rows = torch.zeros((3 * ps, 2, d), dtype=torch.bfloat16, device="cuda")
+    ones, pe = torch.ones(d, dtype=torch.bfloat16, device="cuda"), mha.sinusoidal_pe(3 * ps, d)
+    rows[ps:2 * ps] = 1.0
+    outs = []
+    for bad in (0.0, float("inf")):
+        rows[2 * ps + 3, 1, 7] = bad
+        Q, K, V, table, lens, offs = x.args()
+        sc = x.scales()
+        mha.qk_norm_rope_paged(rows.repeat(1, 2, 1), rows, rows, ones, ones, pe, K, V, table,
+                               i32([3 * ps]), i32([0, 3 * ps]), **sc)
+        assert torch.all(sc["V_scale"][held] == 0)
+        # the values of the append beside the keys of before
+        K, sc["K_scale"] = x.args()[1], x.scales()["K_scale"]
+        outs.append(to_np(mha.sdpa_paged(Q, K, V, table, lens, offs, max_new=new, num_splits=splits,
+                                         out_dtype=F32, **sc)))
+        assert mha.mha_check() == mha.MHA_OK
+    clean, got = outs
+    assert np.all(np.isfinite(clean))
+    first = max(0, 2 * ps + 3 - (400 - new))           # the first token that sees the key
+    assert first < new and np.all(np.isnan(got[first:, 2:, 7]))
+    got[:, 2:, 7] = clean[:, 2:, 7]
+    assert np.array_equal(got, clean)

@@ -122,6 +122,12 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t* v) {
     v[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
+
+// Four codes times 0: `nan` where they are NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w, uint32_t nan) {
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * nan;
+}
+
 // Not to be kept in registers from one use to the next.
 __device__ __forceinline__ float4 lds_f32x4(uint32_t at) {
   float4 v;
@@ -386,7 +392,8 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
       // ------------------------------------------------- value tiles to fp16
       // A thread takes 16 codes of a key at a time: 16 bytes in, two pieces of 16
       // bytes out.  Rows behind the length hold anything, NaN too, and become
-      // zeros, where 0 * NaN would reach the sums; so do codes of scale 0.
+      // zeros, where 0 * NaN would reach the sums; so do codes of scale 0 but
+      // for NaN, which an append may have stored beside zeros.
       const int ct = threadIdx.x - 32 * C::kConvWarp;
       constexpr int kPieces = D / 16;  // of a row of codes
       const int c = ct % kPieces;
@@ -404,8 +411,13 @@ __global__ void __launch_bounds__(Rows8Cfg<D, NQT, NK, NV, BN, kCtas>::kThreads,
 #pragma unroll 1
         for (int r = ct / kPieces; r < BN; r += C::kConvThreads / kPieces) {
           uint4 u = *reinterpret_cast<const uint4*>(from + piece_at<D>(r, c));
-          if (r >= held || v_scales[vs * kPageSlots + (r >> shift)] == 0.f)
-            u = make_uint4(0u, 0u, 0u, 0u);
+          if (r >= held || v_scales[vs * kPageSlots + (r >> shift)] == 0.f) {
+            const uint32_t nan = r < held ? 0x7fu : 0u;
+            u.x = nan_codes(u.x, nan);
+            u.y = nan_codes(u.y, nan);
+            u.z = nan_codes(u.z, nan);
+            u.w = nan_codes(u.w, nan);
+          }
           uint32_t v[8];
           codes_to_half(u.x, v);
           codes_to_half(u.y, v + 2);
