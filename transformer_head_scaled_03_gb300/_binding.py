@@ -758,6 +758,9 @@ def kv_pages_bounds(K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds,
            "kv_pages_bounds")
 
 
+_SMALL_WORKSPACE = 8 << 20   # an allocation more costs a call 4 us
+
+
 def kv_pages_select(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, bounds, bound_scale,
                     n_select: int, layer: int = 0, out=None, workspace=None, stream=None,
                     K_scale=None, V_scale=None):
@@ -786,17 +789,20 @@ def kv_pages_select(Q, K_pages, V_pages, page_table, kv_lengths, q_offsets, boun
     n = T * Hkv * n_select
     need = dev.kv_pages_select_workspace_bytes(T, Hkv, pages.table_cols) if workspace is None else 0
     if out is None:
-        # one allocation: the two tables, and the workspace behind them
+        # one allocation: the two tables, and a small workspace behind them (a large
+        # one would be held as long as they are)
+        small = need if need <= _SMALL_WORKSPACE else 0
         at = -(-(n + T) // 4) * 4
-        own = _new(stream, (at + need // 4,), torch.int32, Q.device)
+        own = _new(stream, (at + small // 4,), torch.int32, Q.device)
         out = own.as_strided((T, Hkv, n_select), (Hkv * n_select, n_select, 1)), own.narrow(0, n, T)
         ws, size = own.data_ptr() + 4 * at, need
     else:
+        small = 0
         _int32("selected", out[0], T, Hkv, n_select)
         _int32("lengths", out[1], T)
-        if workspace is None:
-            own = _new(stream, (need or 16,), torch.uint8, Q.device)
-            ws, size = own.data_ptr(), need
+    if workspace is None and not small:
+        own = _new(stream, (need or 16,), torch.uint8, Q.device)
+        ws, size = own.data_ptr(), need
     if workspace is not None:
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = dev.kv_pages_select(Q.data_ptr(), q_ts, pages, layer, q_offsets.data_ptr(), bounds.data_ptr(),
