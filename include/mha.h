@@ -375,15 +375,17 @@ mha_status sdpa_paged(const void *Q, int64_t q_token_stride,
 /*
  * sdpa_paged_e4m3 -- sdpa_paged over a cache in 8 bits.  Q is bf16; the rest is
  * as for sdpa_paged, but for the products' operands.  A query row meets the
- * keys' codes as two e4m3 parts, which together are off by at most 2^-18 of
- * the row's largest element.  The weights, times the values' scales, meet the
- * values' codes as two e4m3 parts (up to 16 rows, see max_new: off by 2^-8 of a
- * weight, or 2^-23 of the row's largest product of weight and scale) or in
- * fp16 (more rows: off by 2^-11 of a weight, or 2^-31 of that product).  A key
- * whose scale is 0 counts in that product with 2^-30 of the others' (up to 16
- * rows) or 2^-60.  The value scales of one sequence, but for zeros, lie within
- * 2^100 of each other, 2^70 where some are 0.  An infinity in a query gives
- * NaN in its row.
+ * keys' codes as two e4m3 parts, which together are off by at most 2^-17 of
+ * the row's largest element (2^-21 with up to 16 rows, see max_new).  The
+ * weights, times the values' scales, meet the values' codes as two e4m3 parts
+ * (up to 16 rows: off by 2^-8 of a weight, or 2^-23 of the row's largest
+ * product of weight and scale) or in fp16 (more rows: off by 2^-11 of a weight,
+ * or 2^-31 of that product).  A key whose scale is 0 counts in that product
+ * with 2^-30 of the others' (up to 16 rows) or 2^-60.  The value scales of one sequence, but for zeros, lie within 2^100 of each
+ * other, 2^70 where some are 0.  An infinity in a query gives NaN in its row.
+ * Half the bytes make single tokens over long caches up to twice as fast as
+ * sdpa_paged; chunks of hundreds of new tokens and more, which the products and
+ * the softmax bound, take up to a fifth longer.
  */
 mha_status sdpa_paged_e4m3(const void *Q, int64_t q_token_stride,
                            const mha_kv_pages *pages,
@@ -642,8 +644,8 @@ mha_status kv_pages_bounds(const mha_kv_pages *pages,
  *       where an entry is bad (selected then holds -1).
  *   workspace : device, 16-byte aligned, at least
  *       kv_pages_select_workspace_bytes(...) bytes; one call's at a time.
- * The pools are not read: of *pages num_pages, page_size, kv_heads, d, layers
- * and the tables count.  d is 64 or 128, H / kv_heads <= 128, 1 <= n_select <=
+ * The pools are not read (their pointers are checked as anywhere): of *pages
+ * num_pages, page_size, kv_heads, d, layers and the tables count.  d is 64 or 128, H / kv_heads <= 128, 1 <= n_select <=
  * 65536.
  * Checked on the device (MHA_ERR_DEVICE): kv_lengths[b] in [n_b,
  * table_cols*page_size], the page numbers a token sees, offsets ascending in
@@ -667,7 +669,8 @@ size_t kv_pages_select_workspace_bytes(int T, int kv_heads, int table_cols);
  * selected[t, g, :], which kv_pages_select has filled (any table of that
  * layout will do).
  *   Q, O, H, scale, layer, out_dtype, num_splits : as for sdpa_paged.
- *   pages : the pools; its tables are not used.
+ *   pages : the pools; its tables are not used (checked as anywhere: with B = 0
+ *       and table_cols = 1 there need be none).
  *   scales : of a cache in 8 bits (dtype MHA_E4M3, whose operands are as in
  *       sdpa_paged_e4m3); NULL for MHA_BF16.
  *   selected : device int32 [T, kv_heads, n_select]; lengths : device int32

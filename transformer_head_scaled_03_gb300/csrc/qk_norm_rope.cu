@@ -29,7 +29,7 @@
 // bytes' time: two bytes a lane, and x read twice; with d = 256 616 and 1,584
 // us, 4 to 6 times.  Appending 8,262 tokens of 32 + 8 + 8 heads: 48 us (203 MB,
 // 4.2 TB/s: a row is loaded, computed and stored before the next is requested);
-// four tokens: 3 us.  Into pages of 8 bits, 10,000 tokens: 44 us (228 MB, 5.2
+// four tokens: 3 us.  Into pages of 8 bits, 10,000 tokens: 44.5 us (228 MB, 5.1
 // TB/s; the queries alone 33 us, a token to a warp); four tokens: 3.2 us.
 #include <math.h>
 #include <stdint.h>

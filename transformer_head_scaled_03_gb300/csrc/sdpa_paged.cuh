@@ -349,8 +349,9 @@ cudaError_t paged_kernel_attributes(const void* kernel, int smem_bytes,
 int paged_resident_clusters(int threads, int smem_bytes, int splits);
 
 // Split count for `blocks` blocks over sequences of up to `capacity` keys.
-// graded: the merge's cost grows with the splits (the calls on pages in 8 bits
-// and on selected pages; the others keep the choices they were measured with).
+// graded: the merge's cost grows with the splits (the few-rows forms over pages in
+// 8 bits and over selected pages; the others, query tiles in 8 bits among them,
+// keep the choices they were measured with).
 int paged_default_splits(int64_t blocks, int64_t capacity, int threads, int smem_bytes,
                          bool graded = false);
 

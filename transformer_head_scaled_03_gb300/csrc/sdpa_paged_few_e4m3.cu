@@ -22,10 +22,13 @@
 //
 // Half the bytes of the bf16 form for the same tiles: bound by HBM up to eight
 // rows, by the softmax's chain with more.  Measured: 16 sequences of 16 to 32 K
-// tokens, 32 heads on 8 kv heads, d = 128: 117 us, 6.9 TB/s of cache (the bf16
-// cache: 213 us); 64 heads on 8 120 us, 128 on 8 143 us (190 with the slots'
-// scales and last keys in registers, which spilled); d = 64 77 us; 64 sequences
-// of 200 to 1000 tokens 26 us; one token over 700 keys 8 us on the device.
+// tokens, 32 heads on 8 kv heads, d = 128: 118 us, 6.8 TB/s of cache (the bf16
+// cache: 215 us); 64 heads on 8 121 us, 128 on 8 144 us (190 with the slots'
+// scales and last keys in registers, which spilled); d = 64 78 us; 64 sequences
+// of 200 to 1000 tokens 26 us; one token over 700 keys 7.5 us on the device.
+// Keys of scale 0 let m down by 60 instead of 30 and l carried in two steps, which
+// would allow for value scales 2^100 apart beside zeros, too, took 154 us with 128
+// heads.
 #include <math.h>
 #include <stdint.h>
 

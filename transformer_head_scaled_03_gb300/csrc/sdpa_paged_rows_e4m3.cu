@@ -11,25 +11,26 @@
 //   W_t  = 2^(s + v - R)   v = log2 of the value scale over the CTA's first one
 //                          above 0 (a scale of 0: 60 less than the largest so far)
 //   O_t += W_t V_codes     kind::f16, W in fp16 from TMEM, the codes in fp16
-//          (every one is exact) from shared memory, where two warps of their own
-//          write them
+//          (every one is exact) from shared memory, where warps of their own
+//          write them: four beside two query tiles, two beside one
 //   l   += sum 2^(s - R) = sum W_t 2^-v, page by page
 // R is the running maximum of s + v less kHead, so that a weight has room below
 // it: fp16 is off by 2^-11 of a weight, or 2^-25 below 2^-14.
 // Weights as two e4m3 parts would spare the converting warps, but cost the
 // softmax six instructions a pair of weights instead of one, and it is what the
 // loop waits for; a V tile is converted once for all 256 rows of a CTA.  With
-// the value scales multiplied in there, in bf16, the two warps then held the
+// the value scales multiplied in there, in bf16, by two warps, these held the
 // loop up: 947 us for the 4,096-token chunks (641 without the conversion).
 //
-// Bound by the chain softmax, P V, next scores: the tensor pipe is busy 55 % of the
+// Bound by the chain softmax, P V, next scores: the tensor pipe is busy 54 % of the
 // time, and a softmax warp waits longer for its scores than it works on them.  The
-// second part of Q is a tenth of the time (603 us without it, 675 with), the
-// conversion 4 % (646).
+// second part of Q is a tenth of the time (603 us without it, 675 with, when that
+// was measured), the conversion 4 % (646).
 // Measured: two sequences, 4,096 new of 8,192 tokens, 32 heads on 8, d = 128:
-// 667 us, 1.24 PFLOP/s (the bf16 cache: 570); six chunks of 90 to 444 tokens over
-// 900 to 7,800 keys, 40 heads on 8: 165 us (147); 16 new tokens each over 30 K
-// keys, four sequences: 90 us (101).
+// 675 us, 1.22 PFLOP/s (the bf16 cache: 571); six chunks of 90 to 444 tokens over
+// 900 to 7,800 keys, 40 heads on 8: 166 us (146); 16 new tokens each over 30 K
+// keys, four sequences: 90 us (101).  The same work in another order of the code
+// has taken from 667 to 679 us: the roles share one instruction cache.
 #include <math.h>
 #include <stdint.h>
 
@@ -751,7 +752,8 @@ cudaError_t launch_sdpa_paged_rows_e4m3(const PagedSdpaArgs& a, const DeviceCtl&
   // Two query tiles per CTA share the key tiles and the converted value tiles,
   // and keep the tensor core busy during one tile's softmax: taken when a
   // sequence can have two tiles of new tokens.  One tile: two CTAs per SM, with
-  // 64-key tiles, whose scores fit the registers.
+  // 64-key tiles, whose scores fit 128 registers (at d = 128 but for 136 bytes of
+  // spills; two tiles over pages of 16 rows spill 36).
   if (a.max_new > kBlockM / a.G)
     return a.pages.d == 64 ? launch_two<64>(a, ctl) : launch_two<128>(a, ctl);
   return a.pages.d == 64 ? launch_as<64, 1, 4, 4, 64, 2, 16>(a, ctl)
